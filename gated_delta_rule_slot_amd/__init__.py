@@ -8,6 +8,11 @@ The entry points mirror include/gdn_slot.h one to one:
   gdn_verify_tree, gdn_accept_scatter, replayssm_ring_bytes, replayssm_verify,
   replayssm_commit
 
+those of include/gdn_kv.h (the full-attention layers' paged cache beside the state pool)
+
+  kv_pool_bytes, kv_pool_create, kv_append, attn_workspace_bytes, attn_decode_paged,
+  kv_evict_plan, kv_evict_apply, block_norm
+
 and the host checkpoint index of include/gdn_ckpt.h (CheckpointIndex,
 ckpt_chain_hashes).
 
@@ -24,4 +29,9 @@ from ._binding import (  # noqa: F401
     gdn_accept_scatter, gdn_decode_step, gdn_prefill_workspace_bytes, gdn_verify_tree, last_error,
     replayssm_commit, replayssm_ring_bytes, replayssm_verify, restore_slots, state_pool_bytes,
     state_pool_create, track_snapshot,
+)
+from ._kv import (  # noqa: F401
+    ACT_NONE, ACT_SIGMOID, ACT_SILU, ATTN_ACCUM_MASS, ERRW_BAD_PAGE, GDN_F8_E4M3, KvPool, NORM_PLUS_ONE,
+    attn_decode_paged, attn_workspace_bytes, block_norm, kv_append, kv_evict_apply, kv_evict_plan,
+    kv_pool_bytes, kv_pool_create,
 )

@@ -17,7 +17,7 @@ LIB = os.path.join(HERE, "libgdnslot.so")
 OBJDIR = os.path.join(HERE, "_build")
 
 SOURCES = ["api.hip", "slot_copy.hip", "decode.hip", "prefill.hip", "prefill_fused.hip", "verify.hip",
-           "replay.hip"]
+           "replay.hip", "api_kv.hip", "kv_cache.hip", "attn_decode.hip", "norm.hip"]
 HOST_SOURCES = ["ckpt_index.cpp"]  # host-only C++ (the checkpoint index), built with g++
 CXX = os.environ.get("CXX", "g++")
 HOST_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall", "-Wextra",

@@ -1,0 +1,554 @@
+// attn_decode.hip -- attention of one new token per request over a paged key-value cache
+// (formulas: include/gdn_kv.h), split over the cache's length and joined.
+//
+// Every key and value row is read once and used for the up to 16 query heads that share
+// it: 4 * group flops for every element read, so the reads from memory bound it.  One pass
+// keeps the running maximum m and sum l of the softmax per query head.
+//
+// A wave takes tiles of 32 tokens and needs no shared memory for them.
+//   S^T = K Q^T   A = keys (rows = tokens), B = queries (columns = heads).  A lane gets,
+//                 for head c = lane % 16 and group g = lane / 16, the scores of tokens
+//                 4g + j and 16 + 4g + j (j < 4).
+//   O^T = V^T P^T takes P^T as B with exactly those tokens as the lane's eight k
+//                 indices (both operands use the order, so the sum is unchanged).  For A,
+//                 the lane reads, of its eight tokens, the columns that belong to
+//                 c, and picks one column of all eight by byte permutes.  So the values
+//                 are read in whole rows and transposed in registers.
+// The head is the lane's column in both products: m, l and the rescaling of O are
+// lane-local, and only the maximum crosses lanes.
+//
+// P is carried as two bf16 parts (hi + lo, 16 bits): rounded once to bf16 its error would
+// be about as large as the output's own rounding.  Scores, m, l and O are fp32.
+//
+// Workgroups: x = (split, request, key-value head, block of 16 query heads), 4 waves whose
+// tiles alternate; the waves' results join in shared memory.  With more than one split
+// (or with weights to accumulate) m, l and O of each split go to the workspace, and a
+// second kernel joins them.
+#include <algorithm>
+
+#include "kv.hpp"
+#include "lanes.hpp"
+#include "mfma.hpp"
+
+namespace gdn {
+namespace {
+
+constexpr int kTile = 32;
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.693147180559945309417f;
+constexpr float kNegInf = -__builtin_inff();
+
+struct AttnDev {
+  AttnArgs a;
+  int head_blocks, group, chunk, splits;
+  int part;         // 1: write partial results, 0: final ones
+  int64_t lpad;     // row length of the score array
+  float *o;         // [batch][q_heads][splits][D]
+  float *ml;        // [batch][q_heads][splits][2]
+  float *scores;    // [batch][q_heads][lpad], log2 units; NULL without weights
+};
+
+// the visible range of request b; false if there is none (with the reason told once)
+__device__ __forceinline__ bool visible(const KvGeom &g, const AttnArgs &a, int b, bool teller, int *slot,
+                                        int *begin, int *len) {
+  *slot = a.slot_table[b];
+  *len = a.kv_len[b];
+  *begin = a.kv_begin ? a.kv_begin[b] : 0;
+  if (*slot <= 0 || *slot >= g.slots) {
+    if (teller && *slot >= g.slots) set_err(g.err, GDN_ERRW_BAD_SLOT);
+    return false;
+  }
+  if (*len < 0 || *len > a.max_len || *begin < 0) {
+    if (teller) set_err(g.err, GDN_ERRW_BAD_SEQLENS);
+    return false;
+  }
+  return *begin < *len;
+}
+
+// splits that hold tokens: split s has tiles from begin / 32 + s * chunk / 32 on
+__device__ __forceinline__ int active_splits(int begin, int len, int chunk) {
+  const int seen = len - (begin & ~(kTile - 1));
+  return (seen + chunk - 1) / chunk;
+}
+
+// max / sum over the four 16-lane groups (same head), left in every lane
+__device__ __forceinline__ float rows_max(float v) {
+  auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float rows_sum(float v) {
+  auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+// Exponent's reference: a maximum of -inf (nothing seen yet) must not meet -inf - -inf.
+__device__ __forceinline__ float ref(float m) { return m == kNegInf ? 0.f : m; }
+// What a sum taken under the maximum m is worth under the larger maximum to.
+__device__ __forceinline__ float factor(float m, float to) { return m == kNegInf ? 0.f : fexp2(m - to); }
+
+// Element types.  kWords: 32-bit words of one lane's piece of a row.
+//   K: piece s of a row (4 lanes of different g side by side): the k indices of kSteps
+//      MFMA steps.  V: the D / 16 columns of a lane, as bf16 words after conversion.
+typedef uint32_t u32;
+template <int D, bool kF8>
+struct Lay;
+template <int D>
+struct Lay<D, false> {
+  static constexpr int kSize = 2;
+  static constexpr int kPieces = D / 32;       // 16-byte pieces of a key row per lane
+  static constexpr int kVPieces = D == 256 ? 2 : 1;
+  static constexpr int kVWords = D == 64 ? 2 : 4;  // words of one value piece
+  // first dimension of step s for lane group g, and of a lane's value column i
+  static __device__ __forceinline__ int kdim(int s, int g) { return 32 * s + 8 * g; }
+  static __device__ __forceinline__ int vdim(int i, int c) {
+    return D == 64 ? 4 * c + i : 128 * (i >> 3) + 8 * c + (i & 7);
+  }
+};
+template <int D>
+struct Lay<D, true> {
+  static constexpr int kSize = 1;
+  static constexpr int kPieces = D / 64;
+  static constexpr int kVPieces = 1;
+  static constexpr int kVWords = D / 64;
+  static __device__ __forceinline__ int kdim(int s, int g) { return 64 * (s >> 1) + 16 * g + 8 * (s & 1); }
+  static __device__ __forceinline__ int vdim(int i, int c) { return (D / 16) * c + i; }
+};
+
+template <int W>
+struct Words {
+  u32 w[W];
+};
+template <int W>
+__device__ __forceinline__ Words<W> load_words(const char *p) {
+  Words<W> r;
+  if constexpr (W == 4) {
+    const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p));
+    r.w[0] = v[0]; r.w[1] = v[1]; r.w[2] = v[2]; r.w[3] = v[3];
+  } else if constexpr (W == 2) {
+    const u32x2 v = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(p));
+    r.w[0] = v[0]; r.w[1] = v[1];
+  } else {
+    r.w[0] = __builtin_nontemporal_load(reinterpret_cast<const u32 *>(p));
+  }
+  return r;
+}
+// four e4m3 values as two words of bf16 pairs (exact)
+__device__ __forceinline__ void f8_to_bf16(u32 x, u32 *lo, u32 *hi) {
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  const f2 a = __builtin_amdgcn_cvt_pk_f32_fp8(int(x), false);
+  const f2 b = __builtin_amdgcn_cvt_pk_f32_fp8(int(x), true);
+  // an e4m3 value has 4 significant bits, so its fp32 form's low half is zero
+  *lo = __builtin_amdgcn_perm(__float_as_uint(a[1]), __float_as_uint(a[0]), 0x07060302u);
+  *hi = __builtin_amdgcn_perm(__float_as_uint(b[1]), __float_as_uint(b[0]), 0x07060302u);
+}
+
+template <int D, bool kF8>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2)))
+void attn_decode_kernel(KvGeom g, AttnDev p) {
+  using L = Lay<D, kF8>;
+  constexpr int KS = D / 32;        // MFMA steps of a score
+  constexpr int NO = D / 16;        // 16-column tiles of O
+  constexpr int VW = D / 32;        // bf16 words of a lane's columns of one token
+  extern __shared__ __attribute__((aligned(16))) float lds[];
+  __shared__ float sm[kWaves][16], sl[kWaves][16];
+
+  const int lane = threadIdx.x & 63, c = lane & 15, gr = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int split = blockIdx.x % p.splits, unit = blockIdx.x / p.splits;
+  const int hb = unit % p.head_blocks, bh = unit / p.head_blocks;
+  const int h = bh % g.kv_heads, b = bh / g.kv_heads;
+  const int heads = min(16, p.group - 16 * hb);           // query heads of this block
+  const int q0 = h * p.group + 16 * hb;                   // the first of them
+  int slot, begin, len;
+  const bool any = visible(g, p.a, b, split == 0 && hb == 0 && h == 0 && threadIdx.x == 0, &slot, &begin, &len);
+  const int64_t qrow = int64_t(b) * p.a.q_heads + q0;
+  if (!any) {
+    if (!p.part) {
+      for (int i = threadIdx.x; i < heads * D / 2; i += kThreads)
+        reinterpret_cast<u32 *>(p.a.out + qrow * D)[i] = 0;
+      if (p.a.lse && int(threadIdx.x) < heads) p.a.lse[qrow + threadIdx.x] = kNegInf;
+    }
+    return;  // the joining kernel sees the same range
+  }
+  if (split >= active_splits(begin, len, p.chunk)) return;
+  const int first = (begin & ~(kTile - 1)) + split * p.chunk;
+  const int last = min(len, first + p.chunk);
+
+  // queries as the B operand (columns past the group are zero)
+  bf16x8 qf[KS];
+  {
+    const uint16_t *q = p.a.q + int64_t(b) * p.a.q_stride + int64_t(q0 + min(c, heads - 1)) * D;
+#pragma unroll
+    for (int s = 0; s < KS; ++s) {
+      u32x4 w = *reinterpret_cast<const u32x4 *>(q + L::kdim(s, gr));
+      if (c >= heads) w = u32x4{0, 0, 0, 0};
+      qf[s] = __builtin_bit_cast(bf16x8, w);
+    }
+  }
+  const float to_log2 = p.a.scale * g.k_scale * kLog2e;
+  const int32_t *table = g.page_table + int64_t(slot) * g.max_pages;
+  const int in_page = (1 << g.page_shift) - 1;
+
+  f32x4 o[NO];
+#pragma unroll
+  for (int i = 0; i < NO; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  float m = kNegInf, l = 0.f;
+
+  // rows of the tile at t0: lane i < 32 looks up token t0 + i.  A token that is not
+  // visible or has no page reads page 0's first row (always there) and is masked.
+  auto lookup = [&](int t0, int *row, u32 *seen) {
+    const int t = t0 + (lane & 31);
+    int r = 0;
+    bool ok = false;
+    if (t >= begin && t < last) {
+      const int page = table[t >> g.page_shift];
+      ok = page > 0 && page < g.pages;
+      if (ok) r = ((page * g.kv_heads + h) << g.page_shift) + (t & in_page);
+      else set_err(g.err, GDN_ERRW_BAD_PAGE);
+    }
+    *row = r;
+    *seen = u32(__ballot(ok));  // lanes 32 up repeat the lower ones
+  };
+
+  Words<4> kw[2][L::kPieces];
+  Words<L::kVWords> vw[8][L::kVPieces];
+  auto load_k = [&](int row) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int r = __shfl(row, 16 * u + c);
+      const char *at = g.k + int64_t(r) * (D * L::kSize) + 16 * gr;
+#pragma unroll
+      for (int s = 0; s < L::kPieces; ++s) kw[u][s] = load_words<4>(at + 64 * s);
+    }
+  };
+  auto load_v = [&](int row) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int r = __shfl(row, pk(gr, e));
+      const char *at = g.v + int64_t(r) * (D * L::kSize) + 4 * L::kVWords * c;
+#pragma unroll
+      for (int s = 0; s < L::kVPieces; ++s) vw[e][s] = load_words<L::kVWords>(at + 256 * s);
+    }
+  };
+
+  constexpr int kStep = kTile * kWaves;
+  int t0 = first + kTile * wave;
+  int row, row_next = 0;
+  u32 seen, seen_next = 0;
+  if (t0 < last) {
+    lookup(t0, &row, &seen);
+    load_k(row);
+    load_v(row);
+  }
+  for (; t0 < last; t0 += kStep) {
+    const int t1 = t0 + kStep;
+    const bool more = t1 < last;
+    if (more) lookup(t1, &row_next, &seen_next);
+
+    // ---- scores ----------------------------------------------------------
+    f32x4 s[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      s[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int st = 0; st < KS; ++st) {
+        u32x4 w;
+        if constexpr (kF8) {
+          const u32 x0 = kw[u][st >> 1].w[2 * (st & 1)], x1 = kw[u][st >> 1].w[2 * (st & 1) + 1];
+          u32 a0, a1, a2, a3;
+          f8_to_bf16(x0, &a0, &a1);
+          f8_to_bf16(x1, &a2, &a3);
+          w = u32x4{a0, a1, a2, a3};
+        } else {
+          w = u32x4{kw[u][st].w[0], kw[u][st].w[1], kw[u][st].w[2], kw[u][st].w[3]};
+        }
+        s[u] = mfma_bf16(__builtin_bit_cast(bf16x8, w), qf[st], s[u]);
+      }
+    }
+    if (more) load_k(row_next);
+
+    // ---- softmax ---------------------------------------------------------
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = s[e >> 2][e & 3] * to_log2;
+    const bool whole = seen == 0xffffffffu;
+    if (!whole) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = (seen >> pk(gr, e)) & 1 ? x[e] : kNegInf;
+    }
+    if (p.scores && c < heads) {
+      float *at = p.scores + (qrow + c) * p.lpad + t0 + 4 * gr;
+      st4(at, f32x4{x[0], x[1], x[2], x[3]});
+      st4(at + 16, f32x4{x[4], x[5], x[6], x[7]});
+    }
+    float mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+    mx = fmaxf(rows_max(mx), m);
+    if (__any(mx > m)) {  // some head's maximum grew
+      const float f = factor(m, mx);
+      l *= f;
+#pragma unroll
+      for (int i = 0; i < NO; ++i) o[i] *= f;
+      m = mx;
+    }
+    float pr[8];
+    const float base = ref(m);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      pr[e] = fexp2(x[e] - base);
+      l += pr[e];
+    }
+    const Split ps = split8(pr);
+
+    // ---- values: columns of eight tokens by byte permutes --------------------
+#pragma unroll
+    for (int w = 0; w < VW; ++w) {
+      u32 word[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if constexpr (kF8) {
+          u32 lo, hi;
+          f8_to_bf16(vw[e][0].w[w >> 1], &lo, &hi);
+          word[e] = (w & 1) ? hi : lo;
+        } else {
+          word[e] = vw[e][w / L::kVWords].w[w % L::kVWords];
+        }
+        if (!whole) word[e] = (seen >> pk(gr, e)) & 1 ? word[e] : 0u;  // never 0 * inf
+      }
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const u32x4 col = {halves(word[0], word[1], hf), halves(word[2], word[3], hf),
+                           halves(word[4], word[5], hf), halves(word[6], word[7], hf)};
+        const bf16x8 av = __builtin_bit_cast(bf16x8, col);
+        o[2 * w + hf] = mfma_bf16(av, ps.lo, o[2 * w + hf]);
+        o[2 * w + hf] = mfma_bf16(av, ps.hi, o[2 * w + hf]);
+      }
+    }
+    if (more) load_v(row_next);
+    row = row_next;
+    seen = seen_next;
+  }
+
+  // ---- join the waves: o[i][j] is column vdim(i, 4 gr + j) of head c ---------
+  // Two slabs of shared memory: waves 2 and 3 store, waves 0 and 1 add.  Four i make 16
+  // adjacent bytes; rows are padded by 16 bytes, so eight lanes cover all banks.
+  constexpr int DS = D + 4;
+  l = rows_sum(l);
+  if (gr == 0) {
+    sm[wave][c] = m;
+    sl[wave][c] = l;
+  }
+  __syncthreads();
+  float mt = sm[0][c];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) mt = fmaxf(mt, sm[w][c]);
+  const float f = factor(m, mt);
+  float *slab = lds + ((wave & 1) * heads + c) * DS;
+#pragma unroll
+  for (int pass = 0; pass < 2; ++pass) {
+    if ((wave >> 1) != pass && c < heads) {
+#pragma unroll
+      for (int q = 0; q < NO / 4; ++q)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float *at = slab + L::vdim(4 * q, 4 * gr + j);
+          f32x4 x = {o[4 * q][j], o[4 * q + 1][j], o[4 * q + 2][j], o[4 * q + 3][j]};
+          x *= f;
+          if (pass) x += ld4(at);
+          st4(at, x);
+        }
+    }
+    __syncthreads();
+  }
+  for (int i = threadIdx.x; i < heads * (D / 4); i += kThreads) {
+    const int hd = i / (D / 4), d = 4 * (i % (D / 4));
+    float mh = sm[0][hd], lt = 0.f;
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) mh = fmaxf(mh, sm[w][hd]);
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) lt = fmaf(sl[w][hd], factor(sm[w][hd], mh), lt);
+    f32x4 sum = ld4(lds + hd * DS + d) + ld4(lds + (heads + hd) * DS + d);
+    if (p.part) {
+      const int64_t r = (qrow + hd) * p.splits + split;
+      st4(p.o + r * D + d, sum);
+      if (d == 0) {
+        p.ml[2 * r] = mh;
+        p.ml[2 * r + 1] = lt;
+      }
+    } else {
+      sum *= lt == 0.f ? 0.f : g.v_scale / lt;
+      *reinterpret_cast<u32x2 *>(p.a.out + (qrow + hd) * D + d) =
+          u32x2{cvt_pk_bf16(sum[0], sum[1]), cvt_pk_bf16(sum[2], sum[3])};
+      if (p.a.lse && d == 0) p.a.lse[qrow + hd] = lt == 0.f ? kNegInf : (mh + log2f(lt)) * kLn2;
+    }
+  }
+}
+
+// Joins the splits of each (request, query head), and adds the weights
+//   mass[t] += sum over the group's heads of 2^(score - m) / l.
+// Workgroups: first one per (request, query head), then, with weights, one per
+// kMassTokens tokens of each (request, key-value head).
+constexpr int kMassTokens = 1024;
+
+template <int D>
+__global__ __launch_bounds__(kThreads) void attn_join_kernel(KvGeom g, AttnDev p, int mass_blocks) {
+  __shared__ __attribute__((aligned(16))) float acc[kWaves][D];
+  __shared__ float sm[kWaves], sl[kWaves];
+  __shared__ float hm[64], hl[64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int joins = p.a.batch * p.a.q_heads;
+  int slot, begin, len;
+  if (int(blockIdx.x) < joins) {
+    const int64_t qr = blockIdx.x;
+    const int b = int(qr / p.a.q_heads);
+    const bool any = visible(g, p.a, b, false, &slot, &begin, &len);
+    const int ns = any ? active_splits(begin, len, p.chunk) : 0;
+    const float *ml = p.ml + 2 * qr * p.splits;
+    // maximum and sum over the splits, every wave for itself
+    float m = kNegInf, l = 0.f;
+    for (int s = lane; s < ns; s += 64) m = fmaxf(m, ml[2 * s]);
+    for (int x = 32; x; x >>= 1) m = fmaxf(m, __shfl_xor(m, x));
+    for (int s = lane; s < ns; s += 64) l += ml[2 * s + 1] * factor(ml[2 * s], m);
+    l = wave_sum(l);
+    constexpr int C = D / 64;  // columns of a lane
+    float sum[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) sum[i] = 0.f;
+    const float *o = p.o + qr * p.splits * D + C * lane;
+#pragma unroll 4
+    for (int s = wave; s < ns; s += kWaves) {
+      const float f = factor(ml[2 * s], m);
+#pragma unroll
+      for (int i = 0; i < C; ++i) sum[i] = fmaf(f, o[int64_t(s) * D + i], sum[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < C; ++i) acc[wave][C * lane + i] = sum[i];
+    __syncthreads();
+    const float inv = l == 0.f ? 0.f : g.v_scale / l;
+    for (int i = threadIdx.x; i < D; i += kThreads) {
+      float t = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) t += acc[w][i];
+      p.a.out[qr * D + i] = f32_to_bf16(t * inv);
+    }
+    if (p.a.lse && threadIdx.x == 0) p.a.lse[qr] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
+    return;
+  }
+  const int64_t id = int64_t(blockIdx.x) - joins;
+  const int block = int(id % mass_blocks), bh = int(id / mass_blocks);
+  const int h = bh % g.kv_heads, b = bh / g.kv_heads;
+  if (!visible(g, p.a, b, false, &slot, &begin, &len)) return;
+  const int64_t from = int64_t(begin & ~3) + int64_t(block) * kMassTokens;
+  if (from >= len) return;
+  const int ns = active_splits(begin, len, p.chunk);
+  const int64_t qr0 = int64_t(b) * p.a.q_heads + h * p.group;
+  for (int hd = wave; hd < p.group; hd += kWaves) {
+    const float *ml = p.ml + 2 * (qr0 + hd) * p.splits;
+    float m = kNegInf, l = 0.f;
+    for (int s = lane; s < ns; s += 64) m = fmaxf(m, ml[2 * s]);
+    for (int x = 32; x; x >>= 1) m = fmaxf(m, __shfl_xor(m, x));
+    for (int s = lane; s < ns; s += 64) l += ml[2 * s + 1] * factor(ml[2 * s], m);
+    l = wave_sum(l);
+    if (lane == 0) {
+      hm[hd] = ref(m);
+      hl[hd] = l == 0.f ? 0.f : 1.f / l;
+    }
+  }
+  __syncthreads();
+  const int64_t t = from + 4 * threadIdx.x;
+  if (t >= len) return;
+  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+  const float *sc = p.scores + qr0 * p.lpad + t;
+#pragma unroll 4
+  for (int hd = 0; hd < p.group; ++hd) {
+    const f32x4 x = ld4(sc + hd * p.lpad);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sum[j] = fmaf(fexp2(x[j] - hm[hd]), hl[hd], sum[j]);
+  }
+  float *mass = g.mass + (int64_t(slot) * g.kv_heads + h) * g.capacity + t;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (t + j >= begin && t + j < len) mass[j] += sum[j];
+}
+
+size_t pad256(size_t n) { return (n + 255) & ~size_t(255); }
+int64_t score_row(int max_len) { return (int64_t(max_len) + kTile - 1) / kTile * kTile; }
+
+template <int D, bool kF8>
+hipError_t launch_dt(const KvGeom &g, const AttnDev &p, int64_t blocks, hipStream_t s) {
+  const size_t lds = size_t(2) * std::min(16, p.group) * (D + 4) * 4;
+  hipLaunchKernelGGL((attn_decode_kernel<D, kF8>), dim3(unsigned(blocks)), dim3(kThreads), lds, s, g, p);
+  return hipGetLastError();
+}
+
+template <int D>
+hipError_t launch_d(const KvGeom &g, const AttnDev &p, bool f8, int64_t blocks, hipStream_t s) {
+  hipError_t e = f8 ? launch_dt<D, true>(g, p, blocks, s) : launch_dt<D, false>(g, p, blocks, s);
+  if (e != hipSuccess || !p.part) return e;
+  const int mass_blocks = p.scores ? (p.a.max_len + 3 + kMassTokens - 1) / kMassTokens : 0;
+  const int64_t joins = int64_t(p.a.batch) * p.a.q_heads + int64_t(p.a.batch) * g.kv_heads * mass_blocks;
+  if (joins >= (int64_t(1) << 31)) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((attn_join_kernel<D>), dim3(unsigned(joins)), dim3(kThreads), 0, s, g, p, mass_blocks);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+AttnSplit attn_split(const gdn_kv_pool *p, int batch, int q_heads, int max_len) {
+  AttnSplit r;
+  const int group = q_heads / p->d.kv_heads;
+  r.head_blocks = (group + 15) / 16;
+  const int64_t units = std::max<int64_t>(1, int64_t(batch) * p->d.kv_heads * r.head_blocks);
+  const int64_t want = std::max<int64_t>(1, 1024 / units);
+  const int step = kTile * kWaves;
+  const int64_t chunk = std::max<int64_t>(1, (max_len + want - 1) / want);
+  r.chunk = int((chunk + step - 1) / step * step);
+  r.splits = std::max(1, int((int64_t(max_len) + r.chunk - 1) / r.chunk));
+  return r;
+}
+
+size_t attn_workspace(const gdn_kv_pool *p, int batch, int q_heads, int max_len, uint32_t flags) {
+  const AttnSplit sp = attn_split(p, batch, q_heads, max_len);
+  if (sp.splits == 1 && !(flags & GDN_F_ACCUM_MASS)) return 0;
+  const size_t rows = size_t(batch) * q_heads;
+  size_t n = pad256(rows * sp.splits * p->d.head_dim * 4) + pad256(rows * sp.splits * 8);
+  if (flags & GDN_F_ACCUM_MASS) n += rows * size_t(score_row(max_len)) * 4;
+  return n;
+}
+
+hipError_t launch_attn_decode(const gdn_kv_pool *pool, int layer, const AttnArgs &a, hipStream_t s) {
+  const AttnSplit sp = attn_split(pool, a.batch, a.q_heads, a.max_len);
+  const KvGeom g = kv_geom(pool, layer);
+  const int64_t blocks = int64_t(a.batch) * pool->d.kv_heads * sp.head_blocks * sp.splits;
+  if (blocks >= (int64_t(1) << 31)) return hipErrorInvalidValue;
+  AttnDev p{};
+  p.a = a;
+  p.head_blocks = sp.head_blocks;
+  p.group = a.q_heads / pool->d.kv_heads;
+  p.chunk = sp.chunk;
+  p.splits = sp.splits;
+  p.part = sp.splits > 1 || (a.flags & GDN_F_ACCUM_MASS);
+  p.lpad = score_row(a.max_len);
+  if (p.part) {
+    const size_t rows = size_t(a.batch) * a.q_heads;
+    char *ws = static_cast<char *>(a.workspace);
+    p.o = reinterpret_cast<float *>(ws);
+    ws += pad256(rows * sp.splits * pool->d.head_dim * 4);
+    p.ml = reinterpret_cast<float *>(ws);
+    ws += pad256(rows * sp.splits * 8);
+    if (a.flags & GDN_F_ACCUM_MASS) p.scores = reinterpret_cast<float *>(ws);
+  }
+  const bool f8 = pool->d.kv_dtype == GDN_F8_E4M3;
+  switch (pool->d.head_dim) {
+    case 64: return launch_d<64>(g, p, f8, blocks, s);
+    case 128: return launch_d<128>(g, p, f8, blocks, s);
+    case 256: return launch_d<256>(g, p, f8, blocks, s);
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace gdn

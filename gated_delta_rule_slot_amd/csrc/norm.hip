@@ -1,0 +1,191 @@
+// norm.hip -- block_norm: the norm after a block, its gate, the residual scale and sum,
+// and the norm before the next block, in one pass over each row (formulas:
+// include/gdn_kv.h).
+//
+// Every tensor is read or written once, so the call is bound by its bytes; a row stays in
+// registers between the two reductions.  A row is spread over LANES threads, 8
+// consecutive values (16 bytes of bf16) each, VPT such pieces a thread.
+#include "kv.hpp"
+#include "lanes.hpp"
+
+namespace gdn {
+namespace {
+
+constexpr int kNormThreads = 256;
+
+__device__ __forceinline__ void widen8(const u32x4 &r, float *f) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(r[i] << 16);
+    f[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ u32x4 narrow8(const float *f) {
+  u32x4 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+  return r;
+}
+// 8 values at element offset `at` of a bf16 or fp32 array
+__device__ __forceinline__ void load8(const void *p, int64_t at, bool f32, float *f) {
+  if (f32) {
+    const u32x4 *q = reinterpret_cast<const u32x4 *>(static_cast<const float *>(p) + at);
+    const u32x4 lo = q[0], hi = q[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[i] = __uint_as_float(lo[i]);
+      f[4 + i] = __uint_as_float(hi[i]);
+    }
+  } else {
+    widen8(*reinterpret_cast<const u32x4 *>(static_cast<const uint16_t *>(p) + at), f);
+  }
+}
+
+// Sum over a row's LANES threads, the same bits in each of them.
+template <int LANES>
+__device__ __forceinline__ float row_sum(float v, float *red) {
+  if constexpr (LANES <= 64) {
+    return group_sum<LANES>(v);
+  } else {
+    v = wave_sum(v);
+    __syncthreads();  // the previous use of `red` is over
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < LANES / 64; ++i) t += red[i];
+    return t;
+  }
+}
+
+template <int LANES, int VPT>
+__global__ __launch_bounds__((LANES > kNormThreads ? LANES : kNormThreads)) void block_norm_kernel(
+    NormArgs a, int64_t rows) {
+  constexpr int THREADS = LANES > kNormThreads ? LANES : kNormThreads;
+  __shared__ float red[LANES > 64 ? LANES / 64 : 1];
+  const int64_t row = int64_t(blockIdx.x) * (THREADS / LANES) + threadIdx.x / LANES;
+  const bool live = row < rows;  // uniform over a row's threads
+  const int l = threadIdx.x % LANES;
+  const int64_t r0 = live ? row : 0;
+  const int64_t token = r0 / a.groups;
+  const int64_t in_token = (r0 - token * a.groups) * a.dim;
+  const uint16_t *y = a.y + token * a.y_stride + in_token;
+  const uint16_t *gate = a.gate ? a.gate + token * a.gate_stride + in_token : nullptr;
+  const int64_t flat = r0 * a.dim;
+  const bool wf32 = a.w_dtype == GDN_F32, rf32 = a.res_dtype == GDN_F32;
+  const float one = (a.flags & GDN_F_NORM_PLUS_ONE) ? 1.f : 0.f;
+  const float inv_dim = 1.f / float(a.dim);
+
+  // all loads of the row are issued before anything waits
+  u32x4 yr[VPT], gr[VPT];
+  float u[VPT][8], res[VPT][8];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int d = 8 * (l + i * LANES);
+    const bool on = live && d < a.dim;
+    yr[i] = gr[i] = u32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) res[i][e] = 0.f;
+    if (on) {
+      yr[i] = *reinterpret_cast<const u32x4 *>(y + d);
+      if (gate) gr[i] = *reinterpret_cast<const u32x4 *>(gate + d);
+      if (a.residual) load8(a.residual, flat + d, rf32, res[i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) widen8(yr[i], u[i]);
+
+  float inv = 1.f;
+  if (a.w_post) {
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fmaf(u[i][e], u[i][e], ss);
+    inv = 1.f / sqrtf(fmaf(row_sum<LANES>(ss, red), inv_dim, a.eps));
+  }
+  float s2 = 0.f;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int d = 8 * (l + i * LANES);
+    const bool on = live && d < a.dim;
+    if (on) {
+      if (a.w_post) {
+        float w[8];
+        load8(a.w_post, d, wf32, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) u[i][e] = u[i][e] * inv * (one + w[e]);
+      }
+      if (gate) {
+        float z[8];
+        widen8(gr[i], z);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float sg = 1.f / (1.f + __expf(-z[e]));
+          u[i][e] *= a.act == GDN_ACT_NONE ? z[e] : a.act == GDN_ACT_SILU ? z[e] * sg : sg;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        u[i][e] = a.residual ? fmaf(a.scale, u[i][e], res[i][e]) : a.scale * u[i][e];
+        s2 = fmaf(u[i][e], u[i][e], s2);
+      }
+      if (a.residual) {
+        if (rf32) {
+          u32x4 lo, hi;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            lo[e] = __float_as_uint(u[i][e]);
+            hi[e] = __float_as_uint(u[i][4 + e]);
+          }
+          u32x4 *q = reinterpret_cast<u32x4 *>(static_cast<float *>(a.residual_out) + flat + d);
+          q[0] = lo;
+          q[1] = hi;
+        } else {
+          *reinterpret_cast<u32x4 *>(static_cast<uint16_t *>(a.residual_out) + flat + d) = narrow8(u[i]);
+        }
+      }
+    }
+  }
+  float inv2 = 1.f;
+  if (a.w_pre) inv2 = 1.f / sqrtf(fmaf(row_sum<LANES>(s2, red), inv_dim, a.eps));
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int d = 8 * (l + i * LANES);
+    if (live && d < a.dim) {
+      if (a.w_pre) {
+        float w[8];
+        load8(a.w_pre, d, wf32, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) u[i][e] = u[i][e] * inv2 * (one + w[e]);
+      }
+      *reinterpret_cast<u32x4 *>(a.out + flat + d) = narrow8(u[i]);
+    }
+  }
+}
+
+template <int LANES, int VPT>
+hipError_t launch_rows(const NormArgs &a, hipStream_t s) {
+  constexpr int THREADS = LANES > kNormThreads ? LANES : kNormThreads;
+  const int64_t rows = a.tokens * a.groups, per = THREADS / LANES;
+  hipLaunchKernelGGL((block_norm_kernel<LANES, VPT>), dim3(unsigned((rows + per - 1) / per)),
+                     dim3(THREADS), 0, s, a, rows);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_block_norm(const NormArgs &a, hipStream_t s) {
+  const int vecs = a.dim / 8;
+  if (vecs <= 8) return launch_rows<8, 1>(a, s);
+  if (vecs <= 16) return launch_rows<16, 1>(a, s);
+  if (vecs <= 32) return launch_rows<32, 1>(a, s);
+  if (vecs <= 64) return launch_rows<64, 1>(a, s);
+  if (vecs <= 256) return launch_rows<256, 1>(a, s);
+  if (vecs <= 512) return launch_rows<256, 2>(a, s);
+  if (vecs <= 1024) return launch_rows<256, 4>(a, s);
+  if (vecs <= 2048) return launch_rows<512, 4>(a, s);
+  return launch_rows<1024, 4>(a, s);
+}
+
+}  // namespace gdn

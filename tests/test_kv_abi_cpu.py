@@ -1,0 +1,163 @@
+"""Host-side checks of include/gdn_kv.h that need no GPU: sizes, and every refusal before a
+launch (pointers are made-up numbers that nothing reads)."""
+import ctypes as ct
+
+import pytest
+import torch
+
+import gated_delta_rule_slot_amd as gdn
+from gated_delta_rule_slot_amd import _binding as B
+from gated_delta_rule_slot_amd import _kv as K
+
+P = 0x100000  # a 256-byte aligned made-up address
+
+
+def desc(**kw):
+    d = dict(layers=2, pages=9, kv_heads=2, page_size=16, head_dim=64, slots=4, max_pages=5,
+             kv_dtype=B.GDN_BF16, k_scale=1.0, v_scale=1.0, k_base=P, v_base=P, page_table=P, mass=P, pos=P,
+             err_word=None)
+    d.update(kw)
+    return K.KvDesc(*[d[f] for f, _ in K.KvDesc._fields_])
+
+
+def make(**kw):
+    h = ct.c_void_p()
+    return B._lib.kv_pool_create(ct.byref(desc(**kw)), ct.byref(h)), h
+
+
+@pytest.fixture
+def pool():
+    st, h = make()
+    assert st == 0, B.last_error()
+    yield h
+    B._lib.kv_pool_destroy(h)
+
+
+def test_sizes():
+    assert gdn.kv_pool_bytes(2, 9, 2, 16, 64, 4, 5, B.GDN_BF16) == (2 * 9 * 2 * 16 * 64 * 2, 2 * 4 * 2 * 80)
+    assert gdn.kv_pool_bytes(2, 9, 2, 16, 64, 4, 5, gdn.GDN_F8_E4M3)[0] == 2 * 9 * 2 * 16 * 64
+    # past 32 bits
+    assert gdn.kv_pool_bytes(8, 100000, 8, 64, 256, 4, 5, B.GDN_BF16)[0] == 8 * 100000 * 8 * 64 * 256 * 2
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(), 0), (dict(kv_dtype=gdn.GDN_F8_E4M3, k_scale=0.5, v_scale=3.0), 0), (dict(mass=None, pos=None), 0),
+    (dict(page_size=1), 0), (dict(page_size=1024), 0),
+    (dict(layers=0), -1), (dict(kv_heads=0), -1), (dict(max_pages=0), -1), (dict(pages=1), -1),
+    (dict(slots=1), -1), (dict(kv_dtype=B.GDN_F32), -1), (dict(kv_dtype=7), -1),
+    (dict(head_dim=32), -3), (dict(head_dim=96), -3), (dict(page_size=24), -3), (dict(page_size=2048), -3),
+    (dict(page_size=0), -3), (dict(max_pages=1 << 27), -3), (dict(pages=1 << 26), -3),
+    (dict(pages=1 << 30, kv_heads=4), -3), (dict(kv_heads=70000), -3),
+    (dict(k_base=None), -1), (dict(v_base=None), -1), (dict(page_table=None), -1),
+    (dict(k_base=P + 8), -3), (dict(page_table=P + 2), -1), (dict(mass=P + 1), -1), (dict(err_word=P + 2), -1),
+    (dict(k_scale=2.0), -1), (dict(kv_dtype=2, k_scale=0.0), -1), (dict(kv_dtype=2, v_scale=-1.0), -1),
+    (dict(kv_dtype=2, v_scale=float("inf")), -1), (dict(kv_dtype=2, k_scale=float("nan")), -1),
+])
+def test_pool_create_validation(kw, status):
+    st, h = make(**kw)
+    assert st == status, B.last_error()
+    if st == 0:
+        B._lib.kv_pool_destroy(h)
+    else:
+        assert B.last_error()
+
+
+APPEND = dict(layer=0, n=3, slot_ids=P, index=P, position=P, k=P, ks=128, v=P, vs=128, stream=None)
+ATTN = dict(layer=0, batch=2, q_heads=4, max_len=80, slot_table=P, kv_len=P, kv_begin=None, q=P, qs=256,
+            scale=1.0, flags=0, out=P, lse=None, ws=P, ws_bytes=1 << 30, stream=None)
+PLAN = dict(lb=0, le=2, batch=2, max_len=80, slot_table=P, kv_len=P, next_pos=P, budget=32, sink=2, recent=8,
+            max_moves=32, n_moves=P, moves=P, out=P + 4096, stream=None)
+APPLY = dict(lb=0, le=2, batch=2, max_moves=32, slot_table=P, n_moves=P, moves=P, stream=None)
+NORM = dict(tokens=4, groups=2, dim=64, y=P, ys=128, w_post=P, gate=P, gs=128, act=1, scale=1.0, res=P, res_out=P,
+            rt=B.GDN_BF16, w_pre=P, wt=B.GDN_F32, eps=1e-6, flags=0, out=P, stream=None)
+
+
+@pytest.mark.parametrize("fn,base,kw,status", [
+    ("kv_append", APPEND, dict(layer=2), -2), ("kv_append", APPEND, dict(layer=-1), -2),
+    ("kv_append", APPEND, dict(layer=2 ** 31 - 1), -2),
+    ("kv_append", APPEND, dict(n=-1), -2), ("kv_append", APPEND, dict(n=0, k=None), 0),
+    ("kv_append", APPEND, dict(slot_ids=None), -1), ("kv_append", APPEND, dict(index=None), -1),
+    ("kv_append", APPEND, dict(position=None), -1), ("kv_append", APPEND, dict(v=None), -1),
+    ("kv_append", APPEND, dict(ks=120), -1), ("kv_append", APPEND, dict(vs=132), -3),
+    ("kv_append", APPEND, dict(k=P + 8), -3),
+    ("attn_decode_paged", ATTN, dict(layer=2), -2), ("attn_decode_paged", ATTN, dict(batch=-1), -2),
+    ("attn_decode_paged", ATTN, dict(batch=65536), -2), ("attn_decode_paged", ATTN, dict(batch=0, q=None), 0),
+    ("attn_decode_paged", ATTN, dict(q_heads=3), -1), ("attn_decode_paged", ATTN, dict(q_heads=0), -1),
+    ("attn_decode_paged", ATTN, dict(q_heads=130, qs=1 << 14), -3),
+    ("attn_decode_paged", ATTN, dict(max_len=81), -2), ("attn_decode_paged", ATTN, dict(max_len=-1), -2),
+    ("attn_decode_paged", ATTN, dict(flags=2), -1), ("attn_decode_paged", ATTN, dict(scale=float("nan")), -1),
+    ("attn_decode_paged", ATTN, dict(slot_table=None), -1), ("attn_decode_paged", ATTN, dict(kv_len=None), -1),
+    ("attn_decode_paged", ATTN, dict(q=None), -1), ("attn_decode_paged", ATTN, dict(out=None), -1),
+    ("attn_decode_paged", ATTN, dict(qs=248), -1), ("attn_decode_paged", ATTN, dict(qs=260), -3),
+    ("attn_decode_paged", ATTN, dict(q=P + 2), -3), ("attn_decode_paged", ATTN, dict(out=P + 8), -3),
+    ("attn_decode_paged", ATTN, dict(flags=1, ws=None), -1),
+    ("attn_decode_paged", ATTN, dict(flags=1, ws_bytes=64), -1),
+    ("attn_decode_paged", ATTN, dict(flags=1, ws=P + 128), -3),
+    ("kv_evict_plan", PLAN, dict(le=3), -2), ("kv_evict_plan", PLAN, dict(lb=1, le=0), -2),
+    ("kv_evict_plan", PLAN, dict(lb=1, le=1, moves=None), 0), ("kv_evict_plan", PLAN, dict(batch=0), 0),
+    ("kv_evict_plan", PLAN, dict(max_len=81), -2), ("kv_evict_plan", PLAN, dict(budget=0), -1),
+    ("kv_evict_plan", PLAN, dict(sink=25), -1), ("kv_evict_plan", PLAN, dict(sink=-1), -1),
+    ("kv_evict_plan", PLAN, dict(recent=-1), -1), ("kv_evict_plan", PLAN, dict(recent=2 ** 31 - 1), -1),
+    ("kv_evict_plan", PLAN, dict(max_moves=31), -1), ("kv_evict_plan", PLAN, dict(moves=None), -1),
+    ("kv_evict_plan", PLAN, dict(next_pos=None), -1), ("kv_evict_plan", PLAN, dict(n_moves=None), -1),
+    ("kv_evict_plan", PLAN, dict(out=None), -1), ("kv_evict_plan", PLAN, dict(out=P + 4), -1),
+    ("kv_evict_apply", APPLY, dict(le=3), -2), ("kv_evict_apply", APPLY, dict(max_moves=-1), -2),
+    ("kv_evict_apply", APPLY, dict(max_moves=81), -2), ("kv_evict_apply", APPLY, dict(max_moves=0, moves=None), 0),
+    ("kv_evict_apply", APPLY, dict(moves=None), -1), ("kv_evict_apply", APPLY, dict(slot_table=None), -1),
+])
+def test_calls_refuse_before_launch(pool, fn, base, kw, status):
+    a = dict(base, **kw)
+    assert getattr(B._lib, fn)(pool, *a.values()) == status, B.last_error()
+    assert bool(B.last_error()) == (status != 0)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(tokens=0, y=None), 0), (dict(tokens=-1), -2), (dict(tokens=1 << 31), -2), (dict(groups=0), -1),
+    (dict(dim=0), -1), (dict(dim=60), -3), (dict(dim=32776, ys=1 << 20, gs=1 << 20), -3), (dict(act=3), -1),
+    (dict(gate=None), -1), (dict(rt=gdn.GDN_F8_E4M3), -1), (dict(wt=5), -1), (dict(flags=2), -1),
+    (dict(eps=0.0), -1), (dict(eps=float("nan")), -1), (dict(scale=float("inf")), -1), (dict(res=None), -1),
+    (dict(res_out=None), -1), (dict(y=None), -1), (dict(out=None), -1), (dict(ys=120), -1), (dict(gs=120), -1),
+    (dict(ys=132), -3), (dict(gs=140), -3), (dict(y=P + 8), -3), (dict(w_post=P + 4), -3), (dict(w_pre=P + 2), -3),
+    (dict(res=P + 8), -3), (dict(res_out=P + 8), -3), (dict(out=P + 8), -3), (dict(gate=P + 8), -3),
+])
+def test_block_norm_refuses_before_launch(kw, status):
+    assert B._lib.block_norm(*dict(NORM, **kw).values()) == status, B.last_error()
+
+
+def test_null_pool_and_missing_mass():
+    st, h = make(mass=None, pos=None)
+    assert st == 0
+    try:
+        for fn, base in (("kv_append", APPEND), ("attn_decode_paged", ATTN), ("kv_evict_plan", PLAN),
+                         ("kv_evict_apply", APPLY)):
+            assert getattr(B._lib, fn)(None, *base.values()) == -1
+        assert B._lib.kv_evict_plan(h, *PLAN.values()) == -1 and "mass" in B.last_error()
+        assert B._lib.attn_decode_paged(h, *dict(ATTN, flags=1).values()) == -1
+        n = ct.c_size_t()
+        assert B._lib.attn_workspace_bytes(h, 2, 4, 80, 1, ct.byref(n)) == -1
+        assert B._lib.attn_workspace_bytes(h, 2, 4, 80, 0, None) == -1
+    finally:
+        B._lib.kv_pool_destroy(h)
+    B._lib.kv_pool_destroy(None)
+
+
+def test_workspace_grows_with_the_weights(pool):
+    n, m = ct.c_size_t(), ct.c_size_t()
+    assert B._lib.attn_workspace_bytes(pool, 2, 4, 80, 0, ct.byref(n)) == 0
+    assert B._lib.attn_workspace_bytes(pool, 2, 4, 80, 1, ct.byref(m)) == 0
+    assert m.value >= n.value + 2 * 4 * 80 * 4
+    assert B._lib.attn_workspace_bytes(pool, 0, 4, 0, 1, ct.byref(n)) == 0
+
+
+def test_binding_refuses_cpu_tensors_and_wrong_shapes():
+    k = torch.zeros(1, 3, 1, 16, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        gdn.kv_pool_create(k, k, torch.zeros(2, 2, dtype=torch.int32))  # not on the GPU
+    with pytest.raises(ValueError):
+        gdn.kv_pool_create(k, k[:, :2], torch.zeros(2, 2, dtype=torch.int32))
+    with pytest.raises(TypeError):
+        gdn.kv_pool_create(k.float(), k.float(), torch.zeros(2, 2, dtype=torch.int32))
+    with pytest.raises(ValueError):
+        gdn.block_norm(torch.zeros(2, 64), None)
+    with pytest.raises(ValueError):
+        gdn.block_norm(torch.zeros(2, 1, 64, dtype=torch.bfloat16), None)
