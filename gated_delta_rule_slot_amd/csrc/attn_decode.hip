@@ -25,6 +25,7 @@
 // (or with weights to accumulate) m, l and O of each split go to the workspace, and a
 // second kernel joins them.
 #include <algorithm>
+#include <type_traits>
 
 #include "kv.hpp"
 #include "lanes.hpp"
@@ -147,15 +148,21 @@ __device__ __forceinline__ void f8_to_bf16(u32 x, u32 *lo, u32 *hi) {
   *hi = __builtin_amdgcn_perm(__float_as_uint(b[1]), __float_as_uint(b[0]), 0x07060302u);
 }
 
-template <int D, bool kF8>
+// kWide: pages hold whole tiles (page_size >= 32), so a tile's rows are adjacent and its
+// one page id is wave-uniform; otherwise each token's row is looked up.
+template <int D, bool kF8, bool kWide, bool kMass>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2)))
 void attn_decode_kernel(KvGeom g, AttnDev p) {
   using L = Lay<D, kF8>;
   constexpr int KS = D / 32;        // MFMA steps of a score
   constexpr int NO = D / 16;        // 16-column tiles of O
   constexpr int VW = D / 32;        // bf16 words of a lane's columns of one token
+  constexpr int RB = D * L::kSize;  // bytes of a row
+  // head dim 256: the queries stay in shared memory (their 32 registers would spill)
+  constexpr bool kQShared = D == 256;
   extern __shared__ __attribute__((aligned(16))) float lds[];
   __shared__ float sm[kWaves][16], sl[kWaves][16];
+  __shared__ u32x4 sq[kQShared ? KS : 1][64];
 
   const int lane = threadIdx.x & 63, c = lane & 15, gr = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -179,84 +186,131 @@ void attn_decode_kernel(KvGeom g, AttnDev p) {
   const int first = (begin & ~(kTile - 1)) + split * p.chunk;
   const int last = min(len, first + p.chunk);
 
-  // queries as the B operand (columns past the group are zero)
-  bf16x8 qf[KS];
+  // (constant address space: the table does not change during the call, so a wave-uniform
+  // read of it is a scalar load, which the waits for keys and values do not count)
+  typedef const int32_t __attribute__((address_space(4))) *table_t;
+  const table_t table = (table_t)(g.page_table + int64_t(slot) * g.max_pages);
+  const int in_page = (1 << g.page_shift) - 1;
+
+  // Rows of a tile.  A token that is not visible, or whose page id is not a page, reads
+  // page 0's rows (always there) and is masked by its bit of `seen`.
+  struct Rows {
+    int row;   // kWide: first row of the tile; else lane i < 32: row of token t0 + i
+    u32 seen;
+  };
+  // The page ids are loaded two tiles ahead, before the keys and values of the next tile:
+  // loads return in order, so waiting for an id that was asked for after them would wait for
+  // them too.
+  auto ask = [&](int t0) -> int {
+    if constexpr (kWide) return table[min(t0, last - 1) >> g.page_shift];
+    else return table[max(begin, min(t0 + (lane & 31), last - 1)) >> g.page_shift];
+  };
+  auto resolve = [&](int t0, int page) -> Rows {
+    Rows r;
+    if constexpr (kWide) {
+      const bool ok = page > 0 && page < g.pages;
+      if (!ok && t0 < last) {
+        if (lane == 0) set_err(g.err, GDN_ERRW_BAD_PAGE);
+      }
+      r.row = ok ? ((page * g.kv_heads + h) << g.page_shift) + (t0 & in_page) : 0;
+      // bits from begin on, and below last
+      u32 m = ok ? 0xffffffffu : 0u;
+      if (begin > t0) m &= begin - t0 >= 32 ? 0u : 0xffffffffu << (begin - t0);
+      if (last - t0 < 32) m &= last > t0 ? (1u << (last - t0)) - 1u : 0u;
+      r.seen = m;
+    } else {
+      const int t = t0 + (lane & 31);
+      const bool in = t >= begin && t < last;
+      const bool ok = in && page > 0 && page < g.pages;
+      if (__any(in && !ok)) {
+        if (lane == 0) set_err(g.err, GDN_ERRW_BAD_PAGE);
+      }
+      r.row = ok ? ((page * g.kv_heads + h) << g.page_shift) + (t & in_page) : 0;
+      r.seen = u32(__ballot(ok));  // lanes 32 up repeat the lower ones
+    }
+    return r;
+  };
+
+  Words<4> kw[2][L::kPieces];
+  Words<L::kVWords> vw[8][L::kVPieces];
+  const u32 k_off = u32(c * RB + 16 * gr), v_off = u32(4 * gr * RB + 4 * L::kVWords * c);
+  auto load_k = [&](const Rows &r) {
+    const char *tile = g.k + int64_t(r.row) * RB;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const char *at;
+      if constexpr (kWide) at = tile + 16 * u * RB + k_off;
+      else at = g.k + int64_t(__shfl(r.row, 16 * u + c)) * RB + 16 * gr;
+#pragma unroll
+      for (int s = 0; s < L::kPieces; ++s) kw[u][s] = load_words<4>(at + 64 * s);
+    }
+  };
+  auto load_v = [&](const Rows &r) {
+    const char *tile = g.v + int64_t(r.row) * RB;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const char *at;
+      if constexpr (kWide) at = tile + pk(0, e) * RB + v_off;
+      else at = g.v + int64_t(__shfl(r.row, pk(gr, e))) * RB + 4 * L::kVWords * c;
+#pragma unroll
+      for (int s = 0; s < L::kVPieces; ++s) vw[e][s] = load_words<L::kVWords>(at + 256 * s);
+    }
+  };
+
+  // Queries as the B operand (columns past the group are zero), asked for before the first
+  // keys for the same reason.
+  constexpr int kQLoads = kQShared ? KS / kWaves : KS;
+  bf16x8 qf[kQLoads];
   {
     const uint16_t *q = p.a.q + int64_t(b) * p.a.q_stride + int64_t(q0 + min(c, heads - 1)) * D;
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      u32x4 w = *reinterpret_cast<const u32x4 *>(q + L::kdim(s, gr));
-      if (c >= heads) w = u32x4{0, 0, 0, 0};
-      qf[s] = __builtin_bit_cast(bf16x8, w);
-    }
+    for (int i = 0; i < kQLoads; ++i)
+      qf[i] = *reinterpret_cast<const bf16x8 *>(q + L::kdim(kQShared ? wave * kQLoads + i : i, gr));
   }
+  __builtin_amdgcn_sched_barrier(0);
+
+  constexpr int kStep = kTile * kWaves;
+  int t0 = first + kTile * wave;
+  Rows now{0, 0}, next{0, 0};
+  {
+    const int p0 = ask(t0), p1 = ask(t0 + kStep);
+    now = resolve(t0, p0);
+    if (t0 < last) {
+      load_k(now);
+      load_v(now);
+    }
+    next = resolve(t0 + kStep, p1);
+  }
+
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int i = 0; i < kQLoads; ++i) {
+    if (c >= heads) qf[i] = bf16x8{};
+    if constexpr (kQShared) sq[wave * kQLoads + i][lane] = __builtin_bit_cast(u32x4, qf[i]);
+  }
+  if constexpr (kQShared) __syncthreads();
   const float to_log2 = p.a.scale * g.k_scale * kLog2e;
-  const int32_t *table = g.page_table + int64_t(slot) * g.max_pages;
-  const int in_page = (1 << g.page_shift) - 1;
 
   f32x4 o[NO];
 #pragma unroll
   for (int i = 0; i < NO; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
   float m = kNegInf, l = 0.f;
 
-  // rows of the tile at t0: lane i < 32 looks up token t0 + i.  A token that is not
-  // visible or has no page reads page 0's first row (always there) and is masked.
-  auto lookup = [&](int t0, int *row, u32 *seen) {
-    const int t = t0 + (lane & 31);
-    int r = 0;
-    bool ok = false;
-    if (t >= begin && t < last) {
-      const int page = table[t >> g.page_shift];
-      ok = page > 0 && page < g.pages;
-      if (ok) r = ((page * g.kv_heads + h) << g.page_shift) + (t & in_page);
-      else set_err(g.err, GDN_ERRW_BAD_PAGE);
-    }
-    *row = r;
-    *seen = u32(__ballot(ok));  // lanes 32 up repeat the lower ones
-  };
-
-  Words<4> kw[2][L::kPieces];
-  Words<L::kVWords> vw[8][L::kVPieces];
-  auto load_k = [&](int row) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int r = __shfl(row, 16 * u + c);
-      const char *at = g.k + int64_t(r) * (D * L::kSize) + 16 * gr;
-#pragma unroll
-      for (int s = 0; s < L::kPieces; ++s) kw[u][s] = load_words<4>(at + 64 * s);
-    }
-  };
-  auto load_v = [&](int row) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int r = __shfl(row, pk(gr, e));
-      const char *at = g.v + int64_t(r) * (D * L::kSize) + 4 * L::kVWords * c;
-#pragma unroll
-      for (int s = 0; s < L::kVPieces; ++s) vw[e][s] = load_words<L::kVWords>(at + 256 * s);
-    }
-  };
-
-  constexpr int kStep = kTile * kWaves;
-  int t0 = first + kTile * wave;
-  int row, row_next = 0;
-  u32 seen, seen_next = 0;
-  if (t0 < last) {
-    lookup(t0, &row, &seen);
-    load_k(row);
-    load_v(row);
-  }
-  for (; t0 < last; t0 += kStep) {
-    const int t1 = t0 + kStep;
-    const bool more = t1 < last;
-    if (more) lookup(t1, &row_next, &seen_next);
+  // One tile.  The last one of a wave is a body of its own: loads under a condition would
+  // make every wait of the loop assume that they were not issued, and wait for all.
+  auto tile = [&](auto more_c) {
+    constexpr bool more = decltype(more_c)::value;
+    const int page2 = more ? ask(t0 + 2 * kStep) : 0;
 
     // ---- scores ----------------------------------------------------------
-    f32x4 s[2];
+    f32x4 s[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      s[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int st = 0; st < KS; ++st) {
+      bf16x8 qv;
+      if constexpr (kQShared) qv = __builtin_bit_cast(bf16x8, sq[st][lane]);
+      else qv = qf[st];
 #pragma unroll
-      for (int st = 0; st < KS; ++st) {
+      for (int u = 0; u < 2; ++u) {
         u32x4 w;
         if constexpr (kF8) {
           const u32 x0 = kw[u][st >> 1].w[2 * (st & 1)], x1 = kw[u][st >> 1].w[2 * (st & 1) + 1];
@@ -267,21 +321,25 @@ void attn_decode_kernel(KvGeom g, AttnDev p) {
         } else {
           w = u32x4{kw[u][st].w[0], kw[u][st].w[1], kw[u][st].w[2], kw[u][st].w[3]};
         }
-        s[u] = mfma_bf16(__builtin_bit_cast(bf16x8, w), qf[st], s[u]);
+        s[u] = mfma_bf16(__builtin_bit_cast(bf16x8, w), qv, s[u]);
       }
     }
-    if (more) load_k(row_next);
+    // (the barriers keep the next tile's loads behind the last use of their registers)
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (more) load_k(next);
+    __builtin_amdgcn_sched_barrier(0);
 
     // ---- softmax ---------------------------------------------------------
     float x[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = s[e >> 2][e & 3] * to_log2;
+    const u32 seen = now.seen;
     const bool whole = seen == 0xffffffffu;
     if (!whole) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] = (seen >> pk(gr, e)) & 1 ? x[e] : kNegInf;
     }
-    if (p.scores && c < heads) {
+    if (kMass && c < heads) {
       float *at = p.scores + (qrow + c) * p.lpad + t0 + 4 * gr;
       st4(at, f32x4{x[0], x[1], x[2], x[3]});
       st4(at + 16, f32x4{x[4], x[5], x[6], x[7]});
@@ -328,9 +386,17 @@ void attn_decode_kernel(KvGeom g, AttnDev p) {
         o[2 * w + hf] = mfma_bf16(av, ps.hi, o[2 * w + hf]);
       }
     }
-    if (more) load_v(row_next);
-    row = row_next;
-    seen = seen_next;
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (more) {
+      load_v(next);
+      __builtin_amdgcn_sched_barrier(0);
+      now = next;
+      next = resolve(t0 + 2 * kStep, page2);
+    }
+  };
+  if (t0 < last) {
+    for (; t0 + kStep < last; t0 += kStep) tile(std::true_type{});
+    tile(std::false_type{});
   }
 
   // ---- join the waves: o[i][j] is column vdim(i, 4 gr + j) of head c ---------
@@ -481,7 +547,10 @@ int64_t score_row(int max_len) { return (int64_t(max_len) + kTile - 1) / kTile *
 template <int D, bool kF8>
 hipError_t launch_dt(const KvGeom &g, const AttnDev &p, int64_t blocks, hipStream_t s) {
   const size_t lds = size_t(2) * std::min(16, p.group) * (D + 4) * 4;
-  hipLaunchKernelGGL((attn_decode_kernel<D, kF8>), dim3(unsigned(blocks)), dim3(kThreads), lds, s, g, p);
+  const bool wide = (1 << g.page_shift) >= kTile;
+  const auto kernel = wide ? (p.scores ? attn_decode_kernel<D, kF8, true, true> : attn_decode_kernel<D, kF8, true, false>)
+                           : (p.scores ? attn_decode_kernel<D, kF8, false, true> : attn_decode_kernel<D, kF8, false, false>);
+  hipLaunchKernelGGL(kernel, dim3(unsigned(blocks)), dim3(kThreads), lds, s, g, p);
   return hipGetLastError();
 }
 
@@ -503,7 +572,7 @@ AttnSplit attn_split(const gdn_kv_pool *p, int batch, int q_heads, int max_len) 
   const int group = q_heads / p->d.kv_heads;
   r.head_blocks = (group + 15) / 16;
   const int64_t units = std::max<int64_t>(1, int64_t(batch) * p->d.kv_heads * r.head_blocks);
-  const int64_t want = std::max<int64_t>(1, 1024 / units);
+  const int64_t want = std::max<int64_t>(1, 512 / units);
   const int step = kTile * kWaves;
   const int64_t chunk = std::max<int64_t>(1, (max_len + want - 1) / want);
   r.chunk = int((chunk + step - 1) / step * step);
