@@ -11,6 +11,11 @@ import torch
 
 from ._binding import GDN_BF16, GDN_F32, _check, _f32, _i32, _i64, _lib, _sz, _u32, _vp
 
+# the current device and stream as plain numbers (torch.cuda's objects cost more than the
+# launch of a small kernel)
+_current_device = torch._C._cuda_getDevice
+_current_raw_stream = torch._C._cuda_getCurrentRawStream
+
 GDN_F8_E4M3 = 2
 ERRW_BAD_PAGE = 16
 ATTN_ACCUM_MASS = 1
@@ -47,31 +52,31 @@ for _f in ("kv_pool_bytes", "kv_pool_create", "kv_append", "attn_workspace_bytes
     getattr(_lib, _f).restype = ct.c_int
 
 
-def _on(device):
-    """The device that a call runs on; every tensor of the call has to be there."""
-    if device.type != "cuda":
+def _on(index) -> int:
+    """The device that a call runs on, by number; every tensor of the call has to be there."""
+    if index < 0:
         raise ValueError("tensor must be on the GPU")
-    if device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
-    return device
+    if index != _current_device():
+        raise ValueError(f"tensors are on cuda:{index}, the current device is cuda:{_current_device()}")
+    return index
 
 
-def _on_stream(stream, device) -> int:
+def _on_stream(stream, index) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
-        raise ValueError(f"stream of {stream.device}, tensors on {device}")
+        return _current_raw_stream(index)
+    if stream.device_index != index:
+        raise ValueError(f"stream of cuda:{stream.device_index}, tensors on cuda:{index}")
     return stream.cuda_stream
 
 
-def _arg(t, dtype, numel, name, device):
+def _arg(t, dtype, numel, name, index):
     """Pointer of a contiguous tensor of at least numel elements (None stays None)."""
     if t is None:
         return None
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name}: on {t.device}, expected cuda:{index}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
     if t.numel() < numel:
@@ -79,19 +84,19 @@ def _arg(t, dtype, numel, name, device):
     return t.data_ptr()
 
 
-def _rows(t, n, heads, dim, name, device):
+def _rows(t, n, heads, dim, name, index):
     """(pointer, stride) of bf16 [n, heads, dim] whose rows [heads, dim] are contiguous
     at any distance."""
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
-    if tuple(t.shape) != (n, heads, dim):
+    if t.get_device() != index:
+        raise ValueError(f"{name}: on {t.device}, expected cuda:{index}")
+    if t.shape != (n, heads, dim):
         raise ValueError(f"{name}: expected {(n, heads, dim)}, got {tuple(t.shape)}")
-    s = t.stride()
-    if (dim > 1 and s[2] != 1) or (heads > 1 and s[1] != dim):
+    s0, s1, s2 = t.stride()
+    if (dim > 1 and s2 != 1) or (heads > 1 and s1 != dim):
         raise ValueError(f"{name}: [heads, dim] must be contiguous within a row")
-    return t.data_ptr(), s[0] if n > 1 else heads * dim
+    return t.data_ptr(), s0 if n > 1 else heads * dim
 
 
 def kv_pool_bytes(layers, pages, kv_heads, page_size, head_dim, slots, max_pages, kv_dtype):
@@ -111,7 +116,7 @@ class KvPool:
         self.mass, self.pos, self.err_word = mass, pos, err_word
         self.layers, self.pages, self.kv_heads, self.page_size, self.head_dim = k.shape
         self.slots, self.max_pages = page_table.shape
-        self.device = k.device
+        self.device = k.get_device()
 
     @property
     def capacity(self):
@@ -145,7 +150,7 @@ def kv_pool_create(k, v, page_table, mass=None, pos=None, err_word=None, k_scale
         raise TypeError("k and v must be bfloat16 or float8_e4m3fn")
     L, P, H, S, D = k.shape
     N, M = page_table.shape
-    dev = _on(k.device)
+    dev = _on(k.get_device())
     for t, name in ((mass, "mass"), (pos, "pos")):
         if t is not None and tuple(t.shape) != (L, N, H, M * S):
             raise ValueError(f"{name} must be [layers, slots, kv_heads, max_pages * page_size]")
@@ -237,7 +242,7 @@ def block_norm(y, out, w_post=None, gate=None, act=ACT_NONE, scale=1.0, residual
     [tokens, groups, dim]; ``w_post``, ``w_pre`` bf16 or fp32 [dim]."""
     if y.dim() != 3:
         raise ValueError("y must be [tokens, groups, dim]")
-    dev = _on(y.device)
+    dev = _on(y.get_device())
     T, G, D = y.shape
     yp, ys = _rows(y, T, G, D, "y", dev)
     gp, gs = _rows(gate, T, G, D, "gate", dev) if gate is not None else (None, 0)

@@ -71,6 +71,8 @@ gdn_status check_attn(gdn_kv_pool_t p, int batch, int q_heads, int max_len, uint
   if (flags & ~uint32_t(GDN_F_ACCUM_MASS)) return fail(GDN_ERR_ARG, "unknown flag bits 0x%x", flags);
   if ((flags & GDN_F_ACCUM_MASS) && !p->d.mass)
     return fail(GDN_ERR_ARG, "GDN_F_ACCUM_MASS needs a pool with mass");
+  if (!gdn::attn_fits(p, batch, q_heads, max_len))
+    return fail(GDN_ERR_RANGE, "batch * kv_heads * max_len too large (2^31 blocks of 128 tokens)");
   return GDN_OK;
 }
 

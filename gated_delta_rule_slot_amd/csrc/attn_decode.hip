@@ -20,10 +20,14 @@
 // P is carried as two bf16 parts (hi + lo, 16 bits): rounded once to bf16 its error would
 // be about as large as the output's own rounding.  Scores, m, l and O are fp32.
 //
-// Workgroups: x = (split, request, key-value head, block of 16 query heads), 4 waves whose
-// tiles alternate; the waves' results join in shared memory.  With more than one split
-// (or with weights to accumulate) m, l and O of each split go to the workspace, and a
-// second kernel joins them.
+// The work is counted in blocks of 128 tokens (4 waves, a tile each), in the order
+// (request, key-value head, 16 query heads, position), and every workgroup takes an equal
+// run of blocks: as many workgroups as run at once, whatever the requests' lengths.  (Equal
+// splits of the longest length left a third of the chip waiting for a ragged batch.)  A
+// workgroup finds its run from the lengths on the device, walks it unit by unit, and
+// joins its waves in shared memory at the end of each unit.  A unit that lies in
+// one workgroup is final there; of the others m, l and O go to the workspace, and a second
+// kernel joins them (and adds up the weights, from stored scores).
 #include <algorithm>
 #include <type_traits>
 
@@ -41,38 +45,51 @@ constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.693147180559945309417f;
 constexpr float kNegInf = -__builtin_inff();
 
+constexpr int kBlock = kTile * kWaves;  // tokens of a block
+constexpr int kCUs = 256;
+
 struct AttnDev {
   AttnArgs a;
-  int head_blocks, group, chunk, splits;
-  int part;         // 1: write partial results, 0: final ones
+  int head_blocks, group, workers;
+  int join;         // whether the joining kernel runs (else every unit is one block at most)
   int64_t lpad;     // row length of the score array
-  float *o;         // [batch][q_heads][splits][D]
-  float *ml;        // [batch][q_heads][splits][2]
-  float *scores;    // [batch][q_heads][lpad], log2 units; NULL without weights
+  int32_t *pre;     // [batch + 1] blocks of the requests before each, per head and head block
+  float *o;         // [workers][2][16][D]: O of a worker's first and of its last unit
+  float *ml;        // [workers][2][16][2]: their m and l
+  float *done;      // [batch][q_heads][2]: m and l of units within one worker; with weights
+  float *scores;    // [batch][q_heads][lpad], log2 units; with weights
 };
 
-// the visible range of request b; false if there is none (with the reason told once)
-__device__ __forceinline__ bool visible(const KvGeom &g, const AttnArgs &a, int b, bool teller, int *slot,
-                                        int *begin, int *len) {
-  *slot = a.slot_table[b];
-  *len = a.kv_len[b];
-  *begin = a.kv_begin ? a.kv_begin[b] : 0;
-  if (*slot <= 0 || *slot >= g.slots) {
-    if (teller && *slot >= g.slots) set_err(g.err, GDN_ERRW_BAD_SLOT);
-    return false;
+// The visible range of request b and its number of blocks, 0 if it sees nothing (the reason
+// is told by one caller).
+struct Seen {
+  int slot, begin, len, blocks;
+};
+__device__ __forceinline__ Seen seen_by(const KvGeom &g, const AttnArgs &a, int b, bool tell) {
+  Seen r;
+  r.slot = a.slot_table[b];
+  r.len = a.kv_len[b];
+  r.begin = a.kv_begin ? a.kv_begin[b] : 0;
+  r.blocks = 0;
+  if (r.slot <= 0 || r.slot >= g.slots) {
+    if (tell && r.slot >= g.slots) set_err(g.err, GDN_ERRW_BAD_SLOT);
+  } else if (r.len < 0 || r.len > a.max_len || r.begin < 0) {
+    if (tell) set_err(g.err, GDN_ERRW_BAD_SEQLENS);
+  } else if (r.begin < r.len) {
+    r.blocks = (r.len - (r.begin & ~(kTile - 1)) + kBlock - 1) / kBlock;
   }
-  if (*len < 0 || *len > a.max_len || *begin < 0) {
-    if (teller) set_err(g.err, GDN_ERRW_BAD_SEQLENS);
-    return false;
-  }
-  return *begin < *len;
+  return r;
 }
 
-// splits that hold tokens: split s has tiles from begin / 32 + s * chunk / 32 on
-__device__ __forceinline__ int active_splits(int begin, int len, int chunk) {
-  const int seen = len - (begin & ~(kTile - 1));
-  return (seen + chunk - 1) / chunk;
+// First block of worker w, and the worker that holds block x: floor(w all / workers) is the
+// first, so the holder is the largest w with w all < (x + 1) workers.
+// (The host keeps the number of blocks below 2^31.)
+__device__ __forceinline__ int first_block(int w, int all, int workers) { return int(int64_t(w) * all / workers); }
+__device__ __forceinline__ int worker_of(int x, int all, int workers) {
+  return int(((int64_t(x) + 1) * workers - 1) / all);
 }
+// A value that is the same in every lane, as a scalar.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // max / sum over the four 16-lane groups (same head), left in every lane
 __device__ __forceinline__ float rows_max(float v) {
@@ -164,27 +181,89 @@ void attn_decode_kernel(KvGeom g, AttnDev p) {
   __shared__ float sm[kWaves][16], sl[kWaves][16];
   __shared__ u32x4 sq[kQShared ? KS : 1][64];
 
-  const int lane = threadIdx.x & 63, c = lane & 15, gr = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int split = blockIdx.x % p.splits, unit = blockIdx.x / p.splits;
-  const int hb = unit % p.head_blocks, bh = unit / p.head_blocks;
-  const int h = bh % g.kv_heads, b = bh / g.kv_heads;
-  const int heads = min(16, p.group - 16 * hb);           // query heads of this block
-  const int q0 = h * p.group + 16 * hb;                   // the first of them
-  int slot, begin, len;
-  const bool any = visible(g, p.a, b, split == 0 && hb == 0 && h == 0 && threadIdx.x == 0, &slot, &begin, &len);
-  const int64_t qrow = int64_t(b) * p.a.q_heads + q0;
-  if (!any) {
-    if (!p.part) {
-      for (int i = threadIdx.x; i < heads * D / 2; i += kThreads)
-        reinterpret_cast<u32 *>(p.a.out + qrow * D)[i] = 0;
-      if (p.a.lse && int(threadIdx.x) < heads) p.a.lse[qrow + threadIdx.x] = kNegInf;
+  __shared__ int spre[kThreads];
+  __shared__ int sfound[2 + kWaves];
+
+  const int lane = threadIdx.x & 63;
+  const int wave = uniform(threadIdx.x >> 6);
+  const int worker = blockIdx.x;
+  const int units = g.kv_heads * p.head_blocks;  // of a request
+
+  // ---- this worker's run of blocks ---------------------------------------------
+  // scan(base): spre[i] = blocks of requests base .. base + i, returns their sum
+  auto scan = [&](int base) -> int {
+    const int r = base + int(threadIdx.x);
+    int inc = r < p.a.batch ? seen_by(g, p.a, r, false).blocks : 0;
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_up(inc, d);
+      if (lane >= d) inc += o;
     }
-    return;  // the joining kernel sees the same range
+    __syncthreads();  // the previous use of the shared sums is over
+    if (lane == 63) sfound[2 + wave] = inc;
+    __syncthreads();
+    for (int w = 0; w < wave; ++w) inc += sfound[2 + w];
+    spre[threadIdx.x] = inc;
+    __syncthreads();
+    return uniform(spre[kThreads - 1]);
+  };
+  int all = 0;
+  for (int base = 0; base < p.a.batch; base += kThreads) {
+    const int sum = scan(base);
+    if (p.join && worker == 0 && base + int(threadIdx.x) < p.a.batch)
+      p.pre[base + threadIdx.x + 1] = all + spre[threadIdx.x];
+    all += sum;
   }
-  if (split >= active_splits(begin, len, p.chunk)) return;
-  const int first = (begin & ~(kTile - 1)) + split * p.chunk;
-  const int last = min(len, first + p.chunk);
+  if (p.join && worker == 0 && threadIdx.x == 0) p.pre[0] = 0;
+  all *= units;
+  const int sharing = min(p.workers, all);  // so that no worker between two others has nothing
+  const int run_first = worker < sharing ? first_block(worker, all, sharing) : 0;
+  int left = worker < sharing ? first_block(worker + 1, all, sharing) - run_first : 0;
+  int b = 0;       // request, unit within it and block within the unit
+  int unit = 0, blk = 0;
+  Seen rq{0, 0, 0, 0};
+  auto request = [&](int r) -> Seen {
+    const Seen v = seen_by(g, p.a, r, false);
+    return Seen{uniform(v.slot), uniform(v.begin), uniform(v.len), uniform(v.blocks)};
+  };
+  if (left > 0) {
+    const int x = run_first / units;
+    int before = 0;
+    for (int base = 0; base < p.a.batch; base += kThreads) {
+      const int sum = p.a.batch > kThreads ? scan(base) : uniform(spre[kThreads - 1]);
+      if (x < before + sum) {
+        const int lo = before + (threadIdx.x ? spre[threadIdx.x - 1] : 0), hi = before + spre[threadIdx.x];
+        if (lo <= x && x < hi) {
+          sfound[0] = base + threadIdx.x;
+          sfound[1] = lo;
+        }
+        break;
+      }
+      before += sum;
+    }
+    __syncthreads();
+    b = uniform(sfound[0]);
+    rq = request(b);
+    const int in_request = run_first - uniform(sfound[1]) * units;
+    unit = in_request / rq.blocks;
+    blk = in_request - unit * rq.blocks;
+  }
+
+  bool first_unit = true;
+  while (left > 0) {
+    // (made anew for each unit: addresses that depend on the lane alone would otherwise be
+    // kept in registers across all units, 20 of them)
+    int lane_now = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane_now));
+    const int lane = lane_now, c = lane & 15, gr = lane >> 4;
+    const int nblk = min(rq.blocks - blk, left);
+    const int h = unit / p.head_blocks, hb = unit - h * p.head_blocks;
+    const int slot = rq.slot, begin = rq.begin;
+    const int first = (begin & ~(kTile - 1)) + blk * kBlock;
+    const int last = min(rq.len, first + nblk * kBlock);
+    const bool whole_unit = nblk == rq.blocks;
+    const int heads = min(16, p.group - 16 * hb);           // query heads of this unit
+    const int q0 = h * p.group + 16 * hb;                   // the first of them
+    const int64_t qrow = int64_t(b) * p.a.q_heads + q0;
 
   // (constant address space: the table does not change during the call, so a wave-uniform
   // read of it is a scalar load, which the waits for keys and values do not count)
@@ -438,8 +517,8 @@ void attn_decode_kernel(KvGeom g, AttnDev p) {
 #pragma unroll
     for (int w = 0; w < kWaves; ++w) lt = fmaf(sl[w][hd], factor(sm[w][hd], mh), lt);
     f32x4 sum = ld4(lds + hd * DS + d) + ld4(lds + (heads + hd) * DS + d);
-    if (p.part) {
-      const int64_t r = (qrow + hd) * p.splits + split;
+    if (!whole_unit) {
+      const int64_t r = (int64_t(worker) * 2 + (first_unit ? 0 : 1)) * 16 + hd;
       st4(p.o + r * D + d, sum);
       if (d == 0) {
         p.ml[2 * r] = mh;
@@ -449,47 +528,104 @@ void attn_decode_kernel(KvGeom g, AttnDev p) {
       sum *= lt == 0.f ? 0.f : g.v_scale / lt;
       *reinterpret_cast<u32x2 *>(p.a.out + (qrow + hd) * D + d) =
           u32x2{cvt_pk_bf16(sum[0], sum[1]), cvt_pk_bf16(sum[2], sum[3])};
-      if (p.a.lse && d == 0) p.a.lse[qrow + hd] = lt == 0.f ? kNegInf : (mh + log2f(lt)) * kLn2;
+      if (d == 0) {
+        if (p.a.lse) p.a.lse[qrow + hd] = lt == 0.f ? kNegInf : (mh + log2f(lt)) * kLn2;
+        if (kMass) {
+          p.done[2 * (qrow + hd)] = mh;
+          p.done[2 * (qrow + hd) + 1] = lt;
+        }
+      }
     }
+  }
+  __syncthreads();  // the shared arrays are free again
+
+    // ---- the next unit -------------------------------------------------------------
+    left -= nblk;
+    blk = 0;
+    first_unit = false;
+    if (left > 0 && ++unit == units) {
+      unit = 0;
+      do rq = request(++b);
+      while (rq.blocks == 0 && b + 1 < p.a.batch);
+      if (rq.blocks == 0) break;
+    }
+  }
+
+  // ---- requests that see nothing, dealt out to the workers ------------------------
+  for (int e = worker; e < p.a.batch; e += p.workers) {
+    if (seen_by(g, p.a, e, threadIdx.x == 0).blocks) continue;
+    const int64_t row = int64_t(e) * p.a.q_heads;
+    for (int i = threadIdx.x; i < p.a.q_heads * (D / 8); i += kThreads)
+      reinterpret_cast<u32x4 *>(p.a.out + row * D)[i] = u32x4{0, 0, 0, 0};
+    if (p.a.lse && int(threadIdx.x) < p.a.q_heads)
+      for (int i = threadIdx.x; i < p.a.q_heads; i += kThreads) p.a.lse[row + i] = kNegInf;
   }
 }
 
-// Joins the splits of each (request, query head), and adds the weights
+// Joins the parts of each (request, query head) that more than one worker had, and adds
+// the weights
 //   mass[t] += sum over the group's heads of 2^(score - m) / l.
 // Workgroups: first one per (request, query head), then, with weights, one per
 // kMassTokens tokens of each (request, key-value head).
 constexpr int kMassTokens = 1024;
 
+// The workers w0 .. w1 of a unit; the part of w0 is its first unit's where its run begins
+// with the unit, else its last; the others' is their first.
+struct Parts {
+  int w0, w1;
+  bool begins;
+  __device__ __forceinline__ int64_t row(int w, int head) const {
+    return (int64_t(w) * 2 + (w == w0 && !begins ? 1 : 0)) * 16 + head;
+  }
+};
+__device__ __forceinline__ Parts parts_of(const KvGeom &g, const AttnDev &p, int b, int unit) {
+  const int units = g.kv_heads * p.head_blocks;
+  const int n = p.pre[b + 1] - p.pre[b], all = p.pre[p.a.batch] * units;
+  const int first = p.pre[b] * units + unit * n, sharing = min(p.workers, all);
+  Parts r{0, -1, true};
+  if (n > 0) {
+    r.w0 = worker_of(first, all, sharing);
+    r.w1 = worker_of(first + n - 1, all, sharing);
+    r.begins = first_block(r.w0, all, sharing) == first;
+  }
+  return r;
+}
+// m and l of a head over the parts, by the lanes of a wave
+__device__ __forceinline__ void join_ml(const float *ml, const Parts &pt, int head, int lane, float *m, float *l) {
+  float mm = kNegInf, ll = 0.f;
+  for (int w = pt.w0 + lane; w <= pt.w1; w += 64) mm = fmaxf(mm, ml[2 * pt.row(w, head)]);
+  for (int x = 32; x; x >>= 1) mm = fmaxf(mm, __shfl_xor(mm, x));
+  for (int w = pt.w0 + lane; w <= pt.w1; w += 64) {
+    const float *e = ml + 2 * pt.row(w, head);
+    ll = fmaf(e[1], factor(e[0], mm), ll);
+  }
+  *m = mm;
+  *l = wave_sum(ll);
+}
+
 template <int D>
 __global__ __launch_bounds__(kThreads) void attn_join_kernel(KvGeom g, AttnDev p, int mass_blocks) {
   __shared__ __attribute__((aligned(16))) float acc[kWaves][D];
-  __shared__ float sm[kWaves], sl[kWaves];
   __shared__ float hm[64], hl[64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int joins = p.a.batch * p.a.q_heads;
-  int slot, begin, len;
   if (int(blockIdx.x) < joins) {
-    const int64_t qr = blockIdx.x;
-    const int b = int(qr / p.a.q_heads);
-    const bool any = visible(g, p.a, b, false, &slot, &begin, &len);
-    const int ns = any ? active_splits(begin, len, p.chunk) : 0;
-    const float *ml = p.ml + 2 * qr * p.splits;
-    // maximum and sum over the splits, every wave for itself
-    float m = kNegInf, l = 0.f;
-    for (int s = lane; s < ns; s += 64) m = fmaxf(m, ml[2 * s]);
-    for (int x = 32; x; x >>= 1) m = fmaxf(m, __shfl_xor(m, x));
-    for (int s = lane; s < ns; s += 64) l += ml[2 * s + 1] * factor(ml[2 * s], m);
-    l = wave_sum(l);
+    const int qr = blockIdx.x, b = qr / p.a.q_heads, qh = qr - b * p.a.q_heads;
+    const int h = qh / p.group, j = qh - h * p.group;  // head j of the group
+    const Parts pt = parts_of(g, p, b, h * p.head_blocks + (j >> 4));
+    if (pt.w1 <= pt.w0) return;  // nothing, or final already
+    float m, l;
+    join_ml(p.ml, pt, j & 15, lane, &m, &l);  // every wave for itself
     constexpr int C = D / 64;  // columns of a lane
     float sum[C];
 #pragma unroll
     for (int i = 0; i < C; ++i) sum[i] = 0.f;
-    const float *o = p.o + qr * p.splits * D + C * lane;
 #pragma unroll 4
-    for (int s = wave; s < ns; s += kWaves) {
-      const float f = factor(ml[2 * s], m);
+    for (int w = pt.w0 + wave; w <= pt.w1; w += kWaves) {
+      const int64_t r = pt.row(w, j & 15);
+      const float f = factor(p.ml[2 * r], m);
 #pragma unroll
-      for (int i = 0; i < C; ++i) sum[i] = fmaf(f, o[int64_t(s) * D + i], sum[i]);
+      for (int i = 0; i < C; ++i) sum[i] = fmaf(f, p.o[r * D + C * lane + i], sum[i]);
     }
 #pragma unroll
     for (int i = 0; i < C; ++i) acc[wave][C * lane + i] = sum[i];
@@ -499,7 +635,7 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(KvGeom g, AttnDev p
       float t = 0.f;
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) t += acc[w][i];
-      p.a.out[qr * D + i] = f32_to_bf16(t * inv);
+      p.a.out[int64_t(qr) * D + i] = f32_to_bf16(t * inv);
     }
     if (p.a.lse && threadIdx.x == 0) p.a.lse[qr] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
     return;
@@ -507,115 +643,133 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(KvGeom g, AttnDev p
   const int64_t id = int64_t(blockIdx.x) - joins;
   const int block = int(id % mass_blocks), bh = int(id / mass_blocks);
   const int h = bh % g.kv_heads, b = bh / g.kv_heads;
-  if (!visible(g, p.a, b, false, &slot, &begin, &len)) return;
-  const int64_t from = int64_t(begin & ~3) + int64_t(block) * kMassTokens;
-  if (from >= len) return;
-  const int ns = active_splits(begin, len, p.chunk);
+  const Seen rq = seen_by(g, p.a, b, false);
+  const int64_t from = int64_t(rq.begin & ~3) + int64_t(block) * kMassTokens;
+  if (rq.blocks == 0 || from >= rq.len) return;
   const int64_t qr0 = int64_t(b) * p.a.q_heads + h * p.group;
-  for (int hd = wave; hd < p.group; hd += kWaves) {
-    const float *ml = p.ml + 2 * (qr0 + hd) * p.splits;
-    float m = kNegInf, l = 0.f;
-    for (int s = lane; s < ns; s += 64) m = fmaxf(m, ml[2 * s]);
-    for (int x = 32; x; x >>= 1) m = fmaxf(m, __shfl_xor(m, x));
-    for (int s = lane; s < ns; s += 64) l += ml[2 * s + 1] * factor(ml[2 * s], m);
-    l = wave_sum(l);
+  for (int j = wave; j < p.group; j += kWaves) {
+    const Parts pt = parts_of(g, p, b, h * p.head_blocks + (j >> 4));
+    float m, l;
+    if (pt.w1 > pt.w0) {
+      join_ml(p.ml, pt, j & 15, lane, &m, &l);
+    } else {
+      m = p.done[2 * (qr0 + j)];
+      l = p.done[2 * (qr0 + j) + 1];
+    }
     if (lane == 0) {
-      hm[hd] = ref(m);
-      hl[hd] = l == 0.f ? 0.f : 1.f / l;
+      hm[j] = ref(m);
+      hl[j] = l == 0.f ? 0.f : 1.f / l;
     }
   }
   __syncthreads();
   const int64_t t = from + 4 * threadIdx.x;
-  if (t >= len) return;
+  if (t >= rq.len) return;
   f32x4 sum = {0.f, 0.f, 0.f, 0.f};
   const float *sc = p.scores + qr0 * p.lpad + t;
 #pragma unroll 4
-  for (int hd = 0; hd < p.group; ++hd) {
-    const f32x4 x = ld4(sc + hd * p.lpad);
+  for (int j = 0; j < p.group; ++j) {
+    const f32x4 x = ld4(sc + j * p.lpad);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) sum[j] = fmaf(fexp2(x[j] - hm[hd]), hl[hd], sum[j]);
+    for (int e = 0; e < 4; ++e) sum[e] = fmaf(fexp2(x[e] - hm[j]), hl[j], sum[e]);
   }
-  float *mass = g.mass + (int64_t(slot) * g.kv_heads + h) * g.capacity + t;
+  float *mass = g.mass + (int64_t(rq.slot) * g.kv_heads + h) * g.capacity + t;
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (t + j >= begin && t + j < len) mass[j] += sum[j];
+  for (int e = 0; e < 4; ++e)
+    if (t + e >= rq.begin && t + e < rq.len) mass[e] += sum[e];
 }
 
 size_t pad256(size_t n) { return (n + 255) & ~size_t(255); }
 int64_t score_row(int max_len) { return (int64_t(max_len) + kTile - 1) / kTile * kTile; }
 
 template <int D, bool kF8>
-hipError_t launch_dt(const KvGeom &g, const AttnDev &p, int64_t blocks, hipStream_t s) {
+hipError_t launch_dt(const KvGeom &g, const AttnDev &p, hipStream_t s) {
   const size_t lds = size_t(2) * std::min(16, p.group) * (D + 4) * 4;
   const bool wide = (1 << g.page_shift) >= kTile;
   const auto kernel = wide ? (p.scores ? attn_decode_kernel<D, kF8, true, true> : attn_decode_kernel<D, kF8, true, false>)
                            : (p.scores ? attn_decode_kernel<D, kF8, false, true> : attn_decode_kernel<D, kF8, false, false>);
-  hipLaunchKernelGGL(kernel, dim3(unsigned(blocks)), dim3(kThreads), lds, s, g, p);
+  hipLaunchKernelGGL(kernel, dim3(unsigned(p.workers)), dim3(kThreads), lds, s, g, p);
   return hipGetLastError();
 }
 
 template <int D>
-hipError_t launch_d(const KvGeom &g, const AttnDev &p, bool f8, int64_t blocks, hipStream_t s) {
-  hipError_t e = f8 ? launch_dt<D, true>(g, p, blocks, s) : launch_dt<D, false>(g, p, blocks, s);
-  if (e != hipSuccess || !p.part) return e;
+hipError_t launch_d(const KvGeom &g, const AttnDev &p, bool f8, hipStream_t s) {
   const int mass_blocks = p.scores ? (p.a.max_len + 3 + kMassTokens - 1) / kMassTokens : 0;
   const int64_t joins = int64_t(p.a.batch) * p.a.q_heads + int64_t(p.a.batch) * g.kv_heads * mass_blocks;
   if (joins >= (int64_t(1) << 31)) return hipErrorInvalidValue;
+  hipError_t e = f8 ? launch_dt<D, true>(g, p, s) : launch_dt<D, false>(g, p, s);
+  if (e != hipSuccess || !p.join) return e;
   hipLaunchKernelGGL((attn_join_kernel<D>), dim3(unsigned(joins)), dim3(kThreads), 0, s, g, p, mass_blocks);
   return hipGetLastError();
 }
 
-}  // namespace
+// Blocks of a unit of max_len tokens (its first tile may begin before the first one seen).
+int64_t unit_blocks(int max_len) { return std::max<int64_t>(1, (int64_t(max_len) + kTile - 1 + kBlock - 1) / kBlock); }
 
-AttnSplit attn_split(const gdn_kv_pool *p, int batch, int q_heads, int max_len) {
-  AttnSplit r;
+// Workers of a call: what runs at once, or fewer where there are not that many blocks.
+int attn_workers(const gdn_kv_pool *p, int batch, int q_heads, int max_len) {
   const int group = q_heads / p->d.kv_heads;
-  r.head_blocks = (group + 15) / 16;
-  const int64_t units = std::max<int64_t>(1, int64_t(batch) * p->d.kv_heads * r.head_blocks);
-  const int64_t want = std::max<int64_t>(1, 512 / units);
-  const int step = kTile * kWaves;
-  const int64_t chunk = std::max<int64_t>(1, (max_len + want - 1) / want);
-  r.chunk = int((chunk + step - 1) / step * step);
-  r.splits = std::max(1, int((int64_t(max_len) + r.chunk - 1) / r.chunk));
+  const int64_t units = int64_t(batch) * p->d.kv_heads * ((group + 15) / 16);
+  return int(std::max<int64_t>(1, std::min<int64_t>(kCUs * 2, units * unit_blocks(max_len))));
+}
+
+// One block per unit at most: no unit is ever divided.
+bool attn_joins(int max_len, uint32_t flags) { return max_len > kBlock || (flags & GDN_F_ACCUM_MASS); }
+
+// Parts of the workspace, in order.
+struct AttnSpace {
+  size_t pre, o, ml, done, scores;
+};
+AttnSpace attn_space(const gdn_kv_pool *p, int batch, int q_heads, int max_len, uint32_t flags) {
+  AttnSpace r{};
+  if (!attn_joins(max_len, flags)) return r;
+  const size_t parts = size_t(attn_workers(p, batch, q_heads, max_len)) * 2 * 16, rows = size_t(batch) * q_heads;
+  r.pre = pad256((size_t(batch) + 1) * 4);
+  r.o = pad256(parts * p->d.head_dim * 4);
+  r.ml = pad256(parts * 8);
+  if (flags & GDN_F_ACCUM_MASS) {
+    r.done = pad256(rows * 8);
+    r.scores = rows * size_t(score_row(max_len)) * 4;
+  }
   return r;
 }
 
+}  // namespace
+
+bool attn_fits(const gdn_kv_pool *p, int batch, int q_heads, int max_len) {
+  const int64_t head_blocks = (q_heads / p->d.kv_heads + 15) / 16;
+  return int64_t(batch) * p->d.kv_heads * head_blocks < (int64_t(1) << 31) / unit_blocks(max_len);
+}
+
 size_t attn_workspace(const gdn_kv_pool *p, int batch, int q_heads, int max_len, uint32_t flags) {
-  const AttnSplit sp = attn_split(p, batch, q_heads, max_len);
-  if (sp.splits == 1 && !(flags & GDN_F_ACCUM_MASS)) return 0;
-  const size_t rows = size_t(batch) * q_heads;
-  size_t n = pad256(rows * sp.splits * p->d.head_dim * 4) + pad256(rows * sp.splits * 8);
-  if (flags & GDN_F_ACCUM_MASS) n += rows * size_t(score_row(max_len)) * 4;
-  return n;
+  const AttnSpace w = attn_space(p, batch, q_heads, max_len, flags);
+  return w.pre + w.o + w.ml + w.done + w.scores;
 }
 
 hipError_t launch_attn_decode(const gdn_kv_pool *pool, int layer, const AttnArgs &a, hipStream_t s) {
-  const AttnSplit sp = attn_split(pool, a.batch, a.q_heads, a.max_len);
   const KvGeom g = kv_geom(pool, layer);
-  const int64_t blocks = int64_t(a.batch) * pool->d.kv_heads * sp.head_blocks * sp.splits;
-  if (blocks >= (int64_t(1) << 31)) return hipErrorInvalidValue;
   AttnDev p{};
   p.a = a;
-  p.head_blocks = sp.head_blocks;
   p.group = a.q_heads / pool->d.kv_heads;
-  p.chunk = sp.chunk;
-  p.splits = sp.splits;
-  p.part = sp.splits > 1 || (a.flags & GDN_F_ACCUM_MASS);
+  p.head_blocks = (p.group + 15) / 16;
+  p.workers = attn_workers(pool, a.batch, a.q_heads, a.max_len);
+  p.join = attn_joins(a.max_len, a.flags);
   p.lpad = score_row(a.max_len);
-  if (p.part) {
-    const size_t rows = size_t(a.batch) * a.q_heads;
-    char *ws = static_cast<char *>(a.workspace);
-    p.o = reinterpret_cast<float *>(ws);
-    ws += pad256(rows * sp.splits * pool->d.head_dim * 4);
-    p.ml = reinterpret_cast<float *>(ws);
-    ws += pad256(rows * sp.splits * 8);
-    if (a.flags & GDN_F_ACCUM_MASS) p.scores = reinterpret_cast<float *>(ws);
+  if (p.join) {
+    const AttnSpace w = attn_space(pool, a.batch, a.q_heads, a.max_len, a.flags);
+    char *at = static_cast<char *>(a.workspace);
+    p.pre = reinterpret_cast<int32_t *>(at);
+    p.o = reinterpret_cast<float *>(at += w.pre);
+    p.ml = reinterpret_cast<float *>(at += w.o);
+    if (a.flags & GDN_F_ACCUM_MASS) {
+      p.done = reinterpret_cast<float *>(at += w.ml);
+      p.scores = reinterpret_cast<float *>(at += w.done);
+    }
   }
   const bool f8 = pool->d.kv_dtype == GDN_F8_E4M3;
   switch (pool->d.head_dim) {
-    case 64: return launch_d<64>(g, p, f8, blocks, s);
-    case 128: return launch_d<128>(g, p, f8, blocks, s);
-    case 256: return launch_d<256>(g, p, f8, blocks, s);
+    case 64: return launch_d<64>(g, p, f8, s);
+    case 128: return launch_d<128>(g, p, f8, s);
+    case 256: return launch_d<256>(g, p, f8, s);
   }
   return hipErrorInvalidValue;
 }

@@ -67,6 +67,7 @@ struct AppendArgs {
   const int32_t *slot_ids, *index, *position;
   const uint16_t *k, *v;
   int64_t k_stride, v_stride;
+  float k_inv, v_inv;  // set by the launcher
 };
 hipError_t launch_kv_append(const gdn_kv_pool *p, int layer, const AppendArgs &a, hipStream_t s);
 
@@ -78,12 +79,8 @@ struct EvictArgs {
 hipError_t launch_kv_evict_plan(const gdn_kv_pool *p, int layer, const EvictArgs &a, hipStream_t s);
 hipError_t launch_kv_evict_apply(const gdn_kv_pool *p, int layer, const EvictArgs &a, hipStream_t s);
 
-// How an attention call divides the cache: `splits` workgroups of `chunk` tokens (a
-// multiple of the 32-token tile) per request and block of up to 16 query heads.
-struct AttnSplit {
-  int head_blocks, chunk, splits;
-};
-AttnSplit attn_split(const gdn_kv_pool *p, int batch, int q_heads, int max_len);
+// whether the call's blocks of 128 tokens can be counted in 31 bits
+bool attn_fits(const gdn_kv_pool *p, int batch, int q_heads, int max_len);
 size_t attn_workspace(const gdn_kv_pool *p, int batch, int q_heads, int max_len, uint32_t flags);
 
 struct AttnArgs {

@@ -1,5 +1,7 @@
 // kv_cache.hip -- the paged key-value cache's own kernels: append, eviction plan and
 // the moves of an eviction (formulas and rules: include/gdn_kv.h).
+#include <type_traits>
+
 #include "kv.hpp"
 #include "lanes.hpp"
 
@@ -11,9 +13,23 @@ namespace {
 // loads, one store each.  Bound by the bytes (and by the launch for one decode step).
 constexpr int kAppendThreads = 256;
 
+// x / scale rounded to fp32 as a division is, from inv = 1 / scale rounded: two steps of
+// q + (x - q scale) inv leave the correctly rounded quotient (Markstein's division), in
+// half the instructions of the general one, which was the larger part of the e4m3 append.
+// Its remainder is exact while nothing over- or underflows: a quotient beyond 512 (or NaN)
+// is only limited below, one far below 2^-10 only rounds to zero, and the host gives inv = 0
+// (plain division) unless scale lies in [2^-60, 2^60].
+__device__ __forceinline__ float quotient(float x, float scale, float inv) {
+  if (inv == 0.f) return x / scale;  // wave-uniform
+  const float q = x * inv;
+  float r = fmaf(fmaf(-q, scale, x), inv, q);
+  r = fmaf(fmaf(-r, scale, x), inv, r);
+  return fabsf(q) < 512.f ? r : q;
+}
+
 // 8 bf16 values / scale, limited to e4m3's largest value, rounded once to nearest even
 // (the limits keep NaN: both comparisons are false)
-__device__ __forceinline__ u32x2 quantise8(const u32x4 &x, float scale) {
+__device__ __forceinline__ u32x2 quantise8(const u32x4 &x, float scale, float inv) {
   u32x2 r;
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
@@ -21,7 +37,7 @@ __device__ __forceinline__ u32x2 quantise8(const u32x4 &x, float scale) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const uint32_t w = x[2 * p + (e >> 1)];
-      float t = __uint_as_float((e & 1) ? (w & 0xffff0000u) : (w << 16)) / scale;
+      float t = quotient(__uint_as_float((e & 1) ? (w & 0xffff0000u) : (w << 16)), scale, inv);
       t = t > 448.f ? 448.f : t;
       f[e] = t < -448.f ? -448.f : t;
     }
@@ -59,8 +75,8 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(KvGeom g, int
   }
   if (kF8) {
     const int64_t off = int64_t(row) * head_dim + 8 * piece;
-    *reinterpret_cast<u32x2 *>(g.k + off) = quantise8(kx, g.k_scale);
-    *reinterpret_cast<u32x2 *>(g.v + off) = quantise8(vx, g.v_scale);
+    *reinterpret_cast<u32x2 *>(g.k + off) = quantise8(kx, g.k_scale, a.k_inv);
+    *reinterpret_cast<u32x2 *>(g.v + off) = quantise8(vx, g.v_scale, a.v_inv);
   } else {
     const int64_t off = (int64_t(row) * head_dim + 8 * piece) * 2;
     *reinterpret_cast<u32x4 *>(g.k + off) = kx;
@@ -79,59 +95,88 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(KvGeom g, int
 // kept tokens are the `budget` largest keys, ties to the lowest index.
 //
 // The threshold key is found by narrowing a key range [lo, hi]: each round counts the
-// range's keys in up to 2048 equal bins (shared memory), finds the bin that holds the
-// k-th largest and takes it as the next range.  The first range is the smallest and
-// largest unprotected key, so the bins spread over the exponents that occur, and three
-// rounds settle 32 bits.  Then one pass in index order numbers the freed places and the
-// tokens to move by ballots and a scan of the waves' counts.
+// range's keys in up to BINS equal bins (shared memory), finds the bin that holds the
+// k-th largest and takes it as the next range, and stops early where a whole bin is kept.
+// The first range is the smallest and largest weight above 0, so the bins spread over the
+// exponents that occur; a threshold among the weights of 0 is seen at once.
 //
-// Bound by reading mass and pos once: up to kPlanThreads * 32 tokens the keys stay in
-// registers; longer caches read both again in each round (from the caches).
-constexpr int kPlanThreads = 1024;
-constexpr int kPlanWaves = kPlanThreads / 64;
-constexpr int kBins = 2048;
+// Every wave owns a run of adjacent tokens, so the order of the lists needs no barrier per
+// 64 tokens: a wave counts its ties (and then its freed places and tokens to move) by
+// ballots, one sum over the waves gives each its start, and it walks its run again.
+//
+// The keys lie in shared memory (up to 36 * 1024 tokens), so mass and pos are read once; a
+// longer cache reads both again in each pass.  A pass takes U times 64 tokens in a step,
+// all of their keys read before the first is used (the compiler does not unroll loops with
+// ballots by itself); the loads of mass and pos go out kLoads at a time, with no condition
+// between them.
 constexpr uint32_t kProtected = 0xffffffffu;
 
+template <int THREADS, int BINS>
 struct PlanShared {
-  uint32_t bins[kBins];
-  uint32_t wave[2][kPlanWaves];
+  uint32_t bins[BINS];
+  uint32_t wave[4][THREADS / 64];
   uint32_t lo, hi, need, exact;
 };
 
-__device__ __forceinline__ uint32_t wave_add(uint32_t v) {
-  for (int m = 32; m; m >>= 1) v += __shfl_xor(v, m);
+// f over the wave's lanes (commutative), left in every lane: lane permutes in the VALU
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
+  return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), CTRL, 0xF, 0xF, true));
+}
+template <typename F>
+__device__ __forceinline__ uint32_t wave_fold(uint32_t v, F f) {
+  v = f(v, dpp_u32<0xB1>(v));   // quad_perm [1,0,3,2]
+  v = f(v, dpp_u32<0x4E>(v));   // quad_perm [2,3,0,1]
+  v = f(v, dpp_u32<0x141>(v));  // row_half_mirror
+  v = f(v, dpp_u32<0x140>(v));  // row_mirror
+  const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = f(r[0], r[1]);
+  const auto q = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return f(q[0], q[1]);
+}
+// inclusive sum over the lanes in order
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+  v += uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x111, 0xF, 0xF, false));  // row_shr 1
+  v += uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x112, 0xF, 0xF, false));
+  v += uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x114, 0xF, 0xF, false));
+  v += uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x118, 0xF, 0xF, false));
+  v += uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x142, 0xA, 0xF, false));  // row_bcast 15
+  v += uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x143, 0xC, 0xF, false));  // row_bcast 31
   return v;
 }
 
-// exclusive sum of v over the workgroup's threads in thread order, total in *all
-__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *wave, uint32_t *all) {
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  uint32_t inc = v;
-  for (int m = 1; m < 64; m <<= 1) {
-    const uint32_t o = __shfl_up(inc, m);
-    if (lane >= m) inc += o;
-  }
-  __syncthreads();  // the previous use of `wave` is over
-  if (lane == 63) wave[w] = inc;
+// Sum of v over the waves before this one (v wave-uniform); the caller's arrays differ
+// between uses that no barrier parts.
+template <int WAVES>
+__device__ __forceinline__ uint32_t before_wave(uint32_t v, uint32_t *wave) {
+  const int w = threadIdx.x >> 6;
+  if ((threadIdx.x & 63) == 0) wave[w] = v;
   __syncthreads();
-  uint32_t before = 0, total = 0;
-  for (int i = 0; i < kPlanWaves; ++i) {
-    const uint32_t c = wave[i];
-    before += i < w ? c : 0;
-    total += c;
-  }
-  *all = total;
-  return before + inc - v;
+  uint32_t before = 0;
+#pragma unroll
+  for (int i = 0; i < WAVES; ++i) before += i < w ? wave[i] : 0;
+  return before;
 }
 
-// R > 0: up to R * kPlanThreads tokens, keys in registers; R == 0: any number
-template <int R>
-__global__ __launch_bounds__(kPlanThreads) void kv_evict_plan_kernel(KvGeom g, EvictArgs a) {
-  __shared__ PlanShared sh;
+__device__ __forceinline__ uint32_t lanes_below(uint64_t mask) {
+  return __builtin_amdgcn_mbcnt_hi(uint32_t(mask >> 32), __builtin_amdgcn_mbcnt_lo(uint32_t(mask), 0));
+}
+
+// kHeld: the keys of all tokens in dynamic shared memory, a whole number of U * THREADS
+template <int THREADS, bool kHeld, int BINS, int U>
+__global__ __launch_bounds__(THREADS) void kv_evict_plan_kernel(KvGeom g, EvictArgs a) {
+  constexpr int WAVES = THREADS / 64;
+  constexpr int PER = BINS / THREADS;  // bins of a thread
+  constexpr int kBits = BINS == 2048 ? 11 : 10;
+  constexpr int kLoads = THREADS == 256 ? 8 : 16;
+  static_assert(BINS == 1 << kBits, "bins");
+  __shared__ PlanShared<THREADS, BINS> sh;
+  extern __shared__ uint32_t held[];
   const int unit = blockIdx.x;
   const int h = unit % g.kv_heads, lb = unit / g.kv_heads;
   const int b = lb % a.batch, layer = lb / a.batch;
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int slot = a.slot_table[b], n = a.kv_len[b];
   const bool teller = layer == 0 && h == 0 && tid == 0;
   const bool bad_slot = slot <= 0 || slot >= g.slots;
@@ -148,66 +193,93 @@ __global__ __launch_bounds__(kPlanThreads) void kv_evict_plan_kernel(KvGeom g, E
   const int64_t base = ((int64_t(layer) * g.slots + slot) * g.kv_heads + h) * g.capacity;
   const float *mass = g.mass + base;
   const int32_t *pos = g.pos + base;
-  // next_pos - recent may pass the 32-bit range
-  const int64_t from = int64_t(a.next_pos[b]) - a.recent;
-  const int rounds = R > 0 ? R : (n + kPlanThreads - 1) / kPlanThreads;
+  // (next_pos - recent may pass the 32-bit range, downwards)
+  const int32_t from = int32_t(max(int64_t(a.next_pos[b]) - a.recent, int64_t(INT32_MIN)));
+  const int rounds = (n + U * THREADS - 1) / (U * THREADS) * U;  // of 64 tokens, per wave
+  const int first = w * rounds * 64;               // of this wave
 
-  auto load_key = [&](int i) -> uint32_t {
-    const float m = mass[i];
-    const int32_t p = pos[i];
-    const uint32_t key = m > 0.f ? __float_as_uint(m) : 0u;
-    return p < a.sink || int64_t(p) >= from ? kProtected : key;
-  };
-  uint32_t keys[R > 0 ? R : 1];
-  if (R > 0) {
+  // Key of place i.  One behind the last token has key 0 and needs no test in the passes:
+  // it is not below budget, so not freed; it comes after all ties; and a key of 0 is only
+  // ever kept as a tie.
+  auto load_keys = [&](int i0, auto count, uint32_t *out) {
+    constexpr int N = decltype(count)::value;
+    float m[N];
+    int32_t p[N];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int i = r * kPlanThreads + tid;
-      keys[r] = i < n ? load_key(i) : 0u;
+    for (int q = 0; q < N; ++q) {
+      const int at = min(i0 + 64 * q + lane, n - 1);
+      m[q] = mass[at];
+      p[q] = pos[at];
     }
-  }
-  // f(index, key) for this thread's tokens
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+      const uint32_t key = m[q] > 0.f ? __float_as_uint(m[q]) : 0u;
+      const bool safe = (p[q] < a.sink) | (p[q] >= from);
+      out[q] = i0 + 64 * q + lane >= n ? 0u : safe ? kProtected : key;
+    }
+  };
+  // f(first token, key) for this wave's rounds in order
   auto each = [&](auto f) {
-    if constexpr (R > 0) {
+    constexpr int N = kHeld ? U : kLoads;
+    for (int r = 0; r < rounds; r += N) {
+      uint32_t k[N];
+      if constexpr (kHeld) {
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const int i = r * kPlanThreads + tid;
-        if (i < n) f(i, keys[r]);
+        for (int q = 0; q < N; ++q) k[q] = held[first + 64 * (r + q) + lane];
+      } else {
+        load_keys(first + 64 * r, std::integral_constant<int, N>{}, k);
       }
-    } else {
-      for (int i = tid; i < n; i += kPlanThreads) f(i, load_key(i));
+#pragma unroll
+      for (int q = 0; q < N; ++q)
+        if (kHeld || r + q < rounds) f(first + 64 * (r + q), k[q]);
     }
   };
 
-  // ---- range of the unprotected keys, count of the protected ------------------
-  uint32_t kmin = kProtected, kmax = 0, prot = 0;
-  each([&](int, uint32_t key) {
-    if (key == kProtected) {
-      ++prot;
-    } else {
-      kmin = min(kmin, key);
-      kmax = max(kmax, key);
+  // ---- range of the weights above 0, count of them and of the protected ----------
+  // (both ends count from one below: key 0 becomes the largest, the protected key ...fe)
+  uint32_t kmin = kProtected, kmax = 0, prot = 0, some = 0;
+  auto look = [&](uint32_t key) {
+    kmin = min(kmin, key - 1u);
+    kmax = max(kmax, key + 1u);  // the protected key wraps to 0
+    prot += __popcll(__ballot(key == kProtected));
+    some += __popcll(__ballot(key != 0u));
+  };
+  if constexpr (kHeld) {
+    for (int r = 0; r < rounds; r += kLoads) {
+      uint32_t k[kLoads];
+      load_keys(first + 64 * r, std::integral_constant<int, kLoads>{}, k);
+#pragma unroll
+      for (int q = 0; q < kLoads; ++q) {
+        if (r + q < rounds) {
+          held[first + 64 * (r + q) + lane] = k[q];  // read again by this wave only
+          look(k[q]);
+        }
+      }
     }
-  });
-  for (int m = 32; m; m >>= 1) {
-    kmin = min(kmin, __shfl_xor(kmin, m));
-    kmax = max(kmax, __shfl_xor(kmax, m));
+  } else {
+    each([&](int, uint32_t key) { look(key); });
   }
-  prot = wave_add(prot);
-  if (tid == 0) {
-    sh.lo = kProtected;
-    sh.hi = 0;
-    sh.need = 0;
-  }
-  __syncthreads();
+  kmin = wave_fold(kmin, [](uint32_t x, uint32_t y) { return min(x, y); });
+  kmax = wave_fold(kmax, [](uint32_t x, uint32_t y) { return max(x, y); });
   if (lane == 0) {
-    atomicMin(&sh.lo, kmin);
-    atomicMax(&sh.hi, kmax);
-    atomicAdd(&sh.need, prot);
+    sh.wave[0][w] = kmin;
+    sh.wave[1][w] = kmax;
+    sh.wave[2][w] = prot;
+    sh.wave[3][w] = some;
   }
   __syncthreads();
-  uint32_t lo = sh.lo, hi = sh.hi;
-  prot = sh.need;
+  uint32_t lo = kProtected, hi = 0;
+  prot = some = 0;
+#pragma unroll
+  for (int i = 0; i < WAVES; ++i) {
+    lo = min(lo, sh.wave[0][i]);
+    hi = max(hi, sh.wave[1][i]);
+    prot += sh.wave[2][i];
+    some += sh.wave[3][i];
+  }
+  __syncthreads();  // sh.wave is read; it is written again below
+  ++lo;
+  --hi;
   // keep every key above `lo` at the end, and the first `need` of those equal to it;
   // with `exact` every key >= lo
   uint32_t need;
@@ -215,33 +287,43 @@ __global__ __launch_bounds__(kPlanThreads) void kv_evict_plan_kernel(KvGeom g, E
   if (prot >= uint32_t(a.budget)) {  // the protected alone fill the budget
     lo = hi = kProtected;
     need = a.budget;
+  } else if (some < uint32_t(a.budget)) {  // some weights of 0 are kept
+    lo = hi = 0;
+    need = a.budget - some;
   } else {
     need = a.budget - prot;
   }
-  while (lo < hi && !exact) {  // ends: each round leaves at most 1/1024 of the range
-    const uint32_t width = hi - lo;
+  while (lo < hi && !exact) {  // ends: each round leaves at most 2 / BINS of the range
+    const uint32_t width = hi - lo;  // (< 2^31: the largest unprotected key is infinity's)
     const int top = 32 - __clz(width);
-    const int shift = top > 11 ? top - 11 : 0;
-    __syncthreads();
-    for (int i = tid; i < kBins; i += kPlanThreads) sh.bins[i] = 0;
+    const int shift = top > kBits ? top - kBits : 0;
+    // thread t has bins BINS - 1 - PER t downwards: sums from the top
+    const int top_bin = BINS - 1 - PER * tid;
+#pragma unroll
+    for (int q = 0; q < PER; ++q) sh.bins[top_bin - q] = 0;
     __syncthreads();
     each([&](int, uint32_t key) {
-      if (key >= lo && key <= hi) atomicAdd(&sh.bins[(key - lo) >> shift], 1u);
+      const uint32_t d = key - lo;
+      if (d <= width) atomicAdd(&sh.bins[d >> shift], 1u);
     });
     __syncthreads();
-    // thread t looks at bins 2047 - 2t and 2046 - 2t: sums from the top
-    const int b1 = kBins - 1 - 2 * tid, b0 = b1 - 1;
-    const uint32_t c1 = sh.bins[b1], c0 = sh.bins[b0];
-    uint32_t all;
-    const uint32_t above = block_scan(c1 + c0, sh.wave[0], &all);
-    if (above < need && above + c1 + c0 >= need) {
-      const bool second = above + c1 < need;
-      const uint32_t bin = second ? b0 : b1, over = second ? above + c1 : above;
-      const uint32_t in_bin = second ? c0 : c1;
-      sh.lo = lo + (bin << shift);
-      sh.hi = min(hi, sh.lo + ((1u << shift) - 1u));
-      sh.need = need - over;
-      sh.exact = need - over == in_bin;  // the whole bin is kept
+    uint32_t mine = 0, c[PER];
+#pragma unroll
+    for (int q = 0; q < PER; ++q) mine += c[q] = sh.bins[top_bin - q];
+    const uint32_t inc = wave_scan(mine);
+    uint32_t above = before_wave<WAVES>(__builtin_amdgcn_readlane(inc, 63), sh.wave[0]) + inc - mine;
+    if (above < need && above + mine >= need) {
+#pragma unroll
+      for (int q = 0; q < PER; ++q) {
+        if (above < need && above + c[q] >= need) {
+          const uint32_t l = lo + (uint32_t(top_bin - q) << shift);
+          sh.lo = l;
+          sh.hi = min(hi, l + ((1u << shift) - 1u));
+          sh.need = need - above;
+          sh.exact = need - above == c[q];  // the whole bin is kept
+        }
+        above += c[q];
+      }
     }
     __syncthreads();
     lo = sh.lo;
@@ -250,95 +332,136 @@ __global__ __launch_bounds__(kPlanThreads) void kv_evict_plan_kernel(KvGeom g, E
     exact = sh.exact != 0;
   }
 
-  // ---- number the ties, then the freed places and the tokens to move ----------
-  const int64_t list = int64_t(unit) * a.max_moves;
-  uint32_t tie_base = 0, free_base = 0, move_base = 0;
-  for (int r = 0; r < rounds; ++r) {
-    const int i = r * kPlanThreads + tid;
-    uint32_t key = 0;
-    if constexpr (R > 0) {
-#pragma unroll
-      for (int q = 0; q < R; ++q) key = q == r ? keys[q] : key;
-    } else {
-      if (i < n) key = load_key(i);
-    }
-    const bool on = i < n;
-    bool keep = on && (exact ? key >= lo : key > lo);
-    uint32_t all;
-    if (!exact) {
-      const bool tie = on && key == lo;
-      const uint32_t before = block_scan(tie ? 1u : 0u, sh.wave[0], &all);
-      if (tie && tie_base + before < need) keep = true;
-      tie_base += all;
-    }
-    const bool freed = on && !keep && i < a.budget;
-    const bool moved = on && keep && i >= a.budget;
-    const uint32_t before = block_scan((freed ? 1u : 0u) | (moved ? 0x10000u : 0u), sh.wave[1], &all);
-    if (freed) a.moves[2 * (list + free_base + (before & 0xffffu)) + 1] = i;
-    if (moved) a.moves[2 * (list + move_base + (before >> 16))] = i;
-    free_base += all & 0xffffu;
-    move_base += all >> 16;
+  // ---- ties, then freed places and tokens to move ------------------------------
+  uint32_t tie0 = 0;
+  if (!exact) {
+    each([&](int, uint32_t key) { tie0 += __popcll(__ballot(key == lo)); });
+    tie0 = before_wave<WAVES>(tie0, sh.wave[1]);
   }
-  if (tid == 0) a.n_moves[unit] = int(move_base);
+  // kept ones among 64 tokens: keys above lo (with `exact` from lo on) and ties while they
+  // are needed; *ties: how many came before
+  const uint32_t over = exact ? lo - 1u : lo;  // (`exact` only with lo above 0)
+  auto keeps = [&](uint32_t key, uint32_t *ties, auto with_ties) -> uint64_t {
+    uint64_t keep = __ballot(key > over);
+    if constexpr (decltype(with_ties)::value) {
+      const uint64_t equal = __ballot(key == lo);
+      keep |= __ballot(*ties + lanes_below(equal) < need) & equal;
+      *ties += __popcll(equal);
+    }
+    return keep;
+  };
+  auto finish = [&](auto with_ties) {
+    uint32_t freed = 0, moved = 0, ties = tie0;
+    each([&](int i0, uint32_t key) {
+      const uint64_t keep = keeps(key, &ties, with_ties), below = __ballot(lane < a.budget - i0);
+      freed += __popcll(~keep & below);
+      moved += __popcll(keep & ~below);
+    });
+    uint32_t free_at = before_wave<WAVES>(freed, sh.wave[2]);
+    uint32_t move_at = before_wave<WAVES>(moved, sh.wave[3]);
+    if (tid == THREADS - 1) a.n_moves[unit] = int(move_at + moved);
+    int32_t *list = a.moves + 2 * int64_t(unit) * a.max_moves;
+    ties = tie0;
+    each([&](int i0, uint32_t key) {
+      const uint64_t keep = keeps(key, &ties, with_ties), below = __ballot(lane < a.budget - i0);
+      const uint64_t fm = ~keep & below, mm = keep & ~below;
+      if (fm) {
+        if (fm >> lane & 1) list[2 * (free_at + lanes_below(fm)) + 1] = i0 + lane;
+        free_at += __popcll(fm);
+      }
+      if (mm) {
+        if (mm >> lane & 1) list[2 * (move_at + lanes_below(mm))] = i0 + lane;
+        move_at += __popcll(mm);
+      }
+    });
+  };
+  if (exact) finish(std::false_type{});
+  else finish(std::true_type{});
 }
 
 // ---------------------------------------------------------- eviction moves --
-// x: blocks of kMovesPerBlock entries of a list, y: (layer, request, head).  A row is
-// spread over row_bytes / 16 lanes; a thread carries 16 bytes of the key and of the value
-// of each of its entries.  Sources and destinations are disjoint, so there is no order.
+// x: blocks of entries of a (layer, request, head)'s list.  A row is spread over
+// row_bytes / 16 lanes; a thread carries 16 bytes of the key and of the value of kMoveRows
+// entries, all loads issued before the first store.  The rows are looked up once per
+// entry, by one thread each.  Sources and destinations are disjoint, so there is no order.
 constexpr int kMoveThreads = 256;
-constexpr int kMovesPerBlock = 64;
+constexpr int kMoveRows = 4;
 
 __global__ __launch_bounds__(kMoveThreads) void kv_evict_apply_kernel(KvGeom g, int row_bytes, int units,
                                                                       EvictArgs a) {
+  __shared__ int srow[kMoveThreads], drow[kMoveThreads];
   const int unit = blockIdx.x % units, block = blockIdx.x / units;
   const int h = unit % g.kv_heads, lb = unit / g.kv_heads;
   const int b = lb % a.batch, layer = lb / a.batch;
-  const int count = a.n_moves[unit];
+  const int lanes = row_bytes >> 4;                        // per row: 4 .. 32
+  const int entries = kMoveRows * kMoveThreads / lanes;    // of this block: 32 .. 256
+  const int first = block * entries;
+  // (the entry is read beside the count, not after it: max_moves of them are there)
+  const int j = first + threadIdx.x;
+  const int64_t e = 2 * (int64_t(unit) * a.max_moves + min(j, a.max_moves - 1));
+  const int src = a.moves[e], dst = a.moves[e + 1];
+  const int count = a.n_moves[unit], slot = a.slot_table[b];
   const bool teller = block == 0 && threadIdx.x == 0;
   if (count < 0 || count > a.max_moves) {
     if (teller) set_err(g.err, GDN_ERRW_BAD_SEQLENS);
     return;
   }
-  const int first = block * kMovesPerBlock;
   if (first >= count) return;
-  const int slot = a.slot_table[b];
   if (slot <= 0 || slot >= g.slots) {
     if (teller && slot >= g.slots) set_err(g.err, GDN_ERRW_BAD_SLOT);
     return;
   }
-  const int last = min(count, first + kMovesPerBlock);
-  const int lanes = row_bytes >> 4;  // per row
-  const int piece = threadIdx.x % lanes;
+  if (int(threadIdx.x) < entries) {
+    int rs = -1, rd = -1;
+    if (j < count) {
+      if (src < 0 || src >= g.capacity || dst < 0 || dst >= g.capacity) {
+        set_err(g.err, GDN_ERRW_BAD_SEQLENS);
+      } else {
+        rs = kv_row(g, slot, h, src);
+        rd = kv_row(g, slot, h, dst);
+        if (rs < 0 || rd < 0) {
+          set_err(g.err, GDN_ERRW_BAD_PAGE);
+          rs = -1;
+        } else {
+          const int64_t m = ((int64_t(layer) * g.slots + slot) * g.kv_heads + h) * g.capacity;
+          if (g.mass) g.mass[m + dst] = g.mass[m + src];
+          if (g.pos) g.pos[m + dst] = g.pos[m + src];
+        }
+      }
+    }
+    srow[threadIdx.x] = rs;
+    drow[threadIdx.x] = rd;
+  }
+  __syncthreads();
+  const int piece = threadIdx.x % lanes, mine = threadIdx.x / lanes, step = kMoveThreads / lanes;
   char *const k = g.k + int64_t(layer) * g.layer_rows * row_bytes + 16 * piece;
   char *const v = g.v + int64_t(layer) * g.layer_rows * row_bytes + 16 * piece;
-  const int64_t mrow = ((int64_t(layer) * g.slots + slot) * g.kv_heads + h) * g.capacity;
-  for (int j = first + threadIdx.x / lanes; j < last; j += kMoveThreads / lanes) {
-    const int64_t e = 2 * (int64_t(unit) * a.max_moves + j);
-    const int src = a.moves[e], dst = a.moves[e + 1];
-    if (src < 0 || src >= g.capacity || dst < 0 || dst >= g.capacity) {
-      if (piece == 0) set_err(g.err, GDN_ERRW_BAD_SEQLENS);
-      continue;
+  u32x4 kx[kMoveRows], vx[kMoveRows];
+#pragma unroll
+  for (int u = 0; u < kMoveRows; ++u) {
+    const int rs = srow[mine + u * step];
+    if (rs >= 0) {
+      kx[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(k + int64_t(rs) * row_bytes));
+      vx[u] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(v + int64_t(rs) * row_bytes));
     }
-    const int rs = kv_row(g, slot, h, src), rd = kv_row(g, slot, h, dst);
-    if (rs < 0 || rd < 0) {
-      if (piece == 0) set_err(g.err, GDN_ERRW_BAD_PAGE);
-      continue;
-    }
-    const u32x4 kx = *reinterpret_cast<const u32x4 *>(k + int64_t(rs) * row_bytes);
-    const u32x4 vx = *reinterpret_cast<const u32x4 *>(v + int64_t(rs) * row_bytes);
-    *reinterpret_cast<u32x4 *>(k + int64_t(rd) * row_bytes) = kx;
-    *reinterpret_cast<u32x4 *>(v + int64_t(rd) * row_bytes) = vx;
-    if (piece == 0) {
-      if (g.mass) g.mass[mrow + dst] = g.mass[mrow + src];
-      if (g.pos) g.pos[mrow + dst] = g.pos[mrow + src];
+  }
+#pragma unroll
+  for (int u = 0; u < kMoveRows; ++u) {
+    if (srow[mine + u * step] >= 0) {
+      const int64_t rd = drow[mine + u * step];
+      *reinterpret_cast<u32x4 *>(k + rd * row_bytes) = kx[u];
+      *reinterpret_cast<u32x4 *>(v + rd * row_bytes) = vx[u];
     }
   }
 }
 
 }  // namespace
 
-hipError_t launch_kv_append(const gdn_kv_pool *p, int layer, const AppendArgs &a, hipStream_t s) {
+hipError_t launch_kv_append(const gdn_kv_pool *p, int layer, const AppendArgs &args, hipStream_t s) {
+  const auto inverse = [](float x) { return x >= 0x1p-60f && x <= 0x1p60f ? 1.f / x : 0.f; };
+  AppendArgs a = args;
+  a.k_inv = inverse(p->d.k_scale);
+  a.v_inv = inverse(p->d.v_scale);
   const int64_t items = int64_t(a.n) * p->d.kv_heads * (p->d.head_dim >> 3);
   const dim3 grid(unsigned((items + kAppendThreads - 1) / kAppendThreads));
   const KvGeom g = kv_geom(p, layer);
@@ -349,23 +472,28 @@ hipError_t launch_kv_append(const gdn_kv_pool *p, int layer, const AppendArgs &a
   return hipGetLastError();
 }
 
-hipError_t launch_kv_evict_plan(const gdn_kv_pool *p, int layer, const EvictArgs &a, hipStream_t s) {
-  const dim3 grid(unsigned(a.layers * a.batch * p->d.kv_heads)), block(kPlanThreads);
-  const KvGeom g = kv_geom(p, layer);
-  if (a.max_len <= 2 * kPlanThreads)
-    hipLaunchKernelGGL((kv_evict_plan_kernel<2>), grid, block, 0, s, g, a);
-  else if (a.max_len <= 8 * kPlanThreads)
-    hipLaunchKernelGGL((kv_evict_plan_kernel<8>), grid, block, 0, s, g, a);
-  else if (a.max_len <= 32 * kPlanThreads)
-    hipLaunchKernelGGL((kv_evict_plan_kernel<32>), grid, block, 0, s, g, a);
-  else
-    hipLaunchKernelGGL((kv_evict_plan_kernel<0>), grid, block, 0, s, g, a);
+namespace {
+template <int THREADS, bool kHeld, int BINS, int U>
+hipError_t launch_plan(const KvGeom &g, const EvictArgs &a, hipStream_t s) {
+  constexpr int step = U * THREADS;
+  const size_t held = kHeld ? size_t((a.max_len + step - 1) / step) * step * 4 : 0;
+  hipLaunchKernelGGL((kv_evict_plan_kernel<THREADS, kHeld, BINS, U>), dim3(unsigned(a.layers * a.batch * g.kv_heads)),
+                     dim3(THREADS), held, s, g, a);
   return hipGetLastError();
+}
+}  // namespace
+
+hipError_t launch_kv_evict_plan(const gdn_kv_pool *p, int layer, const EvictArgs &a, hipStream_t s) {
+  const KvGeom g = kv_geom(p, layer);
+  if (a.max_len <= 2048) return launch_plan<256, true, 1024, 2>(g, a, s);
+  if (a.max_len <= 36 * 1024) return launch_plan<1024, true, 2048, 4>(g, a, s);
+  return launch_plan<1024, false, 2048, 1>(g, a, s);
 }
 
 hipError_t launch_kv_evict_apply(const gdn_kv_pool *p, int layer, const EvictArgs &a, hipStream_t s) {
   const int units = a.layers * a.batch * p->d.kv_heads;
-  const int64_t blocks = (a.max_moves + kMovesPerBlock - 1) / kMovesPerBlock;
+  const int entries = kMoveRows * kMoveThreads / (p->row_bytes >> 4);
+  const int64_t blocks = (a.max_moves + entries - 1) / entries;
   if (blocks * units >= (int64_t(1) << 31)) return hipErrorInvalidValue;
   hipLaunchKernelGGL(kv_evict_apply_kernel, dim3(unsigned(blocks * units)), dim3(kMoveThreads), 0, s,
                      kv_geom(p, layer), p->row_bytes, units, a);

@@ -275,6 +275,32 @@ def test_append_matches_definition_and_touches_nothing_else(f8, dim, kv_heads, p
     assert int(pool.err_word.item()) == 0
 
 
+@pytest.mark.parametrize("k_scale,v_scale", [(1.0, 1.0 / 3), (0.0123, 7.77), (2.0 ** -9, 1.9999999), (1e-3, 448.0),
+                                             (1e-30, 1e30), (1.17e-38, 3e38), (1e20, 2.0 ** -60)])
+def test_append_divides_every_bf16_value_as_fp32_does(k_scale, v_scale):
+    """All 65536 bf16 values by several scales, against numpy's fp32 division."""
+    import gated_delta_rule_slot_amd as gdn
+
+    bits = torch.arange(65536, dtype=torch.int32)
+    x = (bits << 16).view(torch.float32).to(torch.bfloat16).view(512, 1, 128)
+    pages, S = 33, 16
+    k = torch.zeros(1, pages, 1, S, 128, dtype=torch.float8_e4m3fn, device="cuda")
+    v = torch.zeros_like(k)
+    table = torch.zeros(2, 32, dtype=torch.int32)
+    table[1] = torch.arange(32) + 1
+    pool = gdn.kv_pool_create(k, v, table.cuda(), k_scale=k_scale, v_scale=v_scale)
+    at = torch.arange(512, dtype=torch.int32).cuda()
+    gdn.kv_append(pool, 0, torch.ones(512, dtype=torch.int32).cuda(), at, x.cuda(), x.cuda())
+    xf = x.float().numpy().reshape(-1)
+    for t, s in ((k, k_scale), (v, v_scale)):
+        with np.errstate(over="ignore", invalid="ignore"):
+            want = kv_ops.e4m3_round((xf / np.float32(s)).astype(np.float64))
+        got = t[0, 1:].float().cpu().double().numpy().reshape(-1)
+        nan = np.isnan(want)
+        assert np.array_equal(np.isnan(got), nan)
+        assert np.array_equal(got[~nan], want[~nan])
+
+
 def test_append_skips_and_flags():
     import gated_delta_rule_slot_amd as gdn
 
