@@ -53,7 +53,7 @@ struct AttnDev {
   int head_blocks, group, workers;
   int join;         // whether the joining kernel runs (else every unit is one block at most)
   int64_t lpad;     // row length of the score array
-  int32_t *pre;     // [batch + 1] blocks of the requests before each, per head and head block
+  int32_t *unit;    // [units][2]: first and last worker of a unit, 2 w + (its first unit: 0, later: 1)
   float *o;         // [workers][2][16][D]: O of a worker's first and of its last unit
   float *ml;        // [workers][2][16][2]: their m and l
   float *done;      // [batch][q_heads][2]: m and l of units within one worker; with weights
@@ -65,31 +65,45 @@ struct AttnDev {
 struct Seen {
   int slot, begin, len, blocks;
 };
+__device__ __forceinline__ int blocks_of(const KvGeom &g, const AttnArgs &a, const Seen &r) {
+  const bool ok = r.slot > 0 && r.slot < g.slots && r.len <= a.max_len && r.begin >= 0 && r.begin < r.len;
+  return ok ? (r.len - (r.begin & ~(kTile - 1)) + kBlock - 1) / kBlock : 0;
+}
 __device__ __forceinline__ Seen seen_by(const KvGeom &g, const AttnArgs &a, int b, bool tell) {
   Seen r;
   r.slot = a.slot_table[b];
   r.len = a.kv_len[b];
   r.begin = a.kv_begin ? a.kv_begin[b] : 0;
-  r.blocks = 0;
-  if (r.slot <= 0 || r.slot >= g.slots) {
-    if (tell && r.slot >= g.slots) set_err(g.err, GDN_ERRW_BAD_SLOT);
-  } else if (r.len < 0 || r.len > a.max_len || r.begin < 0) {
-    if (tell) set_err(g.err, GDN_ERRW_BAD_SEQLENS);
-  } else if (r.begin < r.len) {
-    r.blocks = (r.len - (r.begin & ~(kTile - 1)) + kBlock - 1) / kBlock;
+  r.blocks = blocks_of(g, a, r);
+  if (tell) {
+    if (r.slot >= g.slots) set_err(g.err, GDN_ERRW_BAD_SLOT);
+    else if (r.slot > 0 && (r.len < 0 || r.len > a.max_len || r.begin < 0)) set_err(g.err, GDN_ERRW_BAD_SEQLENS);
   }
   return r;
 }
 
-// First block of worker w, and the worker that holds block x: floor(w all / workers) is the
-// first, so the holder is the largest w with w all < (x + 1) workers.
-// (The host keeps the number of blocks below 2^31.)
+// First block of worker w.  (The host keeps the number of blocks below 2^31.)
 __device__ __forceinline__ int first_block(int w, int all, int workers) { return int(int64_t(w) * all / workers); }
-__device__ __forceinline__ int worker_of(int x, int all, int workers) {
-  return int(((int64_t(x) + 1) * workers - 1) / all);
-}
 // A value that is the same in every lane, as a scalar.
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// Workgroup barrier that orders shared memory only: global loads issued before it stay in
+// flight.
+__device__ __forceinline__ void local_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+// inclusive sum over the lanes in order
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr 1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast 15
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast 31
+  return v;
+}
 
 // max / sum over the four 16-lane groups (same head), left in every lane
 __device__ __forceinline__ float rows_max(float v) {
@@ -126,6 +140,9 @@ struct Lay<D, false> {
   static __device__ __forceinline__ int vdim(int i, int c) {
     return D == 64 ? 4 * c + i : 128 * (i >> 3) + 8 * c + (i & 7);
   }
+  // the inverse, for d a multiple of 4: d .. d + 3 are columns vi(d) .. vi(d) + 3 of lane vc(d)
+  static __device__ __forceinline__ int vi(int d) { return D == 64 ? 0 : 8 * (d >> 7) + (d & 7); }
+  static __device__ __forceinline__ int vc(int d) { return D == 64 ? d >> 2 : (d >> 3) & 15; }
 };
 template <int D>
 struct Lay<D, true> {
@@ -135,6 +152,8 @@ struct Lay<D, true> {
   static constexpr int kVWords = D / 64;
   static __device__ __forceinline__ int kdim(int s, int g) { return 64 * (s >> 1) + 16 * g + 8 * (s & 1); }
   static __device__ __forceinline__ int vdim(int i, int c) { return (D / 16) * c + i; }
+  static __device__ __forceinline__ int vi(int d) { return d % (D / 16); }
+  static __device__ __forceinline__ int vc(int d) { return d / (D / 16); }
 };
 
 template <int W>
@@ -167,7 +186,12 @@ __device__ __forceinline__ void f8_to_bf16(u32 x, u32 *lo, u32 *hi) {
 
 // kWide: pages hold whole tiles (page_size >= 32), so a tile's rows are adjacent and its
 // one page id is wave-uniform; otherwise each token's row is looked up.
-template <int D, bool kF8, bool kWide, bool kMass>
+//
+// The keys and values of a wave's next tile are asked for while the present one is worked
+// on, also over the end of a unit: under load a dependent read takes 5 us and more, so a
+// unit that began with its own reads of queries, page ids and keys cost about 8 us each time.
+// kMass: scores are stored for the weights, 1: of up to 8 heads, 2: of up to 16.
+template <int D, bool kF8, bool kWide, int kMass>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2)))
 void attn_decode_kernel(KvGeom g, AttnDev p) {
   using L = Lay<D, kF8>;
@@ -175,101 +199,81 @@ void attn_decode_kernel(KvGeom g, AttnDev p) {
   constexpr int NO = D / 16;        // 16-column tiles of O
   constexpr int VW = D / 32;        // bf16 words of a lane's columns of one token
   constexpr int RB = D * L::kSize;  // bytes of a row
+  // O in shared memory, per wave: 16 bytes (o[i]) of each lane, for each i; a step of 4 floats
+  // between the lane groups and an odd one (in 16 bytes) between the i keep the banks apart
+  constexpr int kOi = 69 * 4, kSlab = NO * kOi;
+  // scores of a tile there, by head (36 floats apart for the banks), and how many tiles fit
+  constexpr int kScoreRow = 36, kScoreTile = 8 * (kMass ? kMass : 1) * kScoreRow, kStaged = kSlab / kScoreTile;
   // head dim 256: the queries stay in shared memory (their 32 registers would spill)
   constexpr bool kQShared = D == 256;
+  constexpr int kQLoads = kQShared ? KS / kWaves : KS;
   extern __shared__ __attribute__((aligned(16))) float lds[];
   __shared__ float sm[kWaves][16], sl[kWaves][16];
   __shared__ u32x4 sq[kQShared ? KS : 1][64];
 
-  __shared__ int spre[kThreads];
-  __shared__ int sfound[2 + kWaves];
-
-  const int lane = threadIdx.x & 63;
+  const int lane = threadIdx.x & 63, c = lane & 15, gr = lane >> 4;
   const int wave = uniform(threadIdx.x >> 6);
   const int worker = blockIdx.x;
   const int units = g.kv_heads * p.head_blocks;  // of a request
 
-  // ---- this worker's run of blocks ---------------------------------------------
-  // scan(base): spre[i] = blocks of requests base .. base + i, returns their sum
+  // (constant address space: these arrays do not change during the call, so wave-uniform
+  // reads are scalar loads, which the waits for keys and values do not count)
+  typedef const int32_t __attribute__((address_space(4))) *table_t;
+  auto request = [&](int r) -> Seen {
+    AttnArgs a = p.a;
+    Seen v;
+    v.slot = ((table_t)a.slot_table)[r];
+    v.len = ((table_t)a.kv_len)[r];
+    v.begin = a.kv_begin ? ((table_t)a.kv_begin)[r] : 0;
+    v.blocks = blocks_of(g, a, v);
+    return v;
+  };
+
+  // ---- this worker's run of blocks, by each wave for itself: lane i has four requests ----
+  int count[4], inc = 0;
   auto scan = [&](int base) -> int {
-    const int r = base + int(threadIdx.x);
-    int inc = r < p.a.batch ? seen_by(g, p.a, r, false).blocks : 0;
-    for (int d = 1; d < 64; d <<= 1) {
-      const int o = __shfl_up(inc, d);
-      if (lane >= d) inc += o;
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = base + 4 * lane + i;
+      count[i] = r < p.a.batch ? seen_by(g, p.a, r, false).blocks : 0;
+      mine += count[i];
     }
-    __syncthreads();  // the previous use of the shared sums is over
-    if (lane == 63) sfound[2 + wave] = inc;
-    __syncthreads();
-    for (int w = 0; w < wave; ++w) inc += sfound[2 + w];
-    spre[threadIdx.x] = inc;
-    __syncthreads();
-    return uniform(spre[kThreads - 1]);
+    inc = wave_scan(mine);
+    const int sum = __builtin_amdgcn_readlane(inc, 63);
+    inc -= mine;  // of the lanes before
+    return sum;
   };
   int all = 0;
-  for (int base = 0; base < p.a.batch; base += kThreads) {
-    const int sum = scan(base);
-    if (p.join && worker == 0 && base + int(threadIdx.x) < p.a.batch)
-      p.pre[base + threadIdx.x + 1] = all + spre[threadIdx.x];
-    all += sum;
-  }
-  if (p.join && worker == 0 && threadIdx.x == 0) p.pre[0] = 0;
+  for (int base = 0; base < p.a.batch; base += 256) all += scan(base);
+  const int last_sum = all;  // of the only step, if the batch fits one
   all *= units;
   const int sharing = min(p.workers, all);  // so that no worker between two others has nothing
   const int run_first = worker < sharing ? first_block(worker, all, sharing) : 0;
   int left = worker < sharing ? first_block(worker + 1, all, sharing) - run_first : 0;
-  int b = 0;       // request, unit within it and block within the unit
-  int unit = 0, blk = 0;
-  Seen rq{0, 0, 0, 0};
-  auto request = [&](int r) -> Seen {
-    const Seen v = seen_by(g, p.a, r, false);
-    return Seen{uniform(v.slot), uniform(v.begin), uniform(v.len), uniform(v.blocks)};
+
+  // A unit's part of the run: request b, key-value head h, query heads q0 .. q0 + heads - 1,
+  // tokens first .. last - 1.
+  struct Part {
+    int b, unit, blk, nblk;
+    Seen rq;
+    int h, heads, q0, first, last;
   };
-  if (left > 0) {
-    const int x = run_first / units;
-    int before = 0;
-    for (int base = 0; base < p.a.batch; base += kThreads) {
-      const int sum = p.a.batch > kThreads ? scan(base) : uniform(spre[kThreads - 1]);
-      if (x < before + sum) {
-        const int lo = before + (threadIdx.x ? spre[threadIdx.x - 1] : 0), hi = before + spre[threadIdx.x];
-        if (lo <= x && x < hi) {
-          sfound[0] = base + threadIdx.x;
-          sfound[1] = lo;
-        }
-        break;
-      }
-      before += sum;
-    }
-    __syncthreads();
-    b = uniform(sfound[0]);
-    rq = request(b);
-    const int in_request = run_first - uniform(sfound[1]) * units;
-    unit = in_request / rq.blocks;
-    blk = in_request - unit * rq.blocks;
-  }
-
-  bool first_unit = true;
-  while (left > 0) {
-    // (made anew for each unit: addresses that depend on the lane alone would otherwise be
-    // kept in registers across all units, 20 of them)
-    int lane_now = threadIdx.x & 63;
-    asm volatile("" : "+v"(lane_now));
-    const int lane = lane_now, c = lane & 15, gr = lane >> 4;
-    const int nblk = min(rq.blocks - blk, left);
-    const int h = unit / p.head_blocks, hb = unit - h * p.head_blocks;
-    const int slot = rq.slot, begin = rq.begin;
-    const int first = (begin & ~(kTile - 1)) + blk * kBlock;
-    const int last = min(rq.len, first + nblk * kBlock);
-    const bool whole_unit = nblk == rq.blocks;
-    const int heads = min(16, p.group - 16 * hb);           // query heads of this unit
-    const int q0 = h * p.group + 16 * hb;                   // the first of them
-    const int64_t qrow = int64_t(b) * p.a.q_heads + q0;
-
-  // (constant address space: the table does not change during the call, so a wave-uniform
-  // read of it is a scalar load, which the waits for keys and values do not count)
-  typedef const int32_t __attribute__((address_space(4))) *table_t;
-  const table_t table = (table_t)(g.page_table + int64_t(slot) * g.max_pages);
-  const int in_page = (1 << g.page_shift) - 1;
+  auto part = [&](int b, int unit, int blk, const Seen &rq, int most) -> Part {
+    Part r;
+    r.b = b;
+    r.unit = unit;
+    r.blk = blk;
+    r.rq = rq;
+    r.nblk = min(rq.blocks - blk, most);
+    r.h = unit / p.head_blocks;
+    const int hb = unit - r.h * p.head_blocks;
+    r.heads = min(16, p.group - 16 * hb);
+    r.q0 = r.h * p.group + 16 * hb;
+    r.first = (rq.begin & ~(kTile - 1)) + blk * kBlock;
+    r.last = min(rq.len, r.first + r.nblk * kBlock);
+    return r;
+  };
 
   // Rows of a tile.  A token that is not visible, or whose page id is not a page, reads
   // page 0's rows (always there) and is masked by its bit of `seen`.
@@ -277,25 +281,27 @@ void attn_decode_kernel(KvGeom g, AttnDev p) {
     int row;   // kWide: first row of the tile; else lane i < 32: row of token t0 + i
     u32 seen;
   };
-  // The page ids are loaded two tiles ahead, before the keys and values of the next tile:
-  // loads return in order, so waiting for an id that was asked for after them would wait for
-  // them too.
-  auto ask = [&](int t0) -> int {
-    if constexpr (kWide) return table[min(t0, last - 1) >> g.page_shift];
-    else return table[max(begin, min(t0 + (lane & 31), last - 1)) >> g.page_shift];
+  const int in_page = (1 << g.page_shift) - 1;
+  // The page ids are asked for a tile before their rows are (and, where the reads are not
+  // scalar, before that tile's keys: loads return in order).
+  auto ask = [&](const Part &u, int t0) -> int {
+    const table_t table = (table_t)(g.page_table + int64_t(u.rq.slot) * g.max_pages);
+    if constexpr (kWide) return table[max(0, min(t0, u.last - 1)) >> g.page_shift];
+    else return table[max(0, max(u.rq.begin, min(t0 + (lane & 31), u.last - 1))) >> g.page_shift];
   };
-  auto resolve = [&](int t0, int page) -> Rows {
+  auto resolve = [&](int h, int begin, int last, int t0, int page) -> Rows {
     Rows r;
     if constexpr (kWide) {
       const bool ok = page > 0 && page < g.pages;
       if (!ok && t0 < last) {
         if (lane == 0) set_err(g.err, GDN_ERRW_BAD_PAGE);
       }
-      r.row = ok ? ((page * g.kv_heads + h) << g.page_shift) + (t0 & in_page) : 0;
+      const bool use = ok && t0 < last;
+      r.row = use ? ((page * g.kv_heads + h) << g.page_shift) + (t0 & in_page) : 0;
       // bits from begin on, and below last
-      u32 m = ok ? 0xffffffffu : 0u;
+      u32 m = use ? 0xffffffffu : 0u;
       if (begin > t0) m &= begin - t0 >= 32 ? 0u : 0xffffffffu << (begin - t0);
-      if (last - t0 < 32) m &= last > t0 ? (1u << (last - t0)) - 1u : 0u;
+      if (use && last - t0 < 32) m &= (1u << (last - t0)) - 1u;
       r.seen = m;
     } else {
       const int t = t0 + (lane & 31);
@@ -312,242 +318,334 @@ void attn_decode_kernel(KvGeom g, AttnDev p) {
 
   Words<4> kw[2][L::kPieces];
   Words<L::kVWords> vw[8][L::kVPieces];
-  const u32 k_off = u32(c * RB + 16 * gr), v_off = u32(4 * gr * RB + 4 * L::kVWords * c);
+  // (lane offsets are made anew for each use: held, they cost the last registers of head dim
+  // 256, and a spilled one is read back in order behind the keys that were just asked for)
+  auto lane_anew = []() -> int {
+    int v = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0));
+    asm volatile("" : "+v"(v));
+    return v;
+  };
   auto load_k = [&](const Rows &r) {
     const char *tile = g.k + int64_t(r.row) * RB;
+    const int ln = lane_anew();
+    const u32 k_off = u32((ln & 15) * RB + 16 * (ln >> 4));
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const char *at;
       if constexpr (kWide) at = tile + 16 * u * RB + k_off;
-      else at = g.k + int64_t(__shfl(r.row, 16 * u + c)) * RB + 16 * gr;
+      else at = g.k + int64_t(__shfl(r.row, 16 * u + (ln & 15))) * RB + 16 * (ln >> 4);
 #pragma unroll
       for (int s = 0; s < L::kPieces; ++s) kw[u][s] = load_words<4>(at + 64 * s);
     }
   };
   auto load_v = [&](const Rows &r) {
     const char *tile = g.v + int64_t(r.row) * RB;
+    const int ln = lane_anew();
+    const u32 v_off = u32(4 * (ln >> 4) * RB + 4 * L::kVWords * (ln & 15));
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const char *at;
       if constexpr (kWide) at = tile + pk(0, e) * RB + v_off;
-      else at = g.v + int64_t(__shfl(r.row, pk(gr, e))) * RB + 4 * L::kVWords * c;
+      else at = g.v + int64_t(__shfl(r.row, pk(ln >> 4, e))) * RB + 4 * L::kVWords * (ln & 15);
 #pragma unroll
       for (int s = 0; s < L::kVPieces; ++s) vw[e][s] = load_words<L::kVWords>(at + 256 * s);
     }
   };
-
-  // Queries as the B operand (columns past the group are zero), asked for before the first
-  // keys for the same reason.
-  constexpr int kQLoads = kQShared ? KS / kWaves : KS;
-  bf16x8 qf[kQLoads];
-  {
-    const uint16_t *q = p.a.q + int64_t(b) * p.a.q_stride + int64_t(q0 + min(c, heads - 1)) * D;
+  // queries as the B operand (columns past the group are zero)
+  auto load_q = [&](const Part &u, bf16x8 *qf) {
+    const uint16_t *q = p.a.q + int64_t(u.b) * p.a.q_stride + int64_t(u.q0 + min(c, u.heads - 1)) * D;
 #pragma unroll
     for (int i = 0; i < kQLoads; ++i)
       qf[i] = *reinterpret_cast<const bf16x8 *>(q + L::kdim(kQShared ? wave * kQLoads + i : i, gr));
-  }
-  __builtin_amdgcn_sched_barrier(0);
+  };
 
-  constexpr int kStep = kTile * kWaves;
-  int t0 = first + kTile * wave;
-  Rows now{0, 0}, next{0, 0};
-  {
-    const int p0 = ask(t0), p1 = ask(t0 + kStep);
-    now = resolve(t0, p0);
-    if (t0 < last) {
+  constexpr int kStep = kBlock;
+  const float to_log2 = p.a.scale * g.k_scale * kLog2e;
+  if (left > 0) {
+    // ---- find the run's first block -----------------------------------------------
+    const int x = run_first / units;
+    int b = 0, lo = 0;
+    for (int base = 0; base < p.a.batch; base += 256) {
+      const int sum = p.a.batch > 256 ? scan(base) : last_sum;
+      if (x < lo + sum) {
+        // the last lane whose requests begin at or before x, and of its four the holder
+        const int at = 63 - __clzll(__ballot(lo + inc <= x));
+        b = base + 4 * at;
+        lo += __builtin_amdgcn_readlane(inc, at);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          const int n = __builtin_amdgcn_readlane(count[i], at);
+          if (b == base + 4 * at + i && x >= lo + n) {
+            lo += n;
+            ++b;
+          }
+        }
+        break;
+      }
+      lo += sum;
+    }
+    Seen rq = request(b);
+    const int in_request = run_first - lo * units;
+    const int unit0 = in_request / rq.blocks;
+    Part cur = part(b, unit0, in_request - unit0 * rq.blocks, rq, left);
+
+    bf16x8 qf[kQLoads];
+    load_q(cur, qf);
+    __builtin_amdgcn_sched_barrier(0);
+    int t0 = cur.first + kTile * wave;
+    int page1;
+    Rows now;
+    {
+      const int page0 = ask(cur, t0);
+      page1 = ask(cur, t0 + kStep);
+      now = resolve(cur.h, cur.rq.begin, cur.last, t0, page0);
       load_k(now);
       load_v(now);
     }
-    next = resolve(t0 + kStep, p1);
-  }
-
-  __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_sched_barrier(0);
+    bool first_unit = true;
+    while (true) {
+      if constexpr (kQShared) {
 #pragma unroll
-  for (int i = 0; i < kQLoads; ++i) {
-    if (c >= heads) qf[i] = bf16x8{};
-    if constexpr (kQShared) sq[wave * kQLoads + i][lane] = __builtin_bit_cast(u32x4, qf[i]);
-  }
-  if constexpr (kQShared) __syncthreads();
-  const float to_log2 = p.a.scale * g.k_scale * kLog2e;
-
-  f32x4 o[NO];
+        for (int i = 0; i < kQLoads; ++i) {
+          if (c >= cur.heads) qf[i] = bf16x8{};
+          sq[wave * kQLoads + i][lane] = __builtin_bit_cast(u32x4, qf[i]);
+        }
+        local_barrier();
+      } else {
 #pragma unroll
-  for (int i = 0; i < NO; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  float m = kNegInf, l = 0.f;
+        for (int i = 0; i < kQLoads; ++i)
+          if (c >= cur.heads) qf[i] = bf16x8{};
+      }
+      // ---- the part after this one (or this one again, unused), its queries and pages -------
+      left -= cur.nblk;
+      Part nx = cur;
+      if (left > 0) {
+        int nb = cur.b, nu = cur.unit + 1;
+        Seen nr = cur.rq;
+        if (nu == units) {
+          nu = 0;
+          do nr = request(++nb);
+          while (nr.blocks == 0 && nb + 1 < p.a.batch);
+        }
+        nx = part(nb, nu, 0, nr, left);
+      }
+      const int nx_last = left > 0 ? nx.last : 0;
+      const int nt0 = nx.first + kTile * wave;
+      bf16x8 qn[kQLoads];
+      load_q(nx, qn);
+      const int npage0 = ask(nx, nt0), npage1 = ask(nx, nt0 + kStep);
 
-  // One tile.  The last one of a wave is a body of its own: loads under a condition would
-  // make every wait of the loop assume that they were not issued, and wait for all.
-  auto tile = [&](auto more_c) {
-    constexpr bool more = decltype(more_c)::value;
-    const int page2 = more ? ask(t0 + 2 * kStep) : 0;
+      f32x4 o[NO];
+#pragma unroll
+      for (int i = 0; i < NO; ++i) o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      float m = kNegInf, l = 0.f;
+      int staged = 0;  // tiles whose scores are in shared memory
+      const int64_t qrow = int64_t(cur.b) * p.a.q_heads + cur.q0;
 
-    // ---- scores ----------------------------------------------------------
-    f32x4 s[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+      // ---- tiles ------------------------------------------------------------------
+      // (a wave without a tile in this part takes one in which no token is seen: one place
+      // in the code asks for keys and values, so their registers are never copied)
+      {
+        bool inside;  // the wave's next tile is of this part
+        do {
+          inside = t0 + kStep < cur.last;
+          const int lane = lane_anew(), c = lane & 15, gr = lane >> 4;
+          const Rows next = resolve(inside ? cur.h : nx.h, inside ? cur.rq.begin : nx.rq.begin,
+                                    inside ? cur.last : nx_last, inside ? t0 + kStep : nt0, inside ? page1 : npage0);
+          // scores
+          f32x4 s[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
-    for (int st = 0; st < KS; ++st) {
-      bf16x8 qv;
-      if constexpr (kQShared) qv = __builtin_bit_cast(bf16x8, sq[st][lane]);
-      else qv = qf[st];
+          for (int st = 0; st < KS; ++st) {
+            bf16x8 qv;
+            if constexpr (kQShared) qv = __builtin_bit_cast(bf16x8, sq[st][lane]);
+            else qv = qf[st];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        u32x4 w;
-        if constexpr (kF8) {
-          const u32 x0 = kw[u][st >> 1].w[2 * (st & 1)], x1 = kw[u][st >> 1].w[2 * (st & 1) + 1];
-          u32 a0, a1, a2, a3;
-          f8_to_bf16(x0, &a0, &a1);
-          f8_to_bf16(x1, &a2, &a3);
-          w = u32x4{a0, a1, a2, a3};
+            for (int u = 0; u < 2; ++u) {
+              u32x4 w;
+              if constexpr (kF8) {
+                const u32 x0 = kw[u][st >> 1].w[2 * (st & 1)], x1 = kw[u][st >> 1].w[2 * (st & 1) + 1];
+                u32 a0, a1, a2, a3;
+                f8_to_bf16(x0, &a0, &a1);
+                f8_to_bf16(x1, &a2, &a3);
+                w = u32x4{a0, a1, a2, a3};
+              } else {
+                w = u32x4{kw[u][st].w[0], kw[u][st].w[1], kw[u][st].w[2], kw[u][st].w[3]};
+              }
+              s[u] = mfma_bf16(__builtin_bit_cast(bf16x8, w), qv, s[u]);
+            }
+          }
+          // (the barriers keep the next tile's loads behind the last use of their registers)
+          __builtin_amdgcn_sched_barrier(0);
+          page1 = inside ? ask(cur, t0 + 2 * kStep) : npage1;
+          load_k(next);
+          __builtin_amdgcn_sched_barrier(0);
+
+          // softmax
+          float x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = s[e >> 2][e & 3] * to_log2;
+          const u32 seen = now.seen;
+          const bool whole = seen == 0xffffffffu;
+          if (!whole) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = (seen >> pk(gr, e)) & 1 ? x[e] : kNegInf;
+          }
+          float mx =
+              fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+          mx = fmaxf(rows_max(mx), m);
+          if (__any(mx > m)) {  // some head's maximum grew
+            const float f = factor(m, mx);
+            l *= f;
+#pragma unroll
+            for (int i = 0; i < NO; ++i) o[i] *= f;
+            m = mx;
+          }
+          float pr[8];
+          const float base = ref(m);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            pr[e] = fexp2(x[e] - base);
+            l += pr[e];
+          }
+          const Split ps = split8(pr);
+
+          // values: columns of eight tokens by byte permutes
+          if (!whole) {  // never 0 * inf
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const bool on = (seen >> pk(gr, e)) & 1;
+#pragma unroll
+              for (int q = 0; q < L::kVPieces; ++q)
+#pragma unroll
+                for (int w = 0; w < L::kVWords; ++w) vw[e][q].w[w] = on ? vw[e][q].w[w] : 0u;
+            }
+          }
+#pragma unroll
+          for (int w = 0; w < VW; ++w) {
+            u32 word[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              if constexpr (kF8) {
+                u32 lo8, hi8;
+                f8_to_bf16(vw[e][0].w[w >> 1], &lo8, &hi8);
+                word[e] = (w & 1) ? hi8 : lo8;
+              } else {
+                word[e] = vw[e][w / L::kVWords].w[w % L::kVWords];
+              }
+            }
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              const u32x4 col = {halves(word[0], word[1], hf), halves(word[2], word[3], hf),
+                                 halves(word[4], word[5], hf), halves(word[6], word[7], hf)};
+              const bf16x8 av = __builtin_bit_cast(bf16x8, col);
+              o[2 * w + hf] = mfma_bf16(av, ps.lo, o[2 * w + hf]);
+              o[2 * w + hf] = mfma_bf16(av, ps.hi, o[2 * w + hf]);
+            }
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          load_v(next);
+          __builtin_amdgcn_sched_barrier(0);
+          // Scores for the weights: kept in the wave's part of the shared memory that O takes
+          // at the end, and stored to memory some tiles at a time.  (Stores count in order with
+          // the loads and take longer: one in every tile, wherever it stood, cost 15 of 120 us
+          // for 128 requests of 2100 tokens.)
+          if constexpr (kMass != 0) {
+            f32x4 lo4 = {x[0], x[1], x[2], x[3]}, hi4 = {x[4], x[5], x[6], x[7]};
+            const int head = kMass == 1 ? c & 7 : c;
+            float *const own = lds + wave * kSlab + head * kScoreRow + 4 * gr + (kMass == 1 ? 2 * (c & 8) : 0);
+            if constexpr (kMass == 1) {  // up to 8 heads: lanes 8 up of 16 take the second half
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float r = dpp_mov<0x128>(hi4[e]);  // row_ror 8
+                lo4[e] = c < 8 ? lo4[e] : r;
+              }
+              st4(own + staged * kScoreTile, lo4);
+            } else {
+              st4(own + staged * kScoreTile, lo4);
+              st4(own + staged * kScoreTile + 16, hi4);
+            }
+            ++staged;
+            if (staged == kStaged || !inside) {
+              if (head < cur.heads) {
+                float *at = p.scores + (qrow + head) * p.lpad + (t0 - (staged - 1) * kStep) + 4 * gr +
+                            (kMass == 1 ? 2 * (c & 8) : 0);
+                // (the one tile of a wave without tokens in this part stays out)
+                for (int k = 0; k < staged && t0 < cur.last; ++k) {
+                  st4(at + k * kStep, ld4(own + k * kScoreTile));
+                  if constexpr (kMass == 2) st4(at + k * kStep + 16, ld4(own + k * kScoreTile + 16));
+                }
+              }
+              staged = 0;
+            }
+          }
+          now = next;
+          t0 += kStep;
+        } while (inside);
+      }
+
+      // ---- join the waves: o[i][j] is column vdim(i, 4 gr + j) of head c ------------------
+      const int lane = lane_anew(), c = lane & 15, gr = lane >> 4, tid = 64 * wave + lane;
+      l = rows_sum(l);
+      if (gr == 0) {
+        sm[wave][c] = m;
+        sl[wave][c] = l;
+      }
+      {
+        float *at = lds + wave * kSlab + 4 * (lane + gr);
+#pragma unroll
+        for (int i = 0; i < NO; ++i) st4(at + i * kOi, o[i]);
+      }
+      local_barrier();
+      const bool whole_unit = cur.nblk == cur.rq.blocks;
+      const int side = first_unit ? 0 : 1;
+      for (int i = tid; i < cur.heads * (D / 4); i += kThreads) {
+        const int hd = i / (D / 4), d = 4 * (i % (D / 4));
+        float mh = sm[0][hd], lt = 0.f;
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) mh = fmaxf(mh, sm[w][hd]);
+        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+        const int r = L::vc(d);  // row r & 3 of lane group r / 4
+        const float *at = lds + L::vi(d) * kOi + 4 * (17 * (r >> 2) + hd) + (r & 3);
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+          const float f = factor(sm[w][hd], mh);
+          lt = fmaf(sl[w][hd], f, lt);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum[e] = fmaf(at[w * kSlab + e * kOi], f, sum[e]);
+        }
+        if (!whole_unit) {
+          const int64_t row = (int64_t(worker) * 2 + side) * 16 + hd;
+          st4(p.o + row * D + d, sum);
+          if (d == 0) {
+            p.ml[2 * row] = mh;
+            p.ml[2 * row + 1] = lt;
+          }
         } else {
-          w = u32x4{kw[u][st].w[0], kw[u][st].w[1], kw[u][st].w[2], kw[u][st].w[3]};
-        }
-        s[u] = mfma_bf16(__builtin_bit_cast(bf16x8, w), qv, s[u]);
-      }
-    }
-    // (the barriers keep the next tile's loads behind the last use of their registers)
-    __builtin_amdgcn_sched_barrier(0);
-    if constexpr (more) load_k(next);
-    __builtin_amdgcn_sched_barrier(0);
-
-    // ---- softmax ---------------------------------------------------------
-    float x[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = s[e >> 2][e & 3] * to_log2;
-    const u32 seen = now.seen;
-    const bool whole = seen == 0xffffffffu;
-    if (!whole) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = (seen >> pk(gr, e)) & 1 ? x[e] : kNegInf;
-    }
-    if (kMass && c < heads) {
-      float *at = p.scores + (qrow + c) * p.lpad + t0 + 4 * gr;
-      st4(at, f32x4{x[0], x[1], x[2], x[3]});
-      st4(at + 16, f32x4{x[4], x[5], x[6], x[7]});
-    }
-    float mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-    mx = fmaxf(rows_max(mx), m);
-    if (__any(mx > m)) {  // some head's maximum grew
-      const float f = factor(m, mx);
-      l *= f;
-#pragma unroll
-      for (int i = 0; i < NO; ++i) o[i] *= f;
-      m = mx;
-    }
-    float pr[8];
-    const float base = ref(m);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      pr[e] = fexp2(x[e] - base);
-      l += pr[e];
-    }
-    const Split ps = split8(pr);
-
-    // ---- values: columns of eight tokens by byte permutes --------------------
-#pragma unroll
-    for (int w = 0; w < VW; ++w) {
-      u32 word[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if constexpr (kF8) {
-          u32 lo, hi;
-          f8_to_bf16(vw[e][0].w[w >> 1], &lo, &hi);
-          word[e] = (w & 1) ? hi : lo;
-        } else {
-          word[e] = vw[e][w / L::kVWords].w[w % L::kVWords];
-        }
-        if (!whole) word[e] = (seen >> pk(gr, e)) & 1 ? word[e] : 0u;  // never 0 * inf
-      }
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const u32x4 col = {halves(word[0], word[1], hf), halves(word[2], word[3], hf),
-                           halves(word[4], word[5], hf), halves(word[6], word[7], hf)};
-        const bf16x8 av = __builtin_bit_cast(bf16x8, col);
-        o[2 * w + hf] = mfma_bf16(av, ps.lo, o[2 * w + hf]);
-        o[2 * w + hf] = mfma_bf16(av, ps.hi, o[2 * w + hf]);
-      }
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    if constexpr (more) {
-      load_v(next);
-      __builtin_amdgcn_sched_barrier(0);
-      now = next;
-      next = resolve(t0 + 2 * kStep, page2);
-    }
-  };
-  if (t0 < last) {
-    for (; t0 + kStep < last; t0 += kStep) tile(std::true_type{});
-    tile(std::false_type{});
-  }
-
-  // ---- join the waves: o[i][j] is column vdim(i, 4 gr + j) of head c ---------
-  // Two slabs of shared memory: waves 2 and 3 store, waves 0 and 1 add.  Four i make 16
-  // adjacent bytes; rows are padded by 16 bytes, so eight lanes cover all banks.
-  constexpr int DS = D + 4;
-  l = rows_sum(l);
-  if (gr == 0) {
-    sm[wave][c] = m;
-    sl[wave][c] = l;
-  }
-  __syncthreads();
-  float mt = sm[0][c];
-#pragma unroll
-  for (int w = 1; w < kWaves; ++w) mt = fmaxf(mt, sm[w][c]);
-  const float f = factor(m, mt);
-  float *slab = lds + ((wave & 1) * heads + c) * DS;
-#pragma unroll
-  for (int pass = 0; pass < 2; ++pass) {
-    if ((wave >> 1) != pass && c < heads) {
-#pragma unroll
-      for (int q = 0; q < NO / 4; ++q)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float *at = slab + L::vdim(4 * q, 4 * gr + j);
-          f32x4 x = {o[4 * q][j], o[4 * q + 1][j], o[4 * q + 2][j], o[4 * q + 3][j]};
-          x *= f;
-          if (pass) x += ld4(at);
-          st4(at, x);
-        }
-    }
-    __syncthreads();
-  }
-  for (int i = threadIdx.x; i < heads * (D / 4); i += kThreads) {
-    const int hd = i / (D / 4), d = 4 * (i % (D / 4));
-    float mh = sm[0][hd], lt = 0.f;
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) mh = fmaxf(mh, sm[w][hd]);
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) lt = fmaf(sl[w][hd], factor(sm[w][hd], mh), lt);
-    f32x4 sum = ld4(lds + hd * DS + d) + ld4(lds + (heads + hd) * DS + d);
-    if (!whole_unit) {
-      const int64_t r = (int64_t(worker) * 2 + (first_unit ? 0 : 1)) * 16 + hd;
-      st4(p.o + r * D + d, sum);
-      if (d == 0) {
-        p.ml[2 * r] = mh;
-        p.ml[2 * r + 1] = lt;
-      }
-    } else {
-      sum *= lt == 0.f ? 0.f : g.v_scale / lt;
-      *reinterpret_cast<u32x2 *>(p.a.out + (qrow + hd) * D + d) =
-          u32x2{cvt_pk_bf16(sum[0], sum[1]), cvt_pk_bf16(sum[2], sum[3])};
-      if (d == 0) {
-        if (p.a.lse) p.a.lse[qrow + hd] = lt == 0.f ? kNegInf : (mh + log2f(lt)) * kLn2;
-        if (kMass) {
-          p.done[2 * (qrow + hd)] = mh;
-          p.done[2 * (qrow + hd) + 1] = lt;
+          sum *= lt == 0.f ? 0.f : g.v_scale / lt;
+          *reinterpret_cast<u32x2 *>(p.a.out + (qrow + hd) * D + d) =
+              u32x2{cvt_pk_bf16(sum[0], sum[1]), cvt_pk_bf16(sum[2], sum[3])};
+          if (d == 0) {
+            if (p.a.lse) p.a.lse[qrow + hd] = lt == 0.f ? kNegInf : (mh + log2f(lt)) * kLn2;
+            if (kMass) {
+              p.done[2 * (qrow + hd)] = mh;
+              p.done[2 * (qrow + hd) + 1] = lt;
+            }
+          }
         }
       }
-    }
-  }
-  __syncthreads();  // the shared arrays are free again
-
-    // ---- the next unit -------------------------------------------------------------
-    left -= nblk;
-    blk = 0;
-    first_unit = false;
-    if (left > 0 && ++unit == units) {
-      unit = 0;
-      do rq = request(++b);
-      while (rq.blocks == 0 && b + 1 < p.a.batch);
-      if (rq.blocks == 0) break;
+      if (p.join && threadIdx.x == 0) {  // where the parts of a unit lie, for the joining kernel
+        int32_t *at = p.unit + 2 * (int64_t(cur.b) * units + cur.unit);
+        if (cur.blk == 0) at[0] = 2 * worker + side;
+        if (cur.blk + cur.nblk == cur.rq.blocks) at[1] = 2 * worker + side;
+      }
+      if (left <= 0) break;
+      local_barrier();  // the shared arrays are free again
+      cur = nx;
+      t0 = nt0;
+      first_unit = false;
+#pragma unroll
+      for (int i = 0; i < kQLoads; ++i) qf[i] = qn[i];
     }
   }
 
@@ -557,8 +655,8 @@ void attn_decode_kernel(KvGeom g, AttnDev p) {
     const int64_t row = int64_t(e) * p.a.q_heads;
     for (int i = threadIdx.x; i < p.a.q_heads * (D / 8); i += kThreads)
       reinterpret_cast<u32x4 *>(p.a.out + row * D)[i] = u32x4{0, 0, 0, 0};
-    if (p.a.lse && int(threadIdx.x) < p.a.q_heads)
-      for (int i = threadIdx.x; i < p.a.q_heads; i += kThreads) p.a.lse[row + i] = kNegInf;
+    for (int i = threadIdx.x; p.a.lse && i < p.a.q_heads; i += kThreads) p.a.lse[row + i] = kNegInf;
+    for (int i = threadIdx.x; p.join && i < 2 * units; i += kThreads) p.unit[2 * int64_t(e) * units + i] = 0;
   }
 }
 
@@ -569,26 +667,17 @@ void attn_decode_kernel(KvGeom g, AttnDev p) {
 // kMassTokens tokens of each (request, key-value head).
 constexpr int kMassTokens = 1024;
 
-// The workers w0 .. w1 of a unit; the part of w0 is its first unit's where its run begins
-// with the unit, else its last; the others' is their first.
+// The workers w0 .. w1 of a unit.  Only w0's part may be a later unit of its run: a worker
+// that goes on with a unit begins with it.
 struct Parts {
-  int w0, w1;
-  bool begins;
+  int w0, w1, side;
   __device__ __forceinline__ int64_t row(int w, int head) const {
-    return (int64_t(w) * 2 + (w == w0 && !begins ? 1 : 0)) * 16 + head;
+    return (int64_t(w) * 2 + (w == w0 ? side : 0)) * 16 + head;
   }
 };
 __device__ __forceinline__ Parts parts_of(const KvGeom &g, const AttnDev &p, int b, int unit) {
-  const int units = g.kv_heads * p.head_blocks;
-  const int n = p.pre[b + 1] - p.pre[b], all = p.pre[p.a.batch] * units;
-  const int first = p.pre[b] * units + unit * n, sharing = min(p.workers, all);
-  Parts r{0, -1, true};
-  if (n > 0) {
-    r.w0 = worker_of(first, all, sharing);
-    r.w1 = worker_of(first + n - 1, all, sharing);
-    r.begins = first_block(r.w0, all, sharing) == first;
-  }
-  return r;
+  const int32_t *at = p.unit + 2 * (int64_t(b) * g.kv_heads * p.head_blocks + unit);
+  return Parts{at[0] >> 1, at[1] >> 1, at[0] & 1};
 }
 // m and l of a head over the parts, by the lanes of a wave
 __device__ __forceinline__ void join_ml(const float *ml, const Parts &pt, int head, int lane, float *m, float *l) {
@@ -647,6 +736,19 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(KvGeom g, AttnDev p
   const int64_t from = int64_t(rq.begin & ~3) + int64_t(block) * kMassTokens;
   if (rq.blocks == 0 || from >= rq.len) return;
   const int64_t qr0 = int64_t(b) * p.a.q_heads + h * p.group;
+  // the scores of the first heads and the weights so far are asked for before the heads' m
+  // and l are known
+  constexpr int kAhead = 8;
+  const int64_t t = from + 4 * threadIdx.x;
+  const bool on = t < rq.len;
+  const float *sc = p.scores + qr0 * p.lpad + (on ? t : from);
+  float *mass = g.mass + (int64_t(rq.slot) * g.kv_heads + h) * g.capacity;
+  f32x4 x[kAhead];
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j) x[j] = ld4(sc + min(j, p.group - 1) * p.lpad);
+  float sum[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) sum[e] = mass[min(t + e, int64_t(rq.len) - 1)];
   for (int j = wave; j < p.group; j += kWaves) {
     const Parts pt = parts_of(g, p, b, h * p.head_blocks + (j >> 4));
     float m, l;
@@ -661,21 +763,22 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(KvGeom g, AttnDev p
       hl[j] = l == 0.f ? 0.f : 1.f / l;
     }
   }
-  __syncthreads();
-  const int64_t t = from + 4 * threadIdx.x;
-  if (t >= rq.len) return;
-  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-  const float *sc = p.scores + qr0 * p.lpad + t;
-#pragma unroll 4
-  for (int j = 0; j < p.group; ++j) {
-    const f32x4 x = ld4(sc + j * p.lpad);
+  local_barrier();
+  f32x4 add = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) sum[e] = fmaf(fexp2(x[e] - hm[j]), hl[j], sum[e]);
+  for (int j = 0; j < kAhead; ++j)
+    if (j < p.group)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) add[e] = fmaf(fexp2(x[j][e] - hm[j]), hl[j], add[e]);
+#pragma unroll 4
+  for (int j = kAhead; j < p.group; ++j) {
+    const f32x4 y = ld4(sc + j * p.lpad);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) add[e] = fmaf(fexp2(y[e] - hm[j]), hl[j], add[e]);
   }
-  float *mass = g.mass + (int64_t(rq.slot) * g.kv_heads + h) * g.capacity + t;
 #pragma unroll
   for (int e = 0; e < 4; ++e)
-    if (t + e >= rq.begin && t + e < rq.len) mass[e] += sum[e];
+    if (on && t + e >= rq.begin && t + e < rq.len) mass[t + e] = sum[e] + add[e];
 }
 
 size_t pad256(size_t n) { return (n + 255) & ~size_t(255); }
@@ -683,10 +786,14 @@ int64_t score_row(int max_len) { return (int64_t(max_len) + kTile - 1) / kTile *
 
 template <int D, bool kF8>
 hipError_t launch_dt(const KvGeom &g, const AttnDev &p, hipStream_t s) {
-  const size_t lds = size_t(2) * std::min(16, p.group) * (D + 4) * 4;
+  const size_t lds = size_t(kWaves) * (D / 16) * 69 * 16;
   const bool wide = (1 << g.page_shift) >= kTile;
-  const auto kernel = wide ? (p.scores ? attn_decode_kernel<D, kF8, true, true> : attn_decode_kernel<D, kF8, true, false>)
-                           : (p.scores ? attn_decode_kernel<D, kF8, false, true> : attn_decode_kernel<D, kF8, false, false>);
+  const int mass = !p.scores ? 0 : p.group <= 8 ? 1 : 2;
+  typedef void (*kernel_t)(KvGeom, AttnDev);
+  static const kernel_t kernels[2][3] = {
+      {attn_decode_kernel<D, kF8, false, 0>, attn_decode_kernel<D, kF8, false, 1>, attn_decode_kernel<D, kF8, false, 2>},
+      {attn_decode_kernel<D, kF8, true, 0>, attn_decode_kernel<D, kF8, true, 1>, attn_decode_kernel<D, kF8, true, 2>}};
+  const kernel_t kernel = kernels[wide][mass];
   hipLaunchKernelGGL(kernel, dim3(unsigned(p.workers)), dim3(kThreads), lds, s, g, p);
   return hipGetLastError();
 }
@@ -717,13 +824,13 @@ bool attn_joins(int max_len, uint32_t flags) { return max_len > kBlock || (flags
 
 // Parts of the workspace, in order.
 struct AttnSpace {
-  size_t pre, o, ml, done, scores;
+  size_t unit, o, ml, done, scores;
 };
 AttnSpace attn_space(const gdn_kv_pool *p, int batch, int q_heads, int max_len, uint32_t flags) {
   AttnSpace r{};
   if (!attn_joins(max_len, flags)) return r;
   const size_t parts = size_t(attn_workers(p, batch, q_heads, max_len)) * 2 * 16, rows = size_t(batch) * q_heads;
-  r.pre = pad256((size_t(batch) + 1) * 4);
+  r.unit = pad256(size_t(batch) * p->d.kv_heads * ((q_heads / p->d.kv_heads + 15) / 16) * 8);
   r.o = pad256(parts * p->d.head_dim * 4);
   r.ml = pad256(parts * 8);
   if (flags & GDN_F_ACCUM_MASS) {
@@ -742,7 +849,7 @@ bool attn_fits(const gdn_kv_pool *p, int batch, int q_heads, int max_len) {
 
 size_t attn_workspace(const gdn_kv_pool *p, int batch, int q_heads, int max_len, uint32_t flags) {
   const AttnSpace w = attn_space(p, batch, q_heads, max_len, flags);
-  return w.pre + w.o + w.ml + w.done + w.scores;
+  return w.unit + w.o + w.ml + w.done + w.scores;
 }
 
 hipError_t launch_attn_decode(const gdn_kv_pool *pool, int layer, const AttnArgs &a, hipStream_t s) {
@@ -757,8 +864,8 @@ hipError_t launch_attn_decode(const gdn_kv_pool *pool, int layer, const AttnArgs
   if (p.join) {
     const AttnSpace w = attn_space(pool, a.batch, a.q_heads, a.max_len, a.flags);
     char *at = static_cast<char *>(a.workspace);
-    p.pre = reinterpret_cast<int32_t *>(at);
-    p.o = reinterpret_cast<float *>(at += w.pre);
+    p.unit = reinterpret_cast<int32_t *>(at);
+    p.o = reinterpret_cast<float *>(at += w.unit);
     p.ml = reinterpret_cast<float *>(at += w.o);
     if (a.flags & GDN_F_ACCUM_MASS) {
       p.done = reinterpret_cast<float *>(at += w.ml);
