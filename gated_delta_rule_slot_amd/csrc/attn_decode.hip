@@ -663,8 +663,8 @@ void attn_decode_kernel(KvGeom g, AttnDev p) {
 // Joins the parts of each (request, query head) that more than one worker had, and adds
 // the weights
 //   mass[t] += sum over the group's heads of 2^(score - m) / l.
-// Workgroups: first one per (request, query head), then, with weights, one per
-// kMassTokens tokens of each (request, key-value head).
+// Workgroups: with weights first one per kMassTokens tokens of each (request, key-value
+// head), then one per (request, query head).
 constexpr int kMassTokens = 1024;
 
 // The workers w0 .. w1 of a unit.  Only w0's part may be a later unit of its run: a worker
@@ -697,9 +697,10 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(KvGeom g, AttnDev p
   __shared__ __attribute__((aligned(16))) float acc[kWaves][D];
   __shared__ float hm[64], hl[64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int joins = p.a.batch * p.a.q_heads;
-  if (int(blockIdx.x) < joins) {
-    const int qr = blockIdx.x, b = qr / p.a.q_heads, qh = qr - b * p.a.q_heads;
+  // (the weights' workgroups come first: they take longer)
+  const int masses = p.a.batch * g.kv_heads * mass_blocks;
+  if (int(blockIdx.x) >= masses) {
+    const int qr = blockIdx.x - masses, b = qr / p.a.q_heads, qh = qr - b * p.a.q_heads;
     const int h = qh / p.group, j = qh - h * p.group;  // head j of the group
     const Parts pt = parts_of(g, p, b, h * p.head_blocks + (j >> 4));
     if (pt.w1 <= pt.w0) return;  // nothing, or final already
@@ -729,8 +730,7 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(KvGeom g, AttnDev p
     if (p.a.lse && threadIdx.x == 0) p.a.lse[qr] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
     return;
   }
-  const int64_t id = int64_t(blockIdx.x) - joins;
-  const int block = int(id % mass_blocks), bh = int(id / mass_blocks);
+  const int block = blockIdx.x % mass_blocks, bh = blockIdx.x / mass_blocks;
   const int h = bh % g.kv_heads, b = bh / g.kv_heads;
   const Seen rq = seen_by(g, p.a, b, false);
   const int64_t from = int64_t(rq.begin & ~3) + int64_t(block) * kMassTokens;
@@ -749,7 +749,24 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(KvGeom g, AttnDev p
   float sum[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) sum[e] = mass[min(t + e, int64_t(rq.len) - 1)];
-  for (int j = wave; j < p.group; j += kWaves) {
+  const Parts whole = parts_of(g, p, b, h * p.head_blocks);
+  if (p.head_blocks == 1 && whole.w1 - whole.w0 < 8) {  // the usual case: 8 lanes a head
+    const int j = threadIdx.x >> 3, w = whole.w0 + (threadIdx.x & 7);
+    float m = kNegInf, l = 0.f;
+    if (j < p.group && w <= whole.w1) {
+      const float *e = whole.w1 > whole.w0 ? p.ml + 2 * whole.row(w, j) : p.done + 2 * (qr0 + j);
+      m = e[0];
+      l = e[1];
+    }
+    float mm = fmaxf(m, dpp_mov<0xB1>(m));
+    mm = fmaxf(mm, dpp_mov<0x4E>(mm));
+    mm = fmaxf(mm, dpp_mov<0x141>(mm));
+    l = group_sum<8>(l * factor(m, mm));
+    if (j < p.group && (threadIdx.x & 7) == 0) {
+      hm[j] = ref(mm);
+      hl[j] = l == 0.f ? 0.f : 1.f / l;
+    }
+  } else for (int j = wave; j < p.group; j += kWaves) {
     const Parts pt = parts_of(g, p, b, h * p.head_blocks + (j >> 4));
     float m, l;
     if (pt.w1 > pt.w0) {
