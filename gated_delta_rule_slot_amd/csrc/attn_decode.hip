@@ -184,8 +184,10 @@ __device__ __forceinline__ void f8_to_bf16(u32 x, u32 *lo, u32 *hi) {
   *hi = __builtin_amdgcn_perm(__float_as_uint(b[1]), __float_as_uint(b[0]), 0x07060302u);
 }
 
-// kWide: pages hold whole tiles (page_size >= 32), so a tile's rows are adjacent and its
-// one page id is wave-uniform; otherwise each token's row is looked up.
+// kWide: pages hold 16 tokens or more, so each half of a tile has adjacent rows and one
+// wave-uniform page id; otherwise each token's row is looked up,
+// about a tenth slower (128 requests of 2048 tokens, 4 heads of 128: 4-token pages 96.8 us,
+// 16-token pages 91.3 us).
 //
 // The keys and values of a wave's next tile are asked for while the present one is worked
 // on, also over the end of a unit: under load a dependent read takes 5 us and more, so a
@@ -230,14 +232,16 @@ void attn_decode_kernel(KvGeom g, AttnDev p) {
   };
 
   // ---- this worker's run of blocks, by each wave for itself: lane i has four requests ----
-  int count[4], inc = 0;
+  Seen four[4];
+  int inc = 0;
   auto scan = [&](int base) -> int {
     int mine = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = base + 4 * lane + i;
-      count[i] = r < p.a.batch ? seen_by(g, p.a, r, false).blocks : 0;
-      mine += count[i];
+      four[i] = seen_by(g, p.a, min(r, p.a.batch - 1), false);
+      if (r >= p.a.batch) four[i].blocks = 0;
+      mine += four[i].blocks;
     }
     inc = wave_scan(mine);
     const int sum = __builtin_amdgcn_readlane(inc, 63);
@@ -278,39 +282,47 @@ void attn_decode_kernel(KvGeom g, AttnDev p) {
   // Rows of a tile.  A token that is not visible, or whose page id is not a page, reads
   // page 0's rows (always there) and is masked by its bit of `seen`.
   struct Rows {
-    int row;   // kWide: first row of the tile; else lane i < 32: row of token t0 + i
+    int row[2];  // kWide: first row of each half; else row[0] of lane i < 32: row of token t0 + i
     u32 seen;
+  };
+  struct Pages {
+    int id[2];   // kWide: of each half; else id[0] of lane i < 32: of token t0 + i
   };
   const int in_page = (1 << g.page_shift) - 1;
   // The page ids are asked for a tile before their rows are (and, where the reads are not
   // scalar, before that tile's keys: loads return in order).
-  auto ask = [&](const Part &u, int t0) -> int {
+  auto ask = [&](const Part &u, int t0) -> Pages {
     const table_t table = (table_t)(g.page_table + int64_t(u.rq.slot) * g.max_pages);
-    if constexpr (kWide) return table[max(0, min(t0, u.last - 1)) >> g.page_shift];
-    else return table[max(0, max(u.rq.begin, min(t0 + (lane & 31), u.last - 1))) >> g.page_shift];
+    if constexpr (kWide)
+      return Pages{{table[max(0, min(t0, u.last - 1)) >> g.page_shift],
+                    table[max(0, min(t0 + 16, u.last - 1)) >> g.page_shift]}};
+    else return Pages{{table[max(0, max(u.rq.begin, min(t0 + (lane & 31), u.last - 1))) >> g.page_shift], 0}};
   };
-  auto resolve = [&](int h, int begin, int last, int t0, int page) -> Rows {
+  auto resolve = [&](int h, int begin, int last, int t0, const Pages &pages) -> Rows {
     Rows r;
     if constexpr (kWide) {
-      const bool ok = page > 0 && page < g.pages;
-      if (!ok && t0 < last) {
-        if (lane == 0) set_err(g.err, GDN_ERRW_BAD_PAGE);
+      u32 m = 0;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int t = t0 + 16 * u, page = pages.id[u];
+        const bool in = t < last && t + 16 > begin, ok = page > 0 && page < g.pages;
+        if (in && !ok && lane == 0) set_err(g.err, GDN_ERRW_BAD_PAGE);
+        r.row[u] = in && ok ? ((page * g.kv_heads + h) << g.page_shift) + (t & in_page) : 0;
+        m |= in && ok ? 0xffffu << (16 * u) : 0u;
       }
-      const bool use = ok && t0 < last;
-      r.row = use ? ((page * g.kv_heads + h) << g.page_shift) + (t0 & in_page) : 0;
       // bits from begin on, and below last
-      u32 m = use ? 0xffffffffu : 0u;
       if (begin > t0) m &= begin - t0 >= 32 ? 0u : 0xffffffffu << (begin - t0);
-      if (use && last - t0 < 32) m &= (1u << (last - t0)) - 1u;
+      if (last - t0 < 32) m &= last > t0 ? (1u << (last - t0)) - 1u : 0u;
       r.seen = m;
     } else {
-      const int t = t0 + (lane & 31);
+      const int t = t0 + (lane & 31), page = pages.id[0];
       const bool in = t >= begin && t < last;
       const bool ok = in && page > 0 && page < g.pages;
       if (__any(in && !ok)) {
         if (lane == 0) set_err(g.err, GDN_ERRW_BAD_PAGE);
       }
-      r.row = ok ? ((page * g.kv_heads + h) << g.page_shift) + (t & in_page) : 0;
+      r.row[0] = ok ? ((page * g.kv_heads + h) << g.page_shift) + (t & in_page) : 0;
+      r.row[1] = 0;
       r.seen = u32(__ballot(ok));  // lanes 32 up repeat the lower ones
     }
     return r;
@@ -326,27 +338,25 @@ void attn_decode_kernel(KvGeom g, AttnDev p) {
     return v;
   };
   auto load_k = [&](const Rows &r) {
-    const char *tile = g.k + int64_t(r.row) * RB;
     const int ln = lane_anew();
     const u32 k_off = u32((ln & 15) * RB + 16 * (ln >> 4));
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const char *at;
-      if constexpr (kWide) at = tile + 16 * u * RB + k_off;
-      else at = g.k + int64_t(__shfl(r.row, 16 * u + (ln & 15))) * RB + 16 * (ln >> 4);
+      if constexpr (kWide) at = g.k + int64_t(r.row[u]) * RB + k_off;
+      else at = g.k + int64_t(__shfl(r.row[0], 16 * u + (ln & 15))) * RB + 16 * (ln >> 4);
 #pragma unroll
       for (int s = 0; s < L::kPieces; ++s) kw[u][s] = load_words<4>(at + 64 * s);
     }
   };
   auto load_v = [&](const Rows &r) {
-    const char *tile = g.v + int64_t(r.row) * RB;
     const int ln = lane_anew();
     const u32 v_off = u32(4 * (ln >> 4) * RB + 4 * L::kVWords * (ln & 15));
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const char *at;
-      if constexpr (kWide) at = tile + pk(0, e) * RB + v_off;
-      else at = g.v + int64_t(__shfl(r.row, pk(ln >> 4, e))) * RB + 4 * L::kVWords * (ln & 15);
+      if constexpr (kWide) at = g.v + int64_t(r.row[e >> 2]) * RB + (e & 3) * RB + v_off;
+      else at = g.v + int64_t(__shfl(r.row[0], pk(ln >> 4, e))) * RB + 4 * L::kVWords * (ln & 15);
 #pragma unroll
       for (int s = 0; s < L::kVPieces; ++s) vw[e][s] = load_words<L::kVWords>(at + 256 * s);
     }
@@ -365,26 +375,31 @@ void attn_decode_kernel(KvGeom g, AttnDev p) {
     // ---- find the run's first block -----------------------------------------------
     const int x = run_first / units;
     int b = 0, lo = 0;
+    Seen rq{0, 0, 0, 0};
     for (int base = 0; base < p.a.batch; base += 256) {
       const int sum = p.a.batch > 256 ? scan(base) : last_sum;
       if (x < lo + sum) {
         // the last lane whose requests begin at or before x, and of its four the holder
         const int at = 63 - __clzll(__ballot(lo + inc <= x));
-        b = base + 4 * at;
         lo += __builtin_amdgcn_readlane(inc, at);
+        bool found = false;
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
-          const int n = __builtin_amdgcn_readlane(count[i], at);
-          if (b == base + 4 * at + i && x >= lo + n) {
-            lo += n;
-            ++b;
+        for (int i = 0; i < 4; ++i) {
+          const Seen v{__builtin_amdgcn_readlane(four[i].slot, at), __builtin_amdgcn_readlane(four[i].begin, at),
+                       __builtin_amdgcn_readlane(four[i].len, at), __builtin_amdgcn_readlane(four[i].blocks, at)};
+          if (found) continue;
+          if (x < lo + v.blocks) {
+            found = true;
+            b = base + 4 * at + i;
+            rq = v;
+          } else {
+            lo += v.blocks;
           }
         }
         break;
       }
       lo += sum;
     }
-    Seen rq = request(b);
     const int in_request = run_first - lo * units;
     const int unit0 = in_request / rq.blocks;
     Part cur = part(b, unit0, in_request - unit0 * rq.blocks, rq, left);
@@ -393,10 +408,10 @@ void attn_decode_kernel(KvGeom g, AttnDev p) {
     load_q(cur, qf);
     __builtin_amdgcn_sched_barrier(0);
     int t0 = cur.first + kTile * wave;
-    int page1;
+    Pages page1;
     Rows now;
     {
-      const int page0 = ask(cur, t0);
+      const Pages page0 = ask(cur, t0);
       page1 = ask(cur, t0 + kStep);
       now = resolve(cur.h, cur.rq.begin, cur.last, t0, page0);
       load_k(now);
@@ -434,7 +449,7 @@ void attn_decode_kernel(KvGeom g, AttnDev p) {
       const int nt0 = nx.first + kTile * wave;
       bf16x8 qn[kQLoads];
       load_q(nx, qn);
-      const int npage0 = ask(nx, nt0), npage1 = ask(nx, nt0 + kStep);
+      const Pages npage0 = ask(nx, nt0), npage1 = ask(nx, nt0 + kStep);
 
       f32x4 o[NO];
 #pragma unroll
@@ -804,7 +819,7 @@ int64_t score_row(int max_len) { return (int64_t(max_len) + kTile - 1) / kTile *
 template <int D, bool kF8>
 hipError_t launch_dt(const KvGeom &g, const AttnDev &p, hipStream_t s) {
   const size_t lds = size_t(kWaves) * (D / 16) * 69 * 16;
-  const bool wide = (1 << g.page_shift) >= kTile;
+  const bool wide = (1 << g.page_shift) >= 16;
   const int mass = !p.scores ? 0 : p.group <= 8 ? 1 : 2;
   typedef void (*kernel_t)(KvGeom, AttnDev);
   static const kernel_t kernels[2][3] = {
@@ -829,11 +844,19 @@ hipError_t launch_d(const KvGeom &g, const AttnDev &p, bool f8, hipStream_t s) {
 // Blocks of a unit of max_len tokens (its first tile may begin before the first one seen).
 int64_t unit_blocks(int max_len) { return std::max<int64_t>(1, (int64_t(max_len) + kTile - 1 + kBlock - 1) / kBlock); }
 
-// Workers of a call: what runs at once, or fewer where there are not that many blocks.
+// Workers of a call: one per compute unit (its 4 waves keep 64 to 128 KB in flight), or fewer
+// where there are not that many blocks.  A second one per compute unit loses where pages hold
+// a tile (128 ragged requests of 2100 tokens, head dim 256: 108.9 against 102.0 us; 16 of
+// 8192 tokens: 39.1 against 33.5 us, a larger part of it joining), and gains with smaller
+// pages, whose short runs of a head otherwise meet on few memory channels at a time
+// (e4m3, 16-token pages, 64 requests of 4096 tokens: 97 against 133 us), once there is work
+// for both.
 int attn_workers(const gdn_kv_pool *p, int batch, int q_heads, int max_len) {
   const int group = q_heads / p->d.kv_heads;
   const int64_t units = int64_t(batch) * p->d.kv_heads * ((group + 15) / 16);
-  return int(std::max<int64_t>(1, std::min<int64_t>(kCUs * 2, units * unit_blocks(max_len))));
+  const int64_t blocks = units * unit_blocks(max_len);
+  const int per_cu = p->d.page_size < kTile && blocks >= 8 * kCUs ? 2 : 1;
+  return int(std::max<int64_t>(1, std::min<int64_t>(kCUs * per_cu, blocks)));
 }
 
 // One block per unit at most: no unit is ever divided.
