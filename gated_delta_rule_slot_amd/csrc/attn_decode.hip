@@ -140,9 +140,6 @@ struct Lay<D, false> {
   static __device__ __forceinline__ int vdim(int i, int c) {
     return D == 64 ? 4 * c + i : 128 * (i >> 3) + 8 * c + (i & 7);
   }
-  // the inverse, for d a multiple of 4: d .. d + 3 are columns vi(d) .. vi(d) + 3 of lane vc(d)
-  static __device__ __forceinline__ int vi(int d) { return D == 64 ? 0 : 8 * (d >> 7) + (d & 7); }
-  static __device__ __forceinline__ int vc(int d) { return D == 64 ? d >> 2 : (d >> 3) & 15; }
 };
 template <int D>
 struct Lay<D, true> {
@@ -152,8 +149,6 @@ struct Lay<D, true> {
   static constexpr int kVWords = D / 64;
   static __device__ __forceinline__ int kdim(int s, int g) { return 64 * (s >> 1) + 16 * g + 8 * (s & 1); }
   static __device__ __forceinline__ int vdim(int i, int c) { return (D / 16) * c + i; }
-  static __device__ __forceinline__ int vi(int d) { return d % (D / 16); }
-  static __device__ __forceinline__ int vc(int d) { return d / (D / 16); }
 };
 
 template <int W>
@@ -280,7 +275,8 @@ void attn_decode_kernel(KvGeom g, AttnDev p) {
   };
 
   // Rows of a tile.  A token that is not visible, or whose page id is not a page, reads
-  // page 0's rows (always there) and is masked by its bit of `seen`.
+  // page 0's rows (always there) and is masked by its bit of `seen`; of a tile without visible
+  // tokens (a wave's next one at the end of its run) all lanes read the same few bytes.
   struct Rows {
     int row[2];  // kWide: first row of each half; else row[0] of lane i < 32: row of token t0 + i
     u32 seen;
@@ -339,7 +335,7 @@ void attn_decode_kernel(KvGeom g, AttnDev p) {
   };
   auto load_k = [&](const Rows &r) {
     const int ln = lane_anew();
-    const u32 k_off = u32((ln & 15) * RB + 16 * (ln >> 4));
+    const u32 k_off = r.seen ? u32((ln & 15) * RB + 16 * (ln >> 4)) : 0u;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const char *at;
@@ -351,7 +347,7 @@ void attn_decode_kernel(KvGeom g, AttnDev p) {
   };
   auto load_v = [&](const Rows &r) {
     const int ln = lane_anew();
-    const u32 v_off = u32(4 * (ln >> 4) * RB + 4 * L::kVWords * (ln & 15));
+    const u32 v_off = r.seen ? u32(4 * (ln >> 4) * RB + 4 * L::kVWords * (ln & 15)) : 0u;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const char *at;
@@ -600,7 +596,7 @@ void attn_decode_kernel(KvGeom g, AttnDev p) {
       }
 
       // ---- join the waves: o[i][j] is column vdim(i, 4 gr + j) of head c ------------------
-      const int lane = lane_anew(), c = lane & 15, gr = lane >> 4, tid = 64 * wave + lane;
+      const int lane = lane_anew(), c = lane & 15, gr = lane >> 4;
       l = rows_sum(l);
       if (gr == 0) {
         sm[wave][c] = m;
@@ -614,37 +610,55 @@ void attn_decode_kernel(KvGeom g, AttnDev p) {
       local_barrier();
       const bool whole_unit = cur.nblk == cur.rq.blocks;
       const int side = first_unit ? 0 : 1;
-      for (int i = tid; i < cur.heads * (D / 4); i += kThreads) {
-        const int hd = i / (D / 4), d = 4 * (i % (D / 4));
-        float mh = sm[0][hd], lt = 0.f;
+      // a thread takes kJ rows j0 up of four columns (4 q up) of its lane's head: 4 adjacent
+      // values of O for each j
+      if (c < cur.heads) {
+        constexpr int kJ = NO / 4;
+        typedef float vec_j __attribute__((ext_vector_type(kJ)));
+        const int q = wave * kJ / 4, j0 = wave * kJ % 4;
+        float mh = sm[0][c], lt = 0.f;
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) mh = fmaxf(mh, sm[w][hd]);
-        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-        const int r = L::vc(d);  // row r & 3 of lane group r / 4
-        const float *at = lds + L::vi(d) * kOi + 4 * (17 * (r >> 2) + hd) + (r & 3);
+        for (int w = 1; w < kWaves; ++w) mh = fmaxf(mh, sm[w][c]);
+        float sum[4][kJ];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int r = 0; r < kJ; ++r) sum[e][r] = 0.f;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
-          const float f = factor(sm[w][hd], mh);
-          lt = fmaf(sl[w][hd], f, lt);
+          const float f = factor(sm[w][c], mh);
+          lt = fmaf(sl[w][c], f, lt);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sum[e] = fmaf(at[w * kSlab + e * kOi], f, sum[e]);
+          for (int e = 0; e < 4; ++e) {
+            const float *at = lds + w * kSlab + (4 * q + e) * kOi + 4 * (lane + gr) + j0;
+            vec_j v;
+            if constexpr (kJ == 1) v[0] = *at;
+            else v = *reinterpret_cast<const vec_j *>(at);
+#pragma unroll
+            for (int r = 0; r < kJ; ++r) sum[e][r] = fmaf(v[r], f, sum[e][r]);
+          }
         }
+        const bool teller = wave == 0 && gr == 0;
         if (!whole_unit) {
-          const int64_t row = (int64_t(worker) * 2 + side) * 16 + hd;
-          st4(p.o + row * D + d, sum);
-          if (d == 0) {
+          const int64_t row = (int64_t(worker) * 2 + side) * 16 + c;
+#pragma unroll
+          for (int r = 0; r < kJ; ++r)
+            st4(p.o + row * D + L::vdim(4 * q, 4 * gr + j0 + r), f32x4{sum[0][r], sum[1][r], sum[2][r], sum[3][r]});
+          if (teller) {
             p.ml[2 * row] = mh;
             p.ml[2 * row + 1] = lt;
           }
         } else {
-          sum *= lt == 0.f ? 0.f : g.v_scale / lt;
-          *reinterpret_cast<u32x2 *>(p.a.out + (qrow + hd) * D + d) =
-              u32x2{cvt_pk_bf16(sum[0], sum[1]), cvt_pk_bf16(sum[2], sum[3])};
-          if (d == 0) {
-            if (p.a.lse) p.a.lse[qrow + hd] = lt == 0.f ? kNegInf : (mh + log2f(lt)) * kLn2;
+          const float inv = lt == 0.f ? 0.f : g.v_scale / lt;
+#pragma unroll
+          for (int r = 0; r < kJ; ++r)
+            *reinterpret_cast<u32x2 *>(p.a.out + (qrow + c) * D + L::vdim(4 * q, 4 * gr + j0 + r)) =
+                u32x2{cvt_pk_bf16(sum[0][r] * inv, sum[1][r] * inv), cvt_pk_bf16(sum[2][r] * inv, sum[3][r] * inv)};
+          if (teller) {
+            if (p.a.lse) p.a.lse[qrow + c] = lt == 0.f ? kNegInf : (mh + log2f(lt)) * kLn2;
             if (kMass) {
-              p.done[2 * (qrow + hd)] = mh;
-              p.done[2 * (qrow + hd) + 1] = lt;
+              p.done[2 * (qrow + c)] = mh;
+              p.done[2 * (qrow + c) + 1] = lt;
             }
           }
         }
@@ -719,28 +733,67 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(KvGeom g, AttnDev p
     const int h = qh / p.group, j = qh - h * p.group;  // head j of the group
     const Parts pt = parts_of(g, p, b, h * p.head_blocks + (j >> 4));
     if (pt.w1 <= pt.w0) return;  // nothing, or final already
-    float m, l;
-    join_ml(p.ml, pt, j & 15, lane, &m, &l);  // every wave for itself
+    // every wave takes each fourth part, four of them at a time under their common maximum
     constexpr int C = D / 64;  // columns of a lane
-    float sum[C];
+    typedef float vec_c __attribute__((ext_vector_type(C)));
+    float m = kNegInf, l = 0.f, sum[C];
 #pragma unroll
     for (int i = 0; i < C; ++i) sum[i] = 0.f;
-#pragma unroll 4
-    for (int w = pt.w0 + wave; w <= pt.w1; w += kWaves) {
-      const int64_t r = pt.row(w, j & 15);
-      const float f = factor(p.ml[2 * r], m);
+    for (int w = pt.w0 + wave; w <= pt.w1; w += 4 * kWaves) {
+      float mw[4], lw[4];
+      vec_c ow[4];
 #pragma unroll
-      for (int i = 0; i < C; ++i) sum[i] = fmaf(f, p.o[r * D + C * lane + i], sum[i]);
+      for (int k = 0; k < 4; ++k) {
+        const int64_t r = pt.row(min(w + k * kWaves, pt.w1), j & 15);
+        mw[k] = p.ml[2 * r];
+        lw[k] = p.ml[2 * r + 1];
+        ow[k] = *reinterpret_cast<const vec_c *>(p.o + r * D + C * lane);
+      }
+      float mt = m;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (w + k * kWaves > pt.w1) mw[k] = kNegInf, lw[k] = 0.f, ow[k] = vec_c(0.f);
+        mt = fmaxf(mt, mw[k]);
+      }
+      const float f0 = factor(m, mt);
+      l *= f0;
+#pragma unroll
+      for (int i = 0; i < C; ++i) sum[i] *= f0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float f = factor(mw[k], mt);
+        l = fmaf(lw[k], f, l);
+#pragma unroll
+        for (int i = 0; i < C; ++i) sum[i] = fmaf(ow[k][i], f, sum[i]);
+      }
+      m = mt;
     }
 #pragma unroll
     for (int i = 0; i < C; ++i) acc[wave][C * lane + i] = sum[i];
-    __syncthreads();
-    const float inv = l == 0.f ? 0.f : g.v_scale / l;
-    for (int i = threadIdx.x; i < D; i += kThreads) {
-      float t = 0.f;
+    if (lane == 0) {
+      hm[wave] = m;
+      hl[wave] = l;
+    }
+    local_barrier();
+    m = hm[0];
+    l = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) t += acc[w][i];
-      p.a.out[int64_t(qr) * D + i] = f32_to_bf16(t * inv);
+    for (int w = 1; w < kWaves; ++w) m = fmaxf(m, hm[w]);
+    float f[kWaves];
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      f[w] = factor(hm[w], m);
+      l = fmaf(hl[w], f[w], l);
+    }
+    const float inv = l == 0.f ? 0.f : g.v_scale / l;
+    if (int(threadIdx.x) < D / 2) {  // two columns a thread
+      float t0 = 0.f, t1 = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        t0 = fmaf(acc[w][2 * threadIdx.x], f[w], t0);
+        t1 = fmaf(acc[w][2 * threadIdx.x + 1], f[w], t1);
+      }
+      reinterpret_cast<u32 *>(p.a.out + int64_t(qr) * D)[threadIdx.x] = cvt_pk_bf16(t0 * inv, t1 * inv);
     }
     if (p.a.lse && threadIdx.x == 0) p.a.lse[qr] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
     return;
