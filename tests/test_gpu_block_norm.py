@@ -96,6 +96,14 @@ def test_block_norm_many_rows_and_in_place():
     check(c, *run(c, in_place=True))
 
 
+def test_block_norm_streamed():
+    """Tensors past the size from which they are not kept in the caches."""
+    c = case(11, 3101, 1, 4096, True, "silu", "f32", True, scale=0.5, g_pad=8)
+    check(c, *run(c))
+    c = case(12, 12001, 8, 136, True, "sigmoid", "bf16", False, "f32")
+    check(c, *run(c, in_place=True))
+
+
 @pytest.mark.parametrize("std,eps", [(1e-18, 1e-6), (1e-3, 1e-5), (1e15, 1e-6), (0.0, 1e-6)])
 def test_block_norm_small_large_and_zero_rows(std, eps):
     """Rows whose squares leave bf16's comfortable range, and rows of zeros."""
