@@ -34,8 +34,8 @@ gdn_status check_shape(const gdn_kv_desc *d) {
     return fail(GDN_ERR_UNSUPPORTED, "head dim %d not in {64, 128, 256}", d->head_dim);
   if (d->page_size < 1 || d->page_size > 1024 || (d->page_size & (d->page_size - 1)))
     return fail(GDN_ERR_UNSUPPORTED, "page_size %d is not a power of two in [1, 1024]", d->page_size);
-  if (int64_t(d->max_pages) * d->page_size >= (int64_t(1) << 31))
-    return fail(GDN_ERR_UNSUPPORTED, "max_pages * page_size must be below 2^31");
+  if (int64_t(d->max_pages) * d->page_size >= (int64_t(1) << 30))
+    return fail(GDN_ERR_UNSUPPORTED, "max_pages * page_size must be below 2^30");
   if (d->kv_heads > 65535 ||
       int64_t(d->pages) * d->page_size >= (int64_t(1) << 31) / d->kv_heads)
     return fail(GDN_ERR_UNSUPPORTED, "pages * kv_heads * page_size must be below 2^31");
@@ -47,7 +47,7 @@ gdn_status check_call(gdn_kv_pool_t p, int layer_begin, int layer_end, int batch
   if (layer_begin < 0 || layer_end > p->d.layers || layer_begin > layer_end)
     return fail(GDN_ERR_RANGE, "layers [%d, %d) outside [0, %d)", layer_begin, layer_end, p->d.layers);
   if (batch < 0 || batch > 65535) return fail(GDN_ERR_RANGE, "batch %d outside [0, 65535]", batch);
-  // the grids hold one workgroup row per (layer, request, head)
+  // (layer, request, head) is counted in 31 bits
   if (int64_t(layer_end - layer_begin) * batch * p->d.kv_heads >= (int64_t(1) << 31))
     return fail(GDN_ERR_RANGE, "layers * batch * kv_heads must be below 2^31");
   return GDN_OK;
@@ -132,7 +132,7 @@ GDN_API gdn_status kv_append(gdn_kv_pool_t pool, int32_t layer, int32_t n, const
     return fail(GDN_ERR_ARG, "k_stride or v_stride below kv_heads * head_dim");
   if (k_stride % 8 || v_stride % 8 || !aligned(k, 16) || !aligned(v, 16))
     return fail(GDN_ERR_UNSUPPORTED, "k and v rows must be 16-byte aligned");
-  // one thread per 8 values of a row, and the grid's extent is 32 bits
+  // one thread per 8 values of a row
   if (int64_t(n) * (row / 8) >= (int64_t(1) << 38))
     return fail(GDN_ERR_RANGE, "n * kv_heads * head_dim too large");
   gdn::AppendArgs a{n, slot_ids, index, position, k, v, k_stride, v_stride};
@@ -159,7 +159,8 @@ GDN_API gdn_status attn_decode_paged(gdn_kv_pool_t pool, int32_t layer, int32_t 
   if (s != GDN_OK) return s;
   if (layer < 0 || layer >= pool->d.layers)
     return fail(GDN_ERR_RANGE, "layer %d outside [0, %d)", layer, pool->d.layers);
-  if (!isfinite(scale)) return fail(GDN_ERR_ARG, "scale must be finite");
+  if (!(fabsf(scale) * pool->d.k_scale <= 1e30f))
+    return fail(GDN_ERR_ARG, "scale * k_scale must be a number of at most 1e30");
   if (batch == 0) return ok();
   if (!slot_table || !kv_len || !q || !out) return fail(GDN_ERR_ARG, "a required pointer is NULL");
   if (q_stride < int64_t(q_heads) * pool->d.head_dim)

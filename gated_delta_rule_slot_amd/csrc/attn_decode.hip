@@ -436,10 +436,12 @@ void attn_decode_kernel(KvGeom g, AttnDev p) {
         Seen nr = cur.rq;
         if (nu == units) {
           nu = 0;
-          do nr = request(++nb);
-          while (nr.blocks == 0 && nb + 1 < p.a.batch);
+          nr.blocks = 0;
+          while (nr.blocks == 0 && ++nb < p.a.batch) nr = request(nb);
         }
-        nx = part(nb, nu, 0, nr, left);
+        // (there always is one, unless the lengths change under the call; then the run ends)
+        if (nr.blocks > 0) nx = part(nb, nu, 0, nr, left);
+        else left = 0;
       }
       const int nx_last = left > 0 ? nx.last : 0;
       const int nt0 = nx.first + kTile * wave;
@@ -727,9 +729,10 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(KvGeom g, AttnDev p
   __shared__ float hm[64], hl[64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   // (the weights' workgroups come first: they take longer)
-  const int masses = p.a.batch * g.kv_heads * mass_blocks;
-  if (int(blockIdx.x) >= masses) {
-    const int qr = blockIdx.x - masses, b = qr / p.a.q_heads, qh = qr - b * p.a.q_heads;
+  const int64_t id = flat_block(), masses = int64_t(p.a.batch) * g.kv_heads * mass_blocks;
+  if (id >= masses) {
+    if (id - masses >= int64_t(p.a.batch) * p.a.q_heads) return;
+    const int qr = int(id - masses), b = qr / p.a.q_heads, qh = qr - b * p.a.q_heads;
     const int h = qh / p.group, j = qh - h * p.group;  // head j of the group
     const Parts pt = parts_of(g, p, b, h * p.head_blocks + (j >> 4));
     if (pt.w1 <= pt.w0) return;  // nothing, or final already
@@ -798,7 +801,7 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(KvGeom g, AttnDev p
     if (p.a.lse && threadIdx.x == 0) p.a.lse[qr] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
     return;
   }
-  const int block = blockIdx.x % mass_blocks, bh = blockIdx.x / mass_blocks;
+  const int block = int(id % mass_blocks), bh = int(id / mass_blocks);
   const int h = bh % g.kv_heads, b = bh / g.kv_heads;
   const Seen rq = seen_by(g, p.a, b, false);
   const int64_t from = int64_t(rq.begin & ~3) + int64_t(block) * kMassTokens;
@@ -887,10 +890,9 @@ template <int D>
 hipError_t launch_d(const KvGeom &g, const AttnDev &p, bool f8, hipStream_t s) {
   const int mass_blocks = p.scores ? (p.a.max_len + 3 + kMassTokens - 1) / kMassTokens : 0;
   const int64_t joins = int64_t(p.a.batch) * p.a.q_heads + int64_t(p.a.batch) * g.kv_heads * mass_blocks;
-  if (joins >= (int64_t(1) << 31)) return hipErrorInvalidValue;
   hipError_t e = f8 ? launch_dt<D, true>(g, p, s) : launch_dt<D, false>(g, p, s);
   if (e != hipSuccess || !p.join) return e;
-  hipLaunchKernelGGL((attn_join_kernel<D>), dim3(unsigned(joins)), dim3(kThreads), 0, s, g, p, mass_blocks);
+  hipLaunchKernelGGL((attn_join_kernel<D>), flat_grid(joins), dim3(kThreads), 0, s, g, p, mass_blocks);
   return hipGetLastError();
 }
 

@@ -3,6 +3,8 @@
 // include/gdn_kv.h.
 #pragma once
 
+#include <algorithm>
+
 #include "common.hpp"
 #include "gdn_kv.h"
 
@@ -58,6 +60,14 @@ __device__ __forceinline__ int kv_row(const KvGeom &g, int slot, int h, int i) {
   return ((page * g.kv_heads + h) << g.page_shift) + (i & ((1 << g.page_shift) - 1));
 }
 
+// A grid of any number of workgroups as two dimensions (a launch holds fewer than 2^32
+// threads in one), and a workgroup's number in it, which may pass the last one.
+inline dim3 flat_grid(int64_t blocks) {
+  const int64_t x = std::min<int64_t>(blocks, 1 << 21);
+  return dim3(unsigned(x), unsigned((blocks + x - 1) / x));
+}
+__device__ __forceinline__ int64_t flat_block() { return int64_t(blockIdx.y) * gridDim.x + blockIdx.x; }
+
 __device__ __forceinline__ void set_err(int32_t *err, int bit) {
   if (err) atomicOr(err, bit);
 }
@@ -67,7 +77,6 @@ struct AppendArgs {
   const int32_t *slot_ids, *index, *position;
   const uint16_t *k, *v;
   int64_t k_stride, v_stride;
-  float k_inv, v_inv;  // set by the launcher
 };
 hipError_t launch_kv_append(const gdn_kv_pool *p, int layer, const AppendArgs &a, hipStream_t s);
 

@@ -13,23 +13,9 @@ namespace {
 // loads, one store each.  Bound by the bytes (and by the launch for one decode step).
 constexpr int kAppendThreads = 256;
 
-// x / scale rounded to fp32 as a division is, from inv = 1 / scale rounded: two steps of
-// q + (x - q scale) inv leave the correctly rounded quotient (Markstein's division), in
-// half the instructions of the general one, which was the larger part of the e4m3 append.
-// Its remainder is exact while nothing over- or underflows: a quotient beyond 512 (or NaN)
-// is only limited below, one far below 2^-10 only rounds to zero, and the host gives inv = 0
-// (plain division) unless scale lies in [2^-60, 2^60].
-__device__ __forceinline__ float quotient(float x, float scale, float inv) {
-  if (inv == 0.f) return x / scale;  // wave-uniform
-  const float q = x * inv;
-  float r = fmaf(fmaf(-q, scale, x), inv, q);
-  r = fmaf(fmaf(-r, scale, x), inv, r);
-  return fabsf(q) < 512.f ? r : q;
-}
-
 // 8 bf16 values / scale, limited to e4m3's largest value, rounded once to nearest even
 // (the limits keep NaN: both comparisons are false)
-__device__ __forceinline__ u32x2 quantise8(const u32x4 &x, float scale, float inv) {
+__device__ __forceinline__ u32x2 quantise8(const u32x4 &x, float scale) {
   u32x2 r;
 #pragma unroll
   for (int p = 0; p < 2; ++p) {
@@ -37,7 +23,7 @@ __device__ __forceinline__ u32x2 quantise8(const u32x4 &x, float scale, float in
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const uint32_t w = x[2 * p + (e >> 1)];
-      float t = quotient(__uint_as_float((e & 1) ? (w & 0xffff0000u) : (w << 16)), scale, inv);
+      float t = __uint_as_float((e & 1) ? (w & 0xffff0000u) : (w << 16)) / scale;
       t = t > 448.f ? 448.f : t;
       f[e] = t < -448.f ? -448.f : t;
     }
@@ -51,9 +37,9 @@ template <bool kF8>
 __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(KvGeom g, int head_dim, AppendArgs a) {
   const int vecs = head_dim >> 3;       // 16-byte pieces of a head's row
   const int per = g.kv_heads * vecs;
-  const int64_t item = int64_t(blockIdx.x) * kAppendThreads + threadIdx.x;
+  const int64_t item = flat_block() * kAppendThreads + threadIdx.x;
+  if (item >= int64_t(a.n) * per) return;
   const int token = int(item / per);
-  if (token >= a.n) return;
   const int j = int(item - int64_t(token) * per);
   const int h = j / vecs, piece = j - h * vecs;
   const int slot = a.slot_ids[token], i = a.index[token];
@@ -75,8 +61,8 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(KvGeom g, int
   }
   if (kF8) {
     const int64_t off = int64_t(row) * head_dim + 8 * piece;
-    *reinterpret_cast<u32x2 *>(g.k + off) = quantise8(kx, g.k_scale, a.k_inv);
-    *reinterpret_cast<u32x2 *>(g.v + off) = quantise8(vx, g.v_scale, a.v_inv);
+    *reinterpret_cast<u32x2 *>(g.k + off) = quantise8(kx, g.k_scale);
+    *reinterpret_cast<u32x2 *>(g.v + off) = quantise8(vx, g.v_scale);
   } else {
     const int64_t off = (int64_t(row) * head_dim + 8 * piece) * 2;
     *reinterpret_cast<u32x4 *>(g.k + off) = kx;
@@ -172,7 +158,9 @@ __global__ __launch_bounds__(THREADS) void kv_evict_plan_kernel(KvGeom g, EvictA
   static_assert(BINS == 1 << kBits, "bins");
   __shared__ PlanShared<THREADS, BINS> sh;
   extern __shared__ uint32_t held[];
-  const int unit = blockIdx.x;
+  const int64_t block = flat_block();
+  if (block >= int64_t(a.layers) * a.batch * g.kv_heads) return;
+  const int unit = int(block);
   const int h = unit % g.kv_heads, lb = unit / g.kv_heads;
   const int b = lb % a.batch, layer = lb / a.batch;
   const int tid = threadIdx.x, lane = tid & 63;
@@ -392,11 +380,13 @@ constexpr int kMoveRows = 4;
 __global__ __launch_bounds__(kMoveThreads) void kv_evict_apply_kernel(KvGeom g, int row_bytes, int units,
                                                                       EvictArgs a) {
   __shared__ int srow[kMoveThreads], drow[kMoveThreads];
-  const int unit = blockIdx.x % units, block = blockIdx.x / units;
+  const int64_t id = flat_block();
+  const int unit = int(id % units), lanes = row_bytes >> 4;  // per row: 4 .. 32
+  const int entries = kMoveRows * kMoveThreads / lanes;      // of this block: 32 .. 256
+  if (id / units * entries >= a.max_moves) return;
+  const int block = int(id / units);
   const int h = unit % g.kv_heads, lb = unit / g.kv_heads;
   const int b = lb % a.batch, layer = lb / a.batch;
-  const int lanes = row_bytes >> 4;                        // per row: 4 .. 32
-  const int entries = kMoveRows * kMoveThreads / lanes;    // of this block: 32 .. 256
   const int first = block * entries;
   // (the entry is read beside the count, not after it: max_moves of them are there)
   const int j = first + threadIdx.x;
@@ -459,13 +449,9 @@ __global__ __launch_bounds__(kMoveThreads) void kv_evict_apply_kernel(KvGeom g, 
 
 }  // namespace
 
-hipError_t launch_kv_append(const gdn_kv_pool *p, int layer, const AppendArgs &args, hipStream_t s) {
-  const auto inverse = [](float x) { return x >= 0x1p-60f && x <= 0x1p60f ? 1.f / x : 0.f; };
-  AppendArgs a = args;
-  a.k_inv = inverse(p->d.k_scale);
-  a.v_inv = inverse(p->d.v_scale);
+hipError_t launch_kv_append(const gdn_kv_pool *p, int layer, const AppendArgs &a, hipStream_t s) {
   const int64_t items = int64_t(a.n) * p->d.kv_heads * (p->d.head_dim >> 3);
-  const dim3 grid(unsigned((items + kAppendThreads - 1) / kAppendThreads));
+  const dim3 grid = flat_grid((items + kAppendThreads - 1) / kAppendThreads);
   const KvGeom g = kv_geom(p, layer);
   if (p->d.kv_dtype == GDN_BF16)
     hipLaunchKernelGGL((kv_append_kernel<false>), grid, dim3(kAppendThreads), 0, s, g, p->d.head_dim, a);
@@ -479,7 +465,7 @@ template <int THREADS, bool kHeld, int BINS, int U>
 hipError_t launch_plan(const KvGeom &g, const EvictArgs &a, hipStream_t s) {
   constexpr int step = U * THREADS;
   const size_t held = kHeld ? size_t((a.max_len + step - 1) / step) * step * 4 : 0;
-  hipLaunchKernelGGL((kv_evict_plan_kernel<THREADS, kHeld, BINS, U>), dim3(unsigned(a.layers * a.batch * g.kv_heads)),
+  hipLaunchKernelGGL((kv_evict_plan_kernel<THREADS, kHeld, BINS, U>), flat_grid(int64_t(a.layers) * a.batch * g.kv_heads),
                      dim3(THREADS), held, s, g, a);
   return hipGetLastError();
 }
@@ -495,9 +481,8 @@ hipError_t launch_kv_evict_plan(const gdn_kv_pool *p, int layer, const EvictArgs
 hipError_t launch_kv_evict_apply(const gdn_kv_pool *p, int layer, const EvictArgs &a, hipStream_t s) {
   const int units = a.layers * a.batch * p->d.kv_heads;
   const int entries = kMoveRows * kMoveThreads / (p->row_bytes >> 4);
-  const int64_t blocks = (a.max_moves + entries - 1) / entries;
-  if (blocks * units >= (int64_t(1) << 31)) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(kv_evict_apply_kernel, dim3(unsigned(blocks * units)), dim3(kMoveThreads), 0, s,
+  const int64_t blocks = (int64_t(a.max_moves) + entries - 1) / entries;
+  hipLaunchKernelGGL(kv_evict_apply_kernel, flat_grid(blocks * units), dim3(kMoveThreads), 0, s,
                      kv_geom(p, layer), p->row_bytes, units, a);
   return hipGetLastError();
 }

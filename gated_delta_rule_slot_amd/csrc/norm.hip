@@ -76,7 +76,7 @@ __global__ __launch_bounds__((LANES > kNormThreads ? LANES : kNormThreads)) void
     NormArgs a, int64_t rows) {
   constexpr int THREADS = LANES > kNormThreads ? LANES : kNormThreads;
   __shared__ float red[LANES > 64 ? LANES / 64 : 1];
-  const int64_t row = int64_t(blockIdx.x) * (THREADS / LANES) + threadIdx.x / LANES;
+  const int64_t row = flat_block() * (THREADS / LANES) + threadIdx.x / LANES;
   const bool live = row < rows;  // uniform over a row's threads
   const int l = threadIdx.x % LANES;
   const int64_t r0 = live ? row : 0;
@@ -181,7 +181,7 @@ template <int LANES, int VPT>
 hipError_t launch_rows(const NormArgs &a, hipStream_t s) {
   constexpr int THREADS = LANES > kNormThreads ? LANES : kNormThreads;
   const int64_t rows = a.tokens * a.groups, per = THREADS / LANES;
-  const dim3 grid(unsigned((rows + per - 1) / per));
+  const dim3 grid = flat_grid((rows + per - 1) / per);
   // From 24 MB a tensor on: 4096 rows of 4096 (33 MB) 27.5 against 30.2 us, 8192 of 2048 32.5
   // against 36.9 us; below, the next kernel finds the rows in the caches (19 MB: no gain,
   // 128 rows of 2048: 4.4 against 4.1 us).

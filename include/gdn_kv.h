@@ -78,7 +78,7 @@ gdn_status kv_pool_bytes(const gdn_kv_desc *desc, size_t *kv_bytes, size_t *mass
 
 /* Validate a descriptor and wrap it in a handle (host memory only; the buffers stay the
  * caller's).  Supported: head_dim in {64, 128, 256}, page_size a power of two in
- * [1, 1024], pages >= 2, slots >= 2, max_pages * page_size < 2^31 and
+ * [1, 1024], pages >= 2, slots >= 2, max_pages * page_size < 2^30 and
  * pages * kv_heads * page_size < 2^31.  Thread-safe; the handle is immutable. */
 gdn_status kv_pool_create(const gdn_kv_desc *desc, gdn_kv_pool_t *out);
 
@@ -121,10 +121,10 @@ gdn_status attn_workspace_bytes(gdn_kv_pool_t pool, int32_t batch, int32_t q_hea
  *             window
  * q           device bf16, request b at q + b * q_stride (elements, a multiple of 8, at
  *             least q_heads * head_dim; 16-byte aligned), [q_heads][head_dim] there
- * scale       any finite value
+ * scale       |scale * k_scale| at most 1e30
  * flags       GDN_F_ACCUM_MASS: add the weights to the pool's mass (which it must have;
  *             live slots must be distinct then).  Only visible tokens' entries change
- * out         device bf16 [batch][q_heads][head_dim], 16-byte aligned
+ * out         device bf16 [batch][q_heads][head_dim], 16-byte aligned, apart from q
  * lse         device fp32 [batch][q_heads] or NULL
  * workspace   attn_workspace_bytes(...) bytes, 256-byte aligned; its contents are not
  *             read across calls

@@ -104,6 +104,22 @@ def test_block_norm_streamed():
     check(c, *run(c, in_place=True))
 
 
+def test_block_norm_of_more_rows_than_one_grid_dimension_takes():
+    """2.1 M rows of a workgroup each, bit for bit what smaller calls give."""
+    import gated_delta_rule_slot_amd as gdn
+
+    T, D = (1 << 21) + 3, 520
+    y = torch.randn(T, 1, D, device="cuda", generator=torch.Generator(device="cuda").manual_seed(2)).to(torch.bfloat16)
+    w = torch.rand(D, device="cuda")
+    out = torch.full_like(y, -7.0)
+    gdn.block_norm(y, out, w_post=w)
+    part = torch.empty(4096, 1, D, dtype=torch.bfloat16, device="cuda")
+    for t in (0, 1 << 20, T - 4096):
+        gdn.block_norm(y[t:t + 4096], part, w_post=w)
+        assert torch.equal(out[t:t + 4096], part), t
+    assert not (out == -7.0).all(dim=-1).any()
+
+
 @pytest.mark.parametrize("std,eps", [(1e-18, 1e-6), (1e-3, 1e-5), (1e15, 1e-6), (0.0, 1e-6)])
 def test_block_norm_small_large_and_zero_rows(std, eps):
     """Rows whose squares leave bf16's comfortable range, and rows of zeros."""

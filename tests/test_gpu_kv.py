@@ -187,6 +187,52 @@ def test_attention_without_err_word_and_lse():
     check_attention(c, q, sc, out)
 
 
+@pytest.mark.parametrize("batch,mass", [(255, True), (257, False), (700, True)])
+def test_attention_many_requests(batch, mass):
+    """More requests than one step of the length scan takes, with empty and skipped ones
+    between them."""
+    r = np.random.default_rng(batch)
+    lens = [int(x) for x in r.integers(0, 60, size=batch)]
+    lens[batch // 2] = 900
+    slots = [int(x) + 1 for x in r.permutation(batch)]
+    for b in range(3, batch, 7):
+        slots[b] = -(b % 2)
+    c = make_cache(batch, lens, None, 1, 64, 16, slots=slots)
+    pool, q, out, lse, sc = run_attention(c, 3, mass=mass)
+    check_attention(c, q, sc, out, lse, pool.mass if mass else None, c.mass)
+    assert int(pool.err_word.item()) == 0
+
+
+def test_attention_largest_batch():
+    """65535 requests of 64 heads (more joins than one grid dimension takes) over the same
+    rows, against a float64 softmax on the device for some of them."""
+    import gated_delta_rule_slot_amd as gdn
+
+    B, Hq, D, n = 65535, 64, 64, 130
+    g = torch.Generator(device="cuda").manual_seed(3)
+    k = torch.randn(1, 20, 1, 16, D, device="cuda", generator=g).to(torch.bfloat16)
+    v = torch.randn(1, 20, 1, 16, D, device="cuda", generator=g).to(torch.bfloat16)
+    table = (torch.arange(9, device="cuda", dtype=torch.int32) + 2).expand(B + 1, 9).contiguous()
+    pool = gdn.kv_pool_create(k, v, table)
+    q = torch.randn(B, Hq, D, device="cuda", generator=g).to(torch.bfloat16)
+    lens = (torch.arange(B, device="cuda", dtype=torch.int32) % (n + 1))
+    out = torch.full((B, Hq, D), -7.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(gdn.attn_workspace_bytes(pool, B, Hq, n), dtype=torch.uint8, device="cuda")
+    gdn.attn_decode_paged(pool, 0, torch.arange(1, B + 1, dtype=torch.int32, device="cuda"), lens, q, out, n, scale=0.125,
+                          workspace=ws)
+    rows_k, rows_v = (t[0, 2:11, 0].reshape(-1, D).double() for t in (k, v))
+    for b in list(range(0, 262)) + list(range(0, B, 997)) + list(range(B - 132, B)):
+        m = int(lens[b])
+        got = out[b].double()
+        if m == 0:
+            assert not got.any(), b
+            continue
+        p = torch.softmax(0.125 * q[b].double() @ rows_k[:m].t(), -1)
+        want = p @ rows_v[:m]
+        # 2^-8 for bf16; 2^-12 of sum p |v| covers kv_helpers.attn_slack for these sizes
+        assert ((got - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -12 * (p @ rows_v[:m].abs())).all(), b
+
+
 @pytest.mark.parametrize("f8", [False, True])
 def test_offsets_past_32_bits(f8):
     """Pages at the far end of a cache of more than 2^32 bytes, through append, attention
@@ -472,6 +518,49 @@ def test_apply_skips_and_flags():
     assert call([1, 2], [2, 2], bad) == (gdn.ERRW_BAD_SEQLENS, True)
     assert call([0, 2], [0, 2], [two[0], [[50, 1], [2, 48]]]) == (gdn.ERRW_BAD_PAGE, True)
     assert call([1, 0], [1, 0], two) == (0, False)  # a good one moves
+
+
+def test_append_and_eviction_of_more_workgroups_than_one_grid_dimension_takes():
+    import gated_delta_rule_slot_amd as gdn
+
+    # 2^21 workgroups of 256 threads and some: 67.2 M tokens of one head of 64
+    n, S = (1 << 26) + 100000, 1024
+    pages = -(-n // S) + 1
+    x = torch.empty(n, 1, 64, dtype=torch.bfloat16, device="cuda")
+    x.view(torch.int32).view(n, 32)[:] = torch.arange(n, dtype=torch.int32, device="cuda")[:, None]
+    k = torch.zeros(1, pages, 1, S, 64, dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").expand(2, pages)[:, 1:].contiguous()
+    pool = gdn.kv_pool_create(k, v, table)
+    at = torch.arange(n, dtype=torch.int32, device="cuda")
+    gdn.kv_append(pool, 0, torch.ones(n, dtype=torch.int32, device="cuda"), at, x, x)
+    for t in (k, v):
+        assert torch.equal(t[0, 1:].view(-1, 64)[:n].view(torch.int32), x.view(n, 64).view(torch.int32))
+        assert not t[0, 1:].view(-1, 64)[n:].any()
+    del k, v, x, pool, at, table
+    torch.cuda.empty_cache()
+
+    # 2.1 M lists of one move each: 64 layers, 4100 requests, 8 heads, 17 tokens, budget 16
+    L, B, H = 64, 4100, 8
+    g = torch.Generator(device="cuda").manual_seed(1)
+    k = torch.zeros(L, 2, H, 32, 64, dtype=torch.float8_e4m3fn, device="cuda")
+    mass = torch.rand(L, B + 1, H, 32, device="cuda", generator=g) + 0.1
+    pos = torch.arange(32, dtype=torch.int32, device="cuda").expand(L, B + 1, H, 32).contiguous()
+    low = torch.randint(0, 16, (L, B, H, 1), device="cuda", generator=g)
+    mass[:, 1:, :, :17].scatter_(3, low, 0.01)
+    table = torch.ones(B + 1, 1, dtype=torch.int32, device="cuda")
+    pool = gdn.kv_pool_create(k, torch.zeros_like(k), table, mass=mass, pos=pos)
+    slots = torch.arange(1, B + 1, dtype=torch.int32, device="cuda")
+    nm = torch.zeros(L, B, H, dtype=torch.int32, device="cuda")
+    mv = torch.zeros(L, B, H, 1, 2, dtype=torch.int32, device="cuda")
+    lo = torch.zeros(B, dtype=torch.int32, device="cuda")
+    lens = torch.full((B,), 17, dtype=torch.int32, device="cuda")
+    gdn.kv_evict_plan(pool, 0, L, slots, lens, lens + 100, 17, 16, 0, 0, nm, mv, lo)
+    assert (nm == 1).all() and (lo == 16).all() and (mv[..., 0] == 16).all() and torch.equal(mv[..., 1].long(), low)
+    want = pos[:, 1:].clone().scatter_(3, low, 16)
+    # (the rows are all in one page and all zero: mass and pos show what was moved)
+    gdn.kv_evict_apply(pool, 0, L, slots, nm, mv)
+    assert torch.equal(pos[:, 1:], want) and (mass[:, 1:, :, :17] > 0.05).all()
 
 
 # ------------------------------------------------------- together, as used --

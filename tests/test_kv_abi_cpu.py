@@ -46,7 +46,7 @@ def test_sizes():
     (dict(layers=0), -1), (dict(kv_heads=0), -1), (dict(max_pages=0), -1), (dict(pages=1), -1),
     (dict(slots=1), -1), (dict(kv_dtype=B.GDN_F32), -1), (dict(kv_dtype=7), -1),
     (dict(head_dim=32), -3), (dict(head_dim=96), -3), (dict(page_size=24), -3), (dict(page_size=2048), -3),
-    (dict(page_size=0), -3), (dict(max_pages=1 << 27), -3), (dict(pages=1 << 26), -3),
+    (dict(page_size=0), -3), (dict(max_pages=1 << 26), -3), (dict(pages=1 << 26), -3),
     (dict(pages=1 << 30, kv_heads=4), -3), (dict(kv_heads=70000), -3),
     (dict(k_base=None), -1), (dict(v_base=None), -1), (dict(page_table=None), -1),
     (dict(k_base=P + 8), -3), (dict(page_table=P + 2), -1), (dict(mass=P + 1), -1), (dict(err_word=P + 2), -1),
@@ -86,6 +86,7 @@ NORM = dict(tokens=4, groups=2, dim=64, y=P, ys=128, w_post=P, gate=P, gs=128, a
     ("attn_decode_paged", ATTN, dict(q_heads=130, qs=1 << 14), -3),
     ("attn_decode_paged", ATTN, dict(max_len=81), -2), ("attn_decode_paged", ATTN, dict(max_len=-1), -2),
     ("attn_decode_paged", ATTN, dict(flags=2), -1), ("attn_decode_paged", ATTN, dict(scale=float("nan")), -1),
+    ("attn_decode_paged", ATTN, dict(scale=float("-inf")), -1), ("attn_decode_paged", ATTN, dict(scale=-2e30), -1),
     ("attn_decode_paged", ATTN, dict(slot_table=None), -1), ("attn_decode_paged", ATTN, dict(kv_len=None), -1),
     ("attn_decode_paged", ATTN, dict(q=None), -1), ("attn_decode_paged", ATTN, dict(out=None), -1),
     ("attn_decode_paged", ATTN, dict(qs=248), -1), ("attn_decode_paged", ATTN, dict(qs=260), -3),
