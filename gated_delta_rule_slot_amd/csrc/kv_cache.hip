@@ -189,22 +189,29 @@ __global__ __launch_bounds__(THREADS) void kv_evict_plan_kernel(KvGeom g, EvictA
   // Key of place i.  One behind the last token has key 0 and needs no test in the passes:
   // it is not below budget, so not freed; it comes after all ties; and a key of 0 is only
   // ever kept as a tie.
-  auto load_keys = [&](int i0, auto count, uint32_t *out) {
+  const char *mass_bytes = reinterpret_cast<const char *>(mass), *pos_bytes = reinterpret_cast<const char *>(pos);
+  auto load_some = [&](int i0, auto count, auto inside, uint32_t *out) {
     constexpr int N = decltype(count)::value;
+    constexpr bool kInside = decltype(inside)::value;  // all of these places are in the cache
     float m[N];
     int32_t p[N];
 #pragma unroll
-    for (int q = 0; q < N; ++q) {
-      const int at = min(i0 + 64 * q + lane, n - 1);
-      m[q] = mass[at];
-      p[q] = pos[at];
+    for (int q = 0; q < N; ++q) {  // (a 32-bit offset to a scalar base; capacity < 2^30)
+      const int i = i0 + 64 * q + lane;
+      const uint32_t at = 4u * uint32_t(kInside ? i : min(i, n - 1));
+      m[q] = *reinterpret_cast<const float *>(mass_bytes + at);
+      p[q] = *reinterpret_cast<const int32_t *>(pos_bytes + at);
     }
 #pragma unroll
     for (int q = 0; q < N; ++q) {
       const uint32_t key = m[q] > 0.f ? __float_as_uint(m[q]) : 0u;
       const bool safe = (p[q] < a.sink) | (p[q] >= from);
-      out[q] = i0 + 64 * q + lane >= n ? 0u : safe ? kProtected : key;
+      out[q] = !kInside && i0 + 64 * q + lane >= n ? 0u : safe ? kProtected : key;
     }
+  };
+  auto load_keys = [&](int i0, auto count, uint32_t *out) {
+    if (THREADS > 256 && i0 + 64 * decltype(count)::value <= n) load_some(i0, count, std::true_type{}, out);
+    else load_some(i0, count, std::false_type{}, out);
   };
   // f(first token, key) for this wave's rounds in order
   auto each = [&](auto f) {
