@@ -23,11 +23,17 @@
 // The work is counted in blocks of 128 tokens (4 waves, a tile each), in the order
 // (request, key-value head, 16 query heads, position), and every workgroup takes an equal
 // run of blocks: as many workgroups as run at once, whatever the requests' lengths.  (Equal
-// splits of the longest length left a third of the chip waiting for a ragged batch.)  A
-// workgroup finds its run from the lengths on the device, walks it unit by unit, and
+// splits of the longest length, at the best number of them, took 138 us for a ragged batch
+// where equal runs took 131.)  A workgroup finds its run from the lengths on the device, walks it unit by unit, and
 // joins its waves in shared memory at the end of each unit.  A unit that lies in
 // one workgroup is final there; of the others m, l and O go to the workspace, and a second
 // kernel joins them (and adds up the weights, from stored scores).
+//
+// Measured on MI355X (both kernels; scaling 4 GiB in place runs at 5.9 TB/s there): 4 requests of
+// 90001-131072 tokens, 2 heads of 256, 956 MB: 152 us, 6.3 TB/s; 128 of 150-4099 tokens with
+// weights, 547 MB: 110-114 us, 4.8-5.0 TB/s (join and weights 8.6 us of it); e4m3 in 16-token
+// pages, 64 of 1000-8192 tokens in a 4096-token window, 8 heads of 128, 460 MB: 81-87 us; one
+// of 777 tokens: 10.4 + 3.9 us, a chain of dependent reads (lengths, page ids, keys).
 #include <algorithm>
 #include <type_traits>
 
