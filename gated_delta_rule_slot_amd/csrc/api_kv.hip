@@ -17,6 +17,21 @@ gdn_status ok() { return gdn::clear_error(); }
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Memory of n >= 1 rows of `row` bytes, one every `stride` (>= row) bytes
+struct Rows {
+  const void *base;
+  int64_t n, row, stride;
+};
+
+// whether a row of `a` shares a byte with [p, p + bytes)
+bool overlap(const Rows &a, const void *p, int64_t bytes) {
+  if (!a.base || !p) return false;
+  const __int128 base = reinterpret_cast<uintptr_t>(a.base), lo = reinterpret_cast<uintptr_t>(p);
+  const __int128 before = lo - base - a.row;  // the first row that ends behind lo
+  const __int128 i = before < 0 ? 0 : before / a.stride + 1;
+  return i < a.n && base + i * a.stride < lo + bytes;
+}
+
 gdn_status launched(hipError_t e, const char *what) {
   if (e != hipSuccess) return fail(GDN_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
   return ok();
@@ -172,6 +187,9 @@ GDN_API gdn_status attn_decode_paged(gdn_kv_pool_t pool, int32_t layer, int32_t 
     return fail(GDN_ERR_ARG, "workspace of %zu bytes is below the needed %zu", workspace_bytes, need);
   if (need && !aligned(workspace, 256))
     return fail(GDN_ERR_UNSUPPORTED, "workspace must be 256-byte aligned");
+  const int64_t row = int64_t(q_heads) * pool->d.head_dim * 2;
+  if (overlap({q, batch, row, q_stride * 2}, out, batch * row))
+    return fail(GDN_ERR_ARG, "out overlaps q");
   gdn::AttnArgs a{batch, q_heads, max_len, slot_table, kv_len, kv_begin, q,
                   q_stride, scale, flags, out, lse, workspace};
   return launched(gdn::launch_attn_decode(pool, layer, a, static_cast<hipStream_t>(stream)),
@@ -212,6 +230,8 @@ GDN_API gdn_status kv_evict_apply(gdn_kv_pool_t pool, int32_t layer_begin, int32
   if (s != GDN_OK) return s;
   if (max_moves < 0 || max_moves > pool->capacity)
     return fail(GDN_ERR_RANGE, "max_moves %d outside [0, %d]", max_moves, pool->capacity);
+  if (int64_t(layer_end - layer_begin) * batch * pool->d.kv_heads * max_moves >= int64_t(1) << 40)
+    return fail(GDN_ERR_RANGE, "layers * batch * kv_heads * max_moves must be below 2^40");
   if (batch == 0 || layer_begin == layer_end || max_moves == 0) return ok();
   if (!slot_table || !n_moves || !moves) return fail(GDN_ERR_ARG, "a required pointer is NULL");
   gdn::EvictArgs a{};
@@ -259,6 +279,22 @@ GDN_API gdn_status block_norm(int64_t tokens, int32_t groups, int32_t dim, const
   for (const void *p : {static_cast<const void *>(y), w_post, static_cast<const void *>(gate), residual,
                         static_cast<const void *>(residual_out), w_pre, static_cast<const void *>(out)})
     if (!aligned(p, 16)) return fail(GDN_ERR_UNSUPPORTED, "pointers must be 16-byte aligned");
+  // a thread reads its own elements before it writes them: the same memory works where the
+  // header says so, a shifted one does not
+  const Rows yr{y, tokens, row * 2, y_stride * 2}, gr{gate, tokens, row * 2, gate_stride * 2};
+  const int64_t out_bytes = tokens * row * 2, res_bytes = tokens * row * (res_dtype == GDN_F32 ? 4 : 2);
+  const int64_t w_bytes = int64_t(dim) * (w_dtype == GDN_F32 ? 4 : 2);
+  const Rows wr[2] = {{w_post, 1, w_bytes, w_bytes}, {w_pre, 1, w_bytes, w_bytes}};
+  const Rows rr{residual, 1, res_bytes, res_bytes};
+  if (!(out == y && (y_stride == row || tokens == 1)) && overlap(yr, out, out_bytes))
+    return fail(GDN_ERR_ARG, "out overlaps y (only out = y with y_stride = groups * dim may)");
+  if (overlap(gr, out, out_bytes) || overlap(rr, out, out_bytes) || overlap(wr[0], out, out_bytes) ||
+      overlap(wr[1], out, out_bytes) || overlap({residual_out, 1, res_bytes, res_bytes}, out, out_bytes))
+    return fail(GDN_ERR_ARG, "out overlaps gate, a weight, residual or residual_out");
+  if (overlap(yr, residual_out, res_bytes) || overlap(gr, residual_out, res_bytes) ||
+      overlap(wr[0], residual_out, res_bytes) || overlap(wr[1], residual_out, res_bytes) ||
+      (residual_out != residual && overlap(rr, residual_out, res_bytes)))
+    return fail(GDN_ERR_ARG, "residual_out overlaps y, gate, a weight or part of residual");
   gdn::NormArgs a{tokens, groups, dim, y, y_stride, w_post, gate, gate_stride, act, scale, residual,
                   residual_out, res_dtype, w_pre, w_dtype, eps, flags, out};
   return launched(gdn::launch_block_norm(a, static_cast<hipStream_t>(stream)), "block_norm launch");

@@ -124,7 +124,7 @@ gdn_status attn_workspace_bytes(gdn_kv_pool_t pool, int32_t batch, int32_t q_hea
  * scale       |scale * k_scale| at most 1e30
  * flags       GDN_F_ACCUM_MASS: add the weights to the pool's mass (which it must have;
  *             live slots must be distinct then).  Only visible tokens' entries change
- * out         device bf16 [batch][q_heads][head_dim], 16-byte aligned, apart from q
+ * out         device bf16 [batch][q_heads][head_dim], 16-byte aligned; must not overlap q
  * lse         device fp32 [batch][q_heads] or NULL
  * workspace   attn_workspace_bytes(...) bytes, 256-byte aligned; its contents are not
  *             read across calls
@@ -168,7 +168,8 @@ gdn_status kv_evict_plan(gdn_kv_pool_t pool, int32_t layer_begin, int32_t layer_
  * source or another destination of it (a plan's never are), live slots must be distinct, and
  * the pages written must belong to their request alone.  A count outside
  * [0, max_moves] sets GDN_ERRW_BAD_SEQLENS and skips that list; an index outside
- * [0, max_pages * page_size) does and skips the entry. */
+ * [0, max_pages * page_size) does and skips the entry.  layers * batch * kv_heads *
+ * max_moves is below 2^40. */
 gdn_status kv_evict_apply(gdn_kv_pool_t pool, int32_t layer_begin, int32_t layer_end,
                           int32_t batch, int32_t max_moves, const int32_t *slot_table,
                           const int32_t *n_moves, const int32_t *moves, void *stream);

@@ -184,3 +184,26 @@ def test_output_norm_of_the_recurrence():
     c = case(10, B, H, D, True, "silu", None, False)
     c["y"] = o.cpu().view(B, H * D)
     check(c, *run(c))
+
+
+def test_block_norm_output_between_wide_rows():
+    """out in the gap that y's rows leave in one buffer is apart from y, and equals the
+    result of memory of its own; one that reaches into the next row is refused."""
+    import gated_delta_rule_slot_amd as gdn
+
+    T, G, D = 3, 2, 64
+    n = T * G * D
+    g = torch.Generator().manual_seed(31)
+    buf = torch.randn(T, G * D + n + 8, generator=g).to(torch.bfloat16).cuda()
+    y = buf[:, :G * D].view(T, G, D)
+    w = torch.rand(D, generator=g).cuda()
+    keep, own = buf.clone(), torch.empty(T, G, D, dtype=torch.bfloat16, device="cuda")
+    gdn.block_norm(y, own, w_pre=w)
+    gap = buf[1, G * D:G * D + n]
+    gdn.block_norm(y, gap.view(T, G, D), w_pre=w)
+    assert torch.equal(gap.view(T, G, D), own)
+    keep[1, G * D:G * D + n] = own.flatten()
+    assert torch.equal(buf, keep)
+    with pytest.raises(Exception, match="out overlaps y"):
+        gdn.block_norm(y, buf.flatten()[G * D + 16:G * D + 16 + n].view(T, G, D), w_pre=w)
+    assert torch.equal(buf, keep)

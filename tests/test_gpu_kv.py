@@ -730,3 +730,23 @@ def test_calls_on_other_streams():
     torch.cuda.synchronize()
     for i in range(2):
         check_attention(c, q[i].cpu(), 0.1, out[i])
+
+
+def test_attention_output_between_wide_q_rows():
+    """out in the gap that q's rows leave in one buffer is apart from q."""
+    import gated_delta_rule_slot_amd as gdn
+
+    c = make_cache(77, [40, 129, 3], None, 2, 64, 16, False)
+    B, Hq = 3, 6
+    n = B * Hq * c.dim
+    g = torch.Generator().manual_seed(78)
+    buf = torch.randn(B, Hq * c.dim + n, generator=g).to(torch.bfloat16).cuda()
+    q = buf[:, :Hq * c.dim].view(B, Hq, c.dim)
+    keep = q.cpu()
+    out = buf[1, Hq * c.dim:].view(B, Hq, c.dim)
+    pool = device_pool(c)
+    need = gdn.attn_workspace_bytes(pool, B, Hq, 129)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda") if need else None
+    gdn.attn_decode_paged(pool, c.layer, i32(c.slots), i32(c.lens), q, out, 129, scale=0.125, workspace=ws)
+    check_attention(c, keep, 0.125, out)
+    assert torch.equal(q.cpu(), keep)

@@ -125,6 +125,50 @@ def test_block_norm_refuses_before_launch(kw, status):
     assert B._lib.block_norm(*dict(NORM, **kw).values()) == status, B.last_error()
 
 
+Q, F = 4 * 128 * 2, 4 * 128 * 4  # bytes of NORM's rows in bf16 and fp32
+APART = dict(y=P, w_post=P + 0x10000, gate=P + 0x20000, res=P + 0x30000, res_out=P + 0x30000, w_pre=P + 0x40000,
+             out=P + 0x50000)
+
+
+@pytest.mark.parametrize("kw,what", [
+    (dict(out=P, ys=136), "out overlaps y"), (dict(out=P + 16), "out overlaps y"),
+    (dict(out=P - 16), "out overlaps y"), (dict(out=P + Q - 16), "out overlaps y"),
+    (dict(out=P - Q + 16), "out overlaps y"), (dict(tokens=1, out=P + 240), "out overlaps y"),
+    (dict(out=P + 1792, ys=1024, tokens=2), "out overlaps y"),
+    (dict(out=P, res=None, res_out=None, y=P + 16), "out overlaps y"),
+    (dict(out=APART["gate"]), "out overlaps gate"), (dict(out=APART["res"]), "out overlaps gate"),
+    (dict(out=APART["res"], res=P + 0x60000), "out overlaps gate"),
+    (dict(out=APART["res"] + F - 16, rt=B.GDN_F32), "out overlaps gate"),
+    (dict(out=APART["w_post"] + 240), "out overlaps gate"), (dict(out=APART["w_pre"]), "out overlaps gate"),
+    (dict(res_out=P), "residual_out overlaps"), (dict(res_out=APART["gate"]), "residual_out overlaps"),
+    (dict(res_out=APART["res"] + 16), "residual_out overlaps"),
+    (dict(res_out=APART["res"] + F - 16, rt=B.GDN_F32), "residual_out overlaps"),
+    (dict(res_out=APART["w_pre"] - 16), "residual_out overlaps"),
+])
+def test_block_norm_refuses_overlaps(kw, what):
+    a = {**NORM, **APART, **kw}
+    assert B._lib.block_norm(*a.values()) == -1
+    assert B.last_error().startswith(what)
+
+
+@pytest.mark.parametrize("off,qs", [(0, 256), (16, 256), (1024 - 16, 256), (-1024 + 16, 256), (1024 - 16, 512),
+                                    (512, 512), (0, 512)])
+def test_attention_refuses_out_over_q(pool, off, qs):
+    a = dict(ATTN, q=P, qs=qs, out=P + off, ws=P + 0x100000)
+    assert B._lib.attn_decode_paged(pool, *a.values()) == -1
+    assert "out overlaps q" in B.last_error()
+
+
+def test_apply_refuses_lists_past_any_grid():
+    st, h = make(layers=1 << 14, pages=2, kv_heads=2, max_pages=1 << 25, page_size=16)
+    assert st == 0, B.last_error()
+    try:
+        a = dict(APPLY, le=1 << 14, batch=1 << 10, max_moves=1 << 20)
+        assert B._lib.kv_evict_apply(h, *a.values()) == -2 and "2^40" in B.last_error()
+    finally:
+        B._lib.kv_pool_destroy(h)
+
+
 def test_null_pool_and_missing_mass():
     st, h = make(mass=None, pos=None)
     assert st == 0
