@@ -24,10 +24,10 @@
 // (request, key-value head, 16 query heads, position), and every workgroup takes an equal
 // run of blocks: as many workgroups as run at once, whatever the requests' lengths.  (Equal
 // splits of the longest length, at the best number of them, took 138 us for a ragged batch
-// where equal runs took 131.)  A workgroup finds its run from the lengths on the device, walks it unit by unit, and
-// joins its waves in shared memory at the end of each unit.  A unit that lies in
-// one workgroup is final there; of the others m, l and O go to the workspace, and a second
-// kernel joins them (and adds up the weights, from stored scores).
+// where equal runs took 131.)  A workgroup finds its run from the lengths on the device, walks
+// it unit by unit, and joins its waves in shared memory at the end of each unit.  A unit that
+// lies in one workgroup is final there; of the others m, l and O go to the workspace, and a
+// second kernel joins them (and adds up the weights, from stored scores).
 //
 // Measured on MI355X (both kernels; scaling 4 GiB in place runs at 5.9 TB/s there): 4 requests of
 // 90001-131072 tokens, 2 heads of 256, 956 MB: 152 us, 6.3 TB/s; 128 of 150-4099 tokens with
@@ -129,9 +129,9 @@ __device__ __forceinline__ float ref(float m) { return m == kNegInf ? 0.f : m; }
 // What a sum taken under the maximum m is worth under the larger maximum to.
 __device__ __forceinline__ float factor(float m, float to) { return m == kNegInf ? 0.f : fexp2(m - to); }
 
-// Element types.  kWords: 32-bit words of one lane's piece of a row.
-//   K: piece s of a row (4 lanes of different g side by side): the k indices of kSteps
-//      MFMA steps.  V: the D / 16 columns of a lane, as bf16 words after conversion.
+// How a lane reads rows of D values.  Keys: kPieces times 16 bytes, those of the four lane
+// groups side by side; a piece of bf16 is the k indices of one MFMA step, one of e4m3 of
+// two.  Values: kVPieces times kVWords words, the lane's D / 16 columns.
 typedef uint32_t u32;
 template <int D, bool kF8>
 struct Lay;
@@ -186,9 +186,8 @@ __device__ __forceinline__ void f8_to_bf16(u32 x, u32 *lo, u32 *hi) {
 }
 
 // kWide: pages hold 16 tokens or more, so each half of a tile has adjacent rows and one
-// wave-uniform page id; otherwise each token's row is looked up,
-// about a tenth slower (128 requests of 2048 tokens, 4 heads of 128: 4-token pages 96.8 us,
-// 16-token pages 91.3 us).
+// wave-uniform page id; otherwise each token's row is looked up (128 requests of 2048 tokens,
+// 4 heads of 128: 4-token pages 96.8 us, 16-token pages 91.3 us).
 //
 // The keys and values of a wave's next tile are asked for while the present one is worked
 // on, also over the end of a unit: under load a dependent read takes 5 us and more, so a
@@ -223,12 +222,11 @@ void attn_decode_kernel(KvGeom g, AttnDev p) {
   // reads are scalar loads, which the waits for keys and values do not count)
   typedef const int32_t __attribute__((address_space(4))) *table_t;
   auto request = [&](int r) -> Seen {
-    AttnArgs a = p.a;
     Seen v;
-    v.slot = ((table_t)a.slot_table)[r];
-    v.len = ((table_t)a.kv_len)[r];
-    v.begin = a.kv_begin ? ((table_t)a.kv_begin)[r] : 0;
-    v.blocks = blocks_of(g, a, v);
+    v.slot = ((table_t)p.a.slot_table)[r];
+    v.len = ((table_t)p.a.kv_len)[r];
+    v.begin = p.a.kv_begin ? ((table_t)p.a.kv_begin)[r] : 0;
+    v.blocks = blocks_of(g, p.a, v);
     return v;
   };
 
