@@ -86,17 +86,21 @@ __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(KvGeom g, int
 // The threshold key is found by narrowing a key range [lo, hi]: each round counts the
 // range's keys in up to BINS equal bins (shared memory), finds the bin that holds the
 // k-th largest and takes it as the next range, and stops early where a whole bin is kept.
-// The first range is the smallest and largest weight above 0, so the bins spread over the
-// exponents that occur; a threshold among the weights of 0 is seen at once.
+// The first round's range is all weights above 0 (8 bins, or 4, an octave), so it counts
+// while the keys are loaded; a threshold among the weights of 0 is seen at once.
 //
 // Every wave owns a run of adjacent tokens, so the order of the lists needs no barrier per
-// 64 tokens: a wave counts its ties (and then its freed places and tokens to move) by
-// ballots, one sum over the waves gives each its start, and it walks its run again.
+// 64 tokens: a wave puts the places that it takes, the freed ones and then the tokens to
+// move, side by side over its own keys, one sum over the waves gives each its start, and it
+// writes its places out 64 at a time.
 //
-// Measured: 512 lists of 1020-1088 tokens 6.7 us (4 MB: latency); 128 lists of 32769
-// tokens and fewer 26.8 us (39 MB, 6.6 us at the rate of reads): the passes' vector
-// instructions and shared-memory atomics on the half of the compute units that have a list.
-// Keys in registers with unrolled passes took 31.7 us, reading them again 61 us.
+// Measured: 512 lists of 1020-1088 tokens 6.8 us (4 MB: latency); 128 lists of 32769
+// tokens and fewer 21 us (39 MB, 6.6 us at the rate of reads).  Of the 21 some 7.5 are the
+// loading, 1 the choice of the range, 2.5 a second round, 4 the taking and 3 the writing, on
+// the half of the compute units that have a list.  A range pass before the first round,
+// counts by ballots in a pass of their own and a store a round took 27 us; keys in registers
+// with unrolled passes 31.7 us, reading them again 61 us.  Equal weights throughout (which a
+// softmax does not leave) are the slow case, 35 us.
 //
 // The keys lie in shared memory (up to 36 * 1024 tokens), so mass and pos are read once; a
 // longer cache reads both again in each pass.  A pass takes U times 64 tokens in a step,
@@ -108,8 +112,8 @@ constexpr uint32_t kProtected = 0xffffffffu;
 template <int THREADS, int BINS>
 struct PlanShared {
   uint32_t bins[BINS];
-  uint32_t wave[4][THREADS / 64];
-  uint32_t lo, hi, need, exact;
+  uint32_t wave[5][THREADS / 64];
+  uint32_t lo, hi, need, exact, held;
 };
 
 // f over the wave's lanes (commutative), left in every lane: lane permutes in the VALU
@@ -139,21 +143,27 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
   return v;
 }
 
-// Sum of v over the waves before this one (v wave-uniform); the caller's arrays differ
-// between uses that no barrier parts.
+// Sum over the waves before this one of what each wrote before the last barrier.
+template <int WAVES>
+__device__ __forceinline__ uint32_t before(const uint32_t *wave) {
+  const int w = threadIdx.x >> 6;
+  uint32_t sum = 0;
+#pragma unroll
+  for (int i = 0; i < WAVES; ++i) sum += i < w ? wave[i] : 0;
+  return sum;
+}
+// The same with v written here (wave-uniform); the caller's arrays differ between uses that
+// no barrier parts.
 template <int WAVES>
 __device__ __forceinline__ uint32_t before_wave(uint32_t v, uint32_t *wave) {
-  const int w = threadIdx.x >> 6;
-  if ((threadIdx.x & 63) == 0) wave[w] = v;
+  if ((threadIdx.x & 63) == 0) wave[threadIdx.x >> 6] = v;
   __syncthreads();
-  uint32_t before = 0;
-#pragma unroll
-  for (int i = 0; i < WAVES; ++i) before += i < w ? wave[i] : 0;
-  return before;
+  return before<WAVES>(wave);
 }
 
-__device__ __forceinline__ uint32_t lanes_below(uint64_t mask) {
-  return __builtin_amdgcn_mbcnt_hi(uint32_t(mask >> 32), __builtin_amdgcn_mbcnt_lo(uint32_t(mask), 0));
+// from + the mask's bits of the lanes below
+__device__ __forceinline__ uint32_t lanes_below(uint64_t mask, uint32_t from) {
+  return __builtin_amdgcn_mbcnt_hi(uint32_t(mask >> 32), __builtin_amdgcn_mbcnt_lo(uint32_t(mask), from));
 }
 
 // kHeld: the keys of all tokens in dynamic shared memory, a whole number of U * THREADS
@@ -165,7 +175,8 @@ __global__ __launch_bounds__(THREADS) void kv_evict_plan_kernel(KvGeom g, EvictA
   constexpr int kLoads = THREADS == 256 ? 8 : 16;
   static_assert(BINS == 1 << kBits, "bins");
   __shared__ PlanShared<THREADS, BINS> sh;
-  extern __shared__ uint32_t held[];
+  extern __shared__ __align__(16) uint32_t held[];
+  using Keys = uint32_t __attribute__((ext_vector_type(kHeld ? U : 2)));
   const int64_t block = flat_block();
   if (block >= int64_t(a.layers) * a.batch * g.kv_heads) return;
   const int unit = int(block);
@@ -221,9 +232,9 @@ __global__ __launch_bounds__(THREADS) void kv_evict_plan_kernel(KvGeom g, EvictA
     if (THREADS > 256 && i0 + 64 * decltype(count)::value <= n) load_some(i0, count, std::true_type{}, out);
     else load_some(i0, count, std::false_type{}, out);
   };
-  // f(first token, key) for this wave's rounds in order
-  auto each = [&](auto f) {
-    constexpr int N = kHeld ? U : kLoads;
+  // f(first token, keys of N rounds), or f(first token, key), for this wave's rounds in order
+  constexpr int N = kHeld ? U : kLoads;
+  auto each_step = [&](auto f) {
     for (int r = 0; r < rounds; r += N) {
       uint32_t k[N];
       if constexpr (kHeld) {
@@ -232,151 +243,253 @@ __global__ __launch_bounds__(THREADS) void kv_evict_plan_kernel(KvGeom g, EvictA
       } else {
         load_keys(first + 64 * r, std::integral_constant<int, N>{}, k);
       }
+      f(first + 64 * r, k);
+    }
+  };
+  auto each = [&](auto f) {
+    each_step([&](int i0, const uint32_t (&k)[N]) {
 #pragma unroll
       for (int q = 0; q < N; ++q)
-        if (kHeld || r + q < rounds) f(first + 64 * (r + q), k[q]);
+        if (kHeld || i0 + 64 * q < first + 64 * rounds) f(i0 + 64 * q, k[q]);
+    });
+  };
+  // f(key) for this wave's keys in any order: U adjacent ones a lane, the next read ahead
+  auto each_key = [&](auto f) {
+    if constexpr (kHeld) {
+      const Keys *mine = reinterpret_cast<const Keys *>(held + first) + lane;
+      Keys x = mine[0];
+      for (int r = 0; r < rounds; r += U) {
+        const Keys next = mine[64 * min(r / U + 1, rounds / U - 1)];
+#pragma unroll
+        for (int q = 0; q < U; ++q) f(x[q]);
+        x = next;
+      }
+    } else {
+      each([&](int, uint32_t key) { f(key); });
     }
   };
 
-  // ---- range of the weights above 0, count of them and of the protected ----------
-  // (both ends count from one below: key 0 becomes the largest, the protected key ...fe)
-  uint32_t kmin = kProtected, kmax = 0, prot = 0, some = 0;
-  auto look = [&](uint32_t key) {
-    kmin = min(kmin, key - 1u);
-    kmax = max(kmax, key + 1u);  // the protected key wraps to 0
-    prot += __popcll(__ballot(key == kProtected));
-    some += __popcll(__ballot(key != 0u));
-  };
-  if constexpr (kHeld) {
-    for (int r = 0; r < rounds; r += kLoads) {
-      uint32_t k[kLoads];
-      load_keys(first + 64 * r, std::integral_constant<int, kLoads>{}, k);
-#pragma unroll
-      for (int q = 0; q < kLoads; ++q) {
-        if (r + q < rounds) {
-          held[first + 64 * (r + q) + lane] = k[q];  // read again by this wave only
-          look(k[q]);
-        }
-      }
-    }
-  } else {
-    each([&](int, uint32_t key) { look(key); });
-  }
-  kmin = wave_fold(kmin, [](uint32_t x, uint32_t y) { return min(x, y); });
-  kmax = wave_fold(kmax, [](uint32_t x, uint32_t y) { return max(x, y); });
-  if (lane == 0) {
-    sh.wave[0][w] = kmin;
-    sh.wave[1][w] = kmax;
-    sh.wave[2][w] = prot;
-    sh.wave[3][w] = some;
-  }
-  __syncthreads();
-  uint32_t lo = kProtected, hi = 0;
-  prot = some = 0;
-#pragma unroll
-  for (int i = 0; i < WAVES; ++i) {
-    lo = min(lo, sh.wave[0][i]);
-    hi = max(hi, sh.wave[1][i]);
-    prot += sh.wave[2][i];
-    some += sh.wave[3][i];
-  }
-  __syncthreads();  // sh.wave is read; it is written again below
-  ++lo;
-  --hi;
-  // keep every key above `lo` at the end, and the first `need` of those equal to it;
-  // with `exact` every key >= lo
-  uint32_t need;
-  bool exact = false;
-  if (prot >= uint32_t(a.budget)) {  // the protected alone fill the budget
-    lo = hi = kProtected;
-    need = a.budget;
-  } else if (some < uint32_t(a.budget)) {  // some weights of 0 are kept
-    lo = hi = 0;
-    need = a.budget - some;
-  } else {
-    need = a.budget - prot;
-  }
-  while (lo < hi && !exact) {  // ends: each round leaves at most 2 / BINS of the range
-    const uint32_t width = hi - lo;  // (< 2^31: the largest unprotected key is infinity's)
-    const int top = 32 - __clz(width);
-    const int shift = top > kBits ? top - kBits : 0;
-    // thread t has bins BINS - 1 - PER t downwards: sums from the top
-    const int top_bin = BINS - 1 - PER * tid;
+  // ---- first round: the weights above 0 by the bits below the sign; the protected ----
+  // thread t has bins BINS - 1 - PER t downwards: sums from the top
+  const int top_bin = BINS - 1 - PER * tid;
+  auto clear = [&] {
 #pragma unroll
     for (int q = 0; q < PER; ++q) sh.bins[top_bin - q] = 0;
     __syncthreads();
-    each([&](int, uint32_t key) {
-      const uint32_t d = key - lo;
-      if (d <= width) atomicAdd(&sh.bins[d >> shift], 1u);
-    });
-    __syncthreads();
+  };
+  // One more in `bin` where `in`.  kAlike: lanes that all have one bin add once (32769 equal
+  // weights: 97 us without)
+  auto count = [&](bool in, uint32_t bin, auto alike) {
+    if constexpr (decltype(alike)::value) {
+      const uint64_t who = __ballot(in);
+      const int one = who ? __ffsll(static_cast<unsigned long long>(who)) - 1 : 0;
+      if (__ballot(in & (bin != uint32_t(__builtin_amdgcn_readlane(bin, one)))) == 0) {
+        if (in & (lane == one)) atomicAdd(&sh.bins[bin], uint32_t(__popcll(who)));
+        return;
+      }
+    }
+    if (in) atomicAdd(&sh.bins[bin], 1u);
+  };
+  // (tested on a step's first round for all of them: a test in every round took 3 us)
+  auto one_bin = [&](bool in, uint32_t bin) -> bool {
+    const uint64_t who = __ballot(in);
+    return who && __ballot(in & (bin != uint32_t(__builtin_amdgcn_readlane(
+                                           bin, __ffsll(static_cast<unsigned long long>(who)) - 1)))) == 0;
+  };
+  uint32_t prot = 0;
+  auto look = [&](int r, const uint32_t (&k)[kLoads]) {
+    auto all = [&](auto alike) {
+#pragma unroll
+      for (int q = 0; q < kLoads; ++q) {
+        if (r + q < rounds) {
+          if (kHeld) held[first + 64 * (r + q) + lane] = k[q];  // read again by this wave only
+          prot += __popcll(__ballot(k[q] == kProtected));
+          count(k[q] - 1u < kProtected - 1u, k[q] >> (31 - kBits), alike);
+        }
+      }
+    };
+    if (one_bin(k[0] - 1u < kProtected - 1u, k[0] >> (31 - kBits))) all(std::true_type{});
+    else all(std::false_type{});
+  };
+  clear();
+  for (int r = 0; r < rounds; r += kLoads) {
+    uint32_t k[kLoads];
+    load_keys(first + 64 * r, std::integral_constant<int, kLoads>{}, k);
+    look(r, k);
+  }
+  if (lane == 0) sh.wave[4][w] = prot;
+  __syncthreads();
+  prot = 0;
+#pragma unroll
+  for (int i = 0; i < WAVES; ++i) prot += sh.wave[4][i];
+
+  // keep every key above `lo` at the end, and the first `need` of those equal to it;
+  // with `exact` every key >= lo
+  uint32_t lo = 0, hi = 0x7fffffffu, need = uint32_t(a.budget) - prot;
+  bool exact = false;
+  // the bin of the range from lo on that holds the need-th largest key becomes the range;
+  // returns the count of all bins
+  auto choose = [&](int shift) -> uint32_t {
     uint32_t mine = 0, c[PER];
 #pragma unroll
     for (int q = 0; q < PER; ++q) mine += c[q] = sh.bins[top_bin - q];
     const uint32_t inc = wave_scan(mine);
     uint32_t above = before_wave<WAVES>(__builtin_amdgcn_readlane(inc, 63), sh.wave[0]) + inc - mine;
+    uint32_t all = 0;
+#pragma unroll
+    for (int i = 0; i < WAVES; ++i) all += sh.wave[0][i];
     if (above < need && above + mine >= need) {
 #pragma unroll
       for (int q = 0; q < PER; ++q) {
         if (above < need && above + c[q] >= need) {
           const uint32_t l = lo + (uint32_t(top_bin - q) << shift);
-          sh.lo = l;
+          sh.lo = max(l, 1u);  // (a weight of 0 is in no bin)
           sh.hi = min(hi, l + ((1u << shift) - 1u));
           sh.need = need - above;
           sh.exact = need - above == c[q];  // the whole bin is kept
+          sh.held = c[q];
         }
         above += c[q];
       }
     }
     __syncthreads();
+    return all;
+  };
+  auto chosen = [&] {
     lo = sh.lo;
     hi = sh.hi;
     need = sh.need;
     exact = sh.exact != 0;
+  };
+  if (prot >= uint32_t(a.budget)) {  // the protected alone fill the budget
+    lo = hi = kProtected;
+    need = a.budget;
+  } else {
+    const uint32_t some = choose(31 - kBits);
+    if (some < need) {  // some weights of 0 are kept
+      lo = hi = 0;
+      need -= some;
+    } else {
+      chosen();
+    }
+  }
+  while (lo < hi && !exact) {  // ends: each round leaves at most 2 / BINS of the range
+    const uint32_t width = hi - lo;
+    const int top = 32 - __clz(width);
+    const int shift = top > kBits ? top - kBits : 0;
+    clear();
+    auto narrow = [&](auto alike) {
+      each_key([&](uint32_t key) { count(key - lo <= width, (key - lo) >> shift, alike); });
+    };
+    // (the test costs more than it saves while other bins hold most keys: weights within one
+    // octave 28 us with it, 24 without)
+    if (sh.held > uint32_t(n) / 2) narrow(std::true_type{});
+    else narrow(std::false_type{});
+    __syncthreads();
+    choose(shift);
+    chosen();
   }
 
-  // ---- ties, then freed places and tokens to move ------------------------------
-  uint32_t tie0 = 0;
-  if (!exact) {
-    each([&](int, uint32_t key) { tie0 += __popcll(__ballot(key == lo)); });
-    tie0 = before_wave<WAVES>(tie0, sh.wave[1]);
-  }
-  // kept ones among 64 tokens: keys above lo (with `exact` from lo on) and ties while they
-  // are needed; *ties: how many came before
+  // ---- freed places and tokens to move -----------------------------------------
+  // Taken are the places below budget that are not kept and those from budget on that are:
+  // in a wave's order all its freed places come before all its tokens to move.
+  const int budget = a.budget;
+  // kept are keys above `over` and, unless `exact`, ties while they are needed
   const uint32_t over = exact ? lo - 1u : lo;  // (`exact` only with lo above 0)
-  auto keeps = [&](uint32_t key, uint32_t *ties, auto with_ties) -> uint64_t {
-    uint64_t keep = __ballot(key > over);
-    if constexpr (decltype(with_ties)::value) {
-      const uint64_t equal = __ballot(key == lo);
-      keep |= __ballot(*ties + lanes_below(equal) < need) & equal;
-      *ties += __popcll(equal);
+  // n_places into a list, four reads of the wave before the first store
+  auto put = [&](int32_t *column, const uint32_t *from_lds, uint32_t n_places) {
+    for (uint32_t e0 = lane; e0 < n_places + lane; e0 += 256) {
+      uint32_t x[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) x[q] = from_lds[min(e0 + 64 * q, n_places - 1)];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (e0 + 64 * q < n_places) column[2 * (e0 + 64 * q)] = x[q];
     }
-    return keep;
   };
   auto finish = [&](auto with_ties) {
-    uint32_t freed = 0, moved = 0, ties = tie0;
-    each([&](int i0, uint32_t key) {
-      const uint64_t keep = keeps(key, &ties, with_ties), below = __ballot(lane < a.budget - i0);
-      freed += __popcll(~keep & below);
-      moved += __popcll(keep & ~below);
-    });
-    uint32_t free_at = before_wave<WAVES>(freed, sh.wave[2]);
-    uint32_t move_at = before_wave<WAVES>(moved, sh.wave[3]);
+    constexpr bool kTies = decltype(with_ties)::value;
+    uint32_t tie0 = 0;
+    if constexpr (kTies) {
+      each([&](int, uint32_t key) { tie0 += __popcll(__ballot(key == lo)); });
+      tie0 = before_wave<WAVES>(tie0, sh.wave[1]);
+    }
+    uint32_t ties = tie0;  // (how many came before)
+    auto kept = [&](uint32_t key) -> bool {
+      if constexpr (!kTies) {
+        return key > over;
+      } else {
+        const uint64_t equal = __ballot(key == lo);
+        const bool tie = key == lo && lanes_below(equal, ties) < need;
+        ties += __popcll(equal);
+        return key > over || tie;
+      }
+    };
+    uint32_t all = 0, freed = 0;
+    if constexpr (kHeld) {
+      // The rounds of a step side by side and with no branch between them (a round at a time
+      // took half as long again): lanes that take nothing write to the bins, which are over.
+      uint32_t *const unused = sh.bins + lane;
+      each_step([&](int i0, const uint32_t (&k)[N]) {
+        auto take = [&](auto is_taken) {
+          uint64_t mask[N];
+          uint32_t *to[N];
+#pragma unroll
+          for (int q = 0; q < N; ++q) {
+            const bool t = is_taken(q);
+            mask[q] = __ballot(t);
+            uint32_t *const at = held + first + lanes_below(mask[q], all);
+            to[q] = t ? at : unused;
+            all += __popcll(mask[q]);
+          }
+#pragma unroll
+          for (int q = 0; q < N; ++q) *to[q] = i0 + 64 * q + lane;  // (keys that were read already)
+        };
+        if (i0 + 64 * N <= budget) {
+          take([&](int q) { return !kept(k[q]); });
+          freed = all;
+        } else if (i0 >= budget) {
+          take([&](int q) { return kept(k[q]); });
+        } else {
+          take([&](int q) {
+            const bool below = i0 + 64 * q + lane < budget, t = kept(k[q]) != below;
+            freed += __popcll(__ballot(t & below));
+            return t;
+          });
+        }
+      });
+    } else {
+      each([&](int i0, uint32_t key) {
+        const bool below = i0 + lane < budget, t = kept(key) != below;
+        all += __popcll(__ballot(t));
+        freed += __popcll(__ballot(t & below));
+      });
+    }
+    const uint32_t moved = all - freed;
+    if (lane == 0) {
+      sh.wave[2][w] = freed;
+      sh.wave[3][w] = moved;
+    }
+    __syncthreads();
+    const uint32_t free_at = __builtin_amdgcn_readfirstlane(before<WAVES>(sh.wave[2]));
+    const uint32_t move_at = __builtin_amdgcn_readfirstlane(before<WAVES>(sh.wave[3]));
     if (tid == THREADS - 1) a.n_moves[unit] = int(move_at + moved);
     int32_t *list = a.moves + 2 * int64_t(unit) * a.max_moves;
-    ties = tie0;
-    each([&](int i0, uint32_t key) {
-      const uint64_t keep = keeps(key, &ties, with_ties), below = __ballot(lane < a.budget - i0);
-      const uint64_t fm = ~keep & below, mm = keep & ~below;
-      if (fm) {
-        if (fm >> lane & 1) list[2 * (free_at + lanes_below(fm)) + 1] = i0 + lane;
-        free_at += __popcll(fm);
-      }
-      if (mm) {
-        if (mm >> lane & 1) list[2 * (move_at + lanes_below(mm))] = i0 + lane;
-        move_at += __popcll(mm);
-      }
-    });
+    int32_t *to = list + 2 * free_at + 1, *src = list + 2 * move_at;
+    if constexpr (kHeld) {
+      put(to, held + first, freed);
+      put(src, held + first + freed, moved);
+    } else {
+      ties = tie0;
+      uint32_t at = 0;
+      each([&](int i0, uint32_t key) {
+        const bool t = kept(key) != (i0 + lane < budget);
+        const uint64_t mask = __ballot(t);
+        const uint32_t e = lanes_below(mask, at);
+        if (t) (e < freed ? to + 2 * e : src + 2 * (e - freed))[0] = i0 + lane;
+        at += __popcll(mask);
+      });
+    }
   };
   if (exact) finish(std::false_type{});
   else finish(std::true_type{});

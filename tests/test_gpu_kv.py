@@ -432,6 +432,45 @@ def test_plan_parity(weights, n_list, budget, sink, recent):
     assert int(pool.err_word.item()) == 0
 
 
+@pytest.mark.parametrize("n", [1100, 2048, 4200, 38000])
+@pytest.mark.parametrize("budget", [1, 63, 64, 65, 127, 128, 129, 191, 255, 256, 257, 320, 511, 512, 513, 1023, 1024,
+                                    1025])
+def test_plan_budgets_inside_a_step(n, budget):
+    """The budget's place in a wave's rounds, with few and with many tokens kept past it."""
+    c = plan_case(n + budget, [n, n - 37], budget, 0, 0, kv_heads=1, layers=1)
+    c.mass[0, c.slots[1], :, budget - budget // 4:] += 1e4  # most of the kept lie past the budget
+    nxt = [c.cap] * 2
+    _, nm, mv, lo = run_plan(c, budget, 0, min(budget, 5), nxt)
+    check_plan(c, budget, 0, min(budget, 5), nxt, nm, mv, lo)
+
+
+@pytest.mark.parametrize("n", [700, 2048, 9000, 36864, 36865])
+def test_plan_runs_of_equal_weights(n):
+    """Runs of one weight, of zeros and of protected tokens beside spread ones, of lengths
+    that begin and end anywhere in a wave's rounds; subnormal weights; two large ones."""
+    g = torch.Generator().manual_seed(n)
+    for kind in range(4):
+        c = plan_case(n + kind, [n], n // 3, 4, n // 9, kv_heads=2, layers=1)
+        m = c.mass[0, c.slots[0]]
+        if kind == 0:
+            at = 0
+            while at < n:
+                run = int(torch.randint(1, 700, (1,), generator=g))
+                v = (0.25, 0.0, None, 3.0)[int(torch.randint(0, 4, (1,), generator=g))]
+                if v is not None:
+                    m[:, at:at + run] = v
+                at += run
+        elif kind == 1:
+            m.copy_(torch.randint(0, 1 << 12, m.shape, generator=g).to(torch.int32).view(torch.float32))
+        elif kind == 2:
+            m.copy_(torch.where(torch.rand(m.shape, generator=g) < 0.5, 3.4e38, float("inf")))
+        else:
+            c.pos = torch.arange(c.cap).expand(c.pos.shape).contiguous().to(torch.int32)
+            m.fill_(0.5)
+        _, nm, mv, lo = run_plan(c, n // 3, 4, n // 9, [n])
+        check_plan(c, n // 3, 4, n // 9, [n], nm, mv, lo)
+
+
 def test_plan_protected_alone_fill_the_budget():
     """Positions that repeat, or a next position too low: more protected than the budget."""
     c = plan_case(7, [900, 300], 128, 4, 60)
