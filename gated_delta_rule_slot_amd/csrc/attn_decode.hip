@@ -18,7 +18,8 @@
 // lane-local, and only the maximum crosses lanes.
 //
 // P is carried as two bf16 parts (hi + lo, 16 bits): rounded once to bf16 its error would
-// be about as large as the output's own rounding.  Scores, m, l and O are fp32.
+// be about as large as the output's own rounding.  Both parts are positive, so an infinite
+// value meets neither 0 nor two signs.  Scores, m, l and O are fp32.
 //
 // The work is counted in blocks of 128 tokens (4 waves, a tile each), in the order
 // (request, key-value head, 16 query heads, position), and every workgroup takes an equal
@@ -128,6 +129,25 @@ __device__ __forceinline__ float rows_sum(float v) {
 __device__ __forceinline__ float ref(float m) { return m == kNegInf ? 0.f : m; }
 // What a sum taken under the maximum m is worth under the larger maximum to.
 __device__ __forceinline__ float factor(float m, float to) { return m == kNegInf ? 0.f : fexp2(m - to); }
+
+// p >= 0 as two bf16 parts: its upper 16 bits, and the rest rounded to nearest (half a step of
+// at most 2^-16 p).  The rest is taken of p (1 + 2^-23), so that it is above 0 for every p from
+// 2^-103 on.
+__device__ __forceinline__ Split split_weights(const float *p) {
+  u32x4 h, l;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float rest[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float x = p[2 * i + e], hi = __uint_as_float(__float_as_uint(x) & 0xffff0000u);
+      rest[e] = fmaf(x, 1.f + 0x1p-23f, -hi);
+    }
+    h[i] = halves(__float_as_uint(p[2 * i]), __float_as_uint(p[2 * i + 1]), 1);
+    l[i] = cvt_pk_bf16(rest[0], rest[1]);
+  }
+  return Split{__builtin_bit_cast(bf16x8, h), __builtin_bit_cast(bf16x8, l)};
+}
 
 // How a lane reads rows of D values.  Keys: kPieces times 16 bytes, those of the four lane
 // groups side by side; a piece of bf16 is the k indices of one MFMA step, one of e4m3 of
@@ -525,7 +545,7 @@ void attn_decode_kernel(KvGeom g, AttnDev p) {
             pr[e] = fexp2(x[e] - base);
             l += pr[e];
           }
-          const Split ps = split8(pr);
+          const Split ps = split_weights(pr);
 
           // values: columns of eight tokens by byte permutes
           if (!whole) {  // never 0 * inf

@@ -130,8 +130,12 @@ gdn_status attn_workspace_bytes(gdn_kv_pool_t pool, int32_t batch, int32_t q_hea
  *             read across calls
  * A request that sees no token (skipped, begin >= len, or every score -inf) gets out = 0
  * and lse = -inf and adds no weight.  Tokens outside [begin, len) are not read into the
- * result whatever their rows hold.  The result does not depend on the order in which
- * the workgroups run. */
+ * result whatever their rows hold.  A visible token's infinite value makes that column of out
+ * infinite (NaN beside one of the other sign; NaN or infinite where the token's weight is below
+ * 2^-100 of the largest).  A score of +inf or NaN has no softmax: that head's out and lse are
+ * NaN, and so are the weights that it adds.  The values' sum before the division by l is
+ * held in fp32: the number of visible tokens times the largest stored |value| stays below
+ * 3.4e38.  The result does not depend on the order in which the workgroups run. */
 gdn_status attn_decode_paged(gdn_kv_pool_t pool, int32_t layer, int32_t batch, int32_t q_heads,
                              int32_t max_len, const int32_t *slot_table, const int32_t *kv_len,
                              const int32_t *kv_begin, const uint16_t *q, int64_t q_stride,

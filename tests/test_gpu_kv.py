@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from oracle import kv_ops
-from tests.kv_helpers import check_attention, device_pool, i32, make_cache, stored
+from tests.kv_helpers import attend_all, check_attention, device_pool, i32, make_cache, stored
 
 pytestmark = pytest.mark.gpu
 
@@ -789,3 +789,32 @@ def test_attention_output_between_wide_q_rows():
     gdn.attn_decode_paged(pool, c.layer, i32(c.slots), i32(c.lens), q, out, 129, scale=0.125, workspace=ws)
     check_attention(c, keep, 0.125, out)
     assert torch.equal(q.cpu(), keep)
+
+
+@pytest.mark.parametrize("dim,kv_heads,group,page,lens,begins", [
+    (64, 1, 2, 16, [1, 40, 131], None), (128, 2, 4, 4, [300, 77], [0, 5]), (256, 1, 8, 64, [700, 2], None),
+    (128, 1, 17, 32, [513], [100]), (256, 2, 1, 8, [33, 260], None), (64, 1, 8, 64, [5003], None)])
+def test_attention_infinite_values(dim, kv_heads, group, page, lens, begins):
+    """An infinite value makes its column infinite whatever its weight's bits are, one of each
+    sign or a NaN makes it NaN, and every other column, lse and the weights stay as they are."""
+    c = make_cache(dim + lens[0], lens, begins, kv_heads, dim, page, layers=1)
+    for b, n in enumerate(lens):
+        lo = c.begins[b]
+        for d in range(dim // 2):  # column d: one token's value, another token in each column
+            i = lo + (d * 7) % (n - lo)
+            c.v[0, c.table[c.slots[b], i // page], :, i % page, d] = float("-inf") if d % 3 == 0 else float("inf")
+        i, j = lo + (n - lo) // 2, n - 1
+        c.v[0, c.table[c.slots[b], i // page], :, i % page, dim - 1] = float("inf")
+        c.v[0, c.table[c.slots[b], j // page], :, j % page, dim - 1] = float("-inf" if i != j else "nan")
+        c.v[0, c.table[c.slots[b], i // page], :, i % page, dim - 2] = float("nan")
+    pool, q, out, lse, sc = run_attention(c, group, mass=True)
+    with np.errstate(invalid="ignore"):
+        want, _, _, _, _ = attend_all(c, q, sc)
+    odd = ~np.isfinite(want)
+    assert odd[:, :, :dim // 2].all() and odd[:, :, dim - 2:].all() and not odd[:, :, dim // 2:dim - 2].any()
+    got = out.float().cpu().double().numpy()
+    assert np.array_equal(got[odd], want[odd], equal_nan=True)
+    out[torch.from_numpy(odd).cuda()] = 0.0
+    c.v[..., :dim // 2] = 0.0  # the other columns against the definition without these
+    c.v[..., dim - 2:] = 0.0
+    check_attention(c, q, sc, out, lse, pool.mass, c.mass)
