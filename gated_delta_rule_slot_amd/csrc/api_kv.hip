@@ -3,6 +3,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <initializer_list>
 #include <new>
 
 #include "errors.hpp"
@@ -30,6 +31,25 @@ bool overlap(const Rows &a, const void *p, int64_t bytes) {
   const __int128 before = lo - base - a.row;  // the first row that ends behind lo
   const __int128 i = before < 0 ? 0 : before / a.stride + 1;
   return i < a.n && base + i * a.stride < lo + bytes;
+}
+
+// An array of a call, for the message
+struct Array {
+  const char *name;
+  Rows rows;
+};
+Array flat(const char *name, const void *p, int64_t bytes) { return {name, {bytes ? p : nullptr, 1, bytes, bytes}}; }
+
+// Workgroups run in any order, so nothing that one writes may be read or written elsewhere:
+// `out` (each flat) has to lie apart from `in` and from each other.
+gdn_status check_apart(std::initializer_list<Array> out, std::initializer_list<Array> in) {
+  for (const Array *w = out.begin(); w != out.end(); ++w) {
+    for (const Array &r : in)
+      if (overlap(r.rows, w->rows.base, w->rows.row)) return fail(GDN_ERR_ARG, "%s overlaps %s", w->name, r.name);
+    for (const Array *x = out.begin(); x != w; ++x)
+      if (overlap(x->rows, w->rows.base, w->rows.row)) return fail(GDN_ERR_ARG, "%s overlaps %s", w->name, x->name);
+  }
+  return GDN_OK;
 }
 
 gdn_status launched(hipError_t e, const char *what) {
@@ -188,8 +208,15 @@ GDN_API gdn_status attn_decode_paged(gdn_kv_pool_t pool, int32_t layer, int32_t 
   if (need && !aligned(workspace, 256))
     return fail(GDN_ERR_UNSUPPORTED, "workspace must be 256-byte aligned");
   const int64_t row = int64_t(q_heads) * pool->d.head_dim * 2;
-  if (overlap({q, batch, row, q_stride * 2}, out, batch * row))
-    return fail(GDN_ERR_ARG, "out overlaps q");
+  const gdn::KvGeom g = gdn::kv_geom(pool, layer);
+  const int64_t mass_bytes = flags & GDN_F_ACCUM_MASS ? int64_t(g.slots) * g.kv_heads * g.capacity * 4 : 0;
+  s = check_apart({flat("out", out, batch * row), flat("lse", lse, int64_t(batch) * q_heads * 4),
+                   flat("workspace", workspace, int64_t(need)), flat("mass", g.mass, mass_bytes),
+                   flat("err_word", g.err, 4)},
+                  {{"q", {q, batch, row, q_stride * 2}}, flat("slot_table", slot_table, batch * 4),
+                   flat("kv_len", kv_len, batch * 4), flat("kv_begin", kv_begin, batch * 4),
+                   flat("page_table", g.page_table, int64_t(g.slots) * g.max_pages * 4)});
+  if (s != GDN_OK) return s;
   gdn::AttnArgs a{batch, q_heads, max_len, slot_table, kv_len, kv_begin, q,
                   q_stride, scale, flags, out, lse, workspace};
   return launched(gdn::launch_attn_decode(pool, layer, a, static_cast<hipStream_t>(stream)),

@@ -124,10 +124,13 @@ gdn_status attn_workspace_bytes(gdn_kv_pool_t pool, int32_t batch, int32_t q_hea
  * scale       |scale * k_scale| at most 1e30
  * flags       GDN_F_ACCUM_MASS: add the weights to the pool's mass (which it must have;
  *             live slots must be distinct then).  Only visible tokens' entries change
- * out         device bf16 [batch][q_heads][head_dim], 16-byte aligned; must not overlap q
+ * out         device bf16 [batch][q_heads][head_dim], 16-byte aligned
  * lse         device fp32 [batch][q_heads] or NULL
  * workspace   attn_workspace_bytes(...) bytes, 256-byte aligned; its contents are not
  *             read across calls
+ * What the call writes (out, lse, workspace, with the flag the layer's mass, and the error
+ * word) must not overlap what it reads (q, slot_table, kv_len, kv_begin, page_table) or each
+ * other.
  * A request that sees no token (skipped, begin >= len, or every score -inf) gets out = 0
  * and lse = -inf and adds no weight.  Tokens outside [begin, len) are not read into the
  * result whatever their rows hold.  A visible token's infinite value makes that column of out

@@ -818,3 +818,31 @@ def test_attention_infinite_values(dim, kv_heads, group, page, lens, begins):
     c.v[..., :dim // 2] = 0.0  # the other columns against the definition without these
     c.v[..., dim - 2:] = 0.0
     check_attention(c, q, sc, out, lse, pool.mass, c.mass)
+
+
+def test_attention_arrays_side_by_side():
+    """Inputs, outputs, weights and workspace back to back in one buffer are apart."""
+    import gated_delta_rule_slot_amd as gdn
+
+    c = make_cache(91, [40, 129, 300], None, 2, 64, 16)
+    B, Hq, D = 3, 4, 64
+    q = torch.randn(B, Hq, D, generator=c.g).to(torch.bfloat16)
+    probe = device_pool(c)
+    n = gdn.attn_workspace_bytes(probe, B, Hq, 300, 1)
+    ints = c.table.numel() + 3 * B
+    sizes = [q.numel() * 2, q.numel() * 2, n, c.mass.numel() * 4, B * Hq * 4, 4, ints * 4]
+    buf = torch.zeros(256 + sum(sizes), dtype=torch.uint8, device="cuda")
+    at = (-buf.data_ptr()) % 256  # the workspace lies after q and out: 3 * 4 * 64 * 2 * 2 bytes, 12 * 256
+    parts = []
+    for size in sizes:
+        parts.append(buf[at:at + size])
+        at += size
+    qd, out = (t.view(torch.bfloat16).view(B, Hq, D) for t in parts[:2])
+    ws, mass = parts[2], parts[3].view(torch.float32).view(c.mass.shape)
+    lse, err, word = parts[4].view(torch.float32).view(B, Hq), parts[5].view(torch.int32), parts[6].view(torch.int32)
+    table, slots, lens, begin = word[:c.table.numel()].view(c.table.shape), *word[c.table.numel():].split(B)
+    qd.copy_(q), mass.copy_(c.mass), table.copy_(c.table), slots.copy_(i32(c.slots)), lens.copy_(i32(c.lens))
+    pool = gdn.kv_pool_create(c.k.cuda(), c.v.cuda(), table, mass=mass, err_word=err)
+    gdn.attn_decode_paged(pool, 0, slots, lens, qd, out, 300, kv_begin=begin, scale=0.125, flags=1, lse=lse, workspace=ws)
+    check_attention(c, q, 0.125, out, lse, mass, c.mass)
+    assert torch.equal(qd.cpu(), q) and lens.tolist() == c.lens and int(err.item()) == 0

@@ -206,3 +206,52 @@ def test_binding_refuses_cpu_tensors_and_wrong_shapes():
         gdn.block_norm(torch.zeros(2, 64), None)
     with pytest.raises(ValueError):
         gdn.block_norm(torch.zeros(2, 1, 64, dtype=torch.bfloat16), None)
+
+
+# every array of an attention call at a place of its own: (address, bytes)
+AT = {n: P + 0x200000 * (i + 1) for i, n in enumerate(
+    ("q", "slot_table", "kv_len", "kv_begin", "page_table", "mass", "err_word", "out", "lse", "ws"))}
+
+
+def attention_at(**kw):
+    """The call over a pool with every array apart but for `kw`."""
+    at = {**AT, **kw}
+    st, h = make(page_table=at["page_table"], mass=at["mass"], err_word=at["err_word"])
+    assert st == 0, B.last_error()
+    n = ct.c_size_t()
+    assert B._lib.attn_workspace_bytes(h, 2, 4, 80, 1, ct.byref(n)) == 0
+    a = dict(ATTN, flags=1, ws_bytes=n.value, layer=1,
+             **{k: at[k] for k in ("q", "slot_table", "kv_len", "kv_begin", "out", "lse", "ws")})
+    try:
+        return B._lib.attn_decode_paged(h, *a.values()), n.value
+    finally:
+        B._lib.kv_pool_destroy(h)
+
+
+# bytes of each: q and out 2 x 4 x 64 bf16, page_table 4 x 5, a layer's mass (of two) 4 x 2 x 80
+SIZE = dict(q=1024, slot_table=8, kv_len=8, kv_begin=8, page_table=80, mass=2560, err_word=4, out=1024, lse=32)
+
+
+@pytest.mark.parametrize("written,name", [("out", "out"), ("lse", "lse"), ("ws", "workspace"), ("mass", "mass"),
+                                          ("err_word", "err_word")])
+@pytest.mark.parametrize("read", ["q", "slot_table", "kv_len", "kv_begin", "page_table"])
+def test_attention_refuses_outputs_over_inputs(written, name, read):
+    """The read array's first and last 4 bytes (or its first 16 or 256, by the alignment)
+    inside the written one, and the written one's inside it."""
+    ws = attention_at(lse=AT["slot_table"])[1]
+    size = dict(SIZE, ws=ws)
+    base = AT[written] + (2560 if written == "mass" else 0)  # layer 1 is called
+    offs = [0, size[written] - 4] if read not in ("q",) else [0, (size[written] - 1) // 16 * 16]
+    for off in offs:
+        if base + off != AT[read]:
+            assert attention_at(**{read: base + off})[0] == -1, off
+            assert B.last_error() == f"{name} overlaps {read}", off
+
+
+@pytest.mark.parametrize("a,b,text", [("lse", "out", "lse overlaps out"), ("ws", "out", "workspace overlaps out"),
+                                      ("ws", "lse", "workspace overlaps lse"), ("mass", "out", "mass overlaps out"),
+                                      ("mass", "ws", "mass overlaps workspace"),
+                                      ("err_word", "lse", "err_word overlaps lse")])
+def test_attention_refuses_outputs_over_each_other(a, b, text):
+    at = AT[b] - (2560 if a == "mass" else 0)
+    assert attention_at(**{a: at})[0] == -1 and B.last_error() == text
