@@ -239,11 +239,20 @@ GDN_API gdn_status kv_evict_plan(gdn_kv_pool_t pool, int32_t layer_begin, int32_
   const int most = std::max(0, std::min(budget, max_len - budget));
   if (max_moves < most)
     return fail(GDN_ERR_ARG, "max_moves %d below min(budget, max_len - budget) = %d", max_moves, most);
+  const int64_t lists = int64_t(layer_end - layer_begin) * batch * pool->d.kv_heads;
+  if (lists * max_moves >= int64_t(1) << 40)
+    return fail(GDN_ERR_RANGE, "layers * batch * kv_heads * max_moves must be below 2^40");
   if (batch == 0 || layer_begin == layer_end) return ok();
   if (!slot_table || !kv_len || !next_pos || !n_moves || !kv_len_out || (!moves && most > 0))
     return fail(GDN_ERR_ARG, "a required pointer is NULL");
-  if (kv_len < kv_len_out + batch && kv_len_out < kv_len + batch)
-    return fail(GDN_ERR_ARG, "kv_len_out overlaps kv_len");
+  const gdn::KvGeom g = gdn::kv_geom(pool, layer_begin);
+  const int64_t mass_bytes = (layer_end - layer_begin) * (int64_t(g.slots) * g.kv_heads * g.capacity * 4);
+  s = check_apart({flat("kv_len_out", kv_len_out, batch * 4), flat("n_moves", n_moves, lists * 4),
+                   flat("moves", moves, lists * max_moves * 8), flat("err_word", g.err, 4)},
+                  {flat("slot_table", slot_table, batch * 4), flat("kv_len", kv_len, batch * 4),
+                   flat("next_pos", next_pos, batch * 4), flat("mass", g.mass, mass_bytes),
+                   flat("pos", g.pos, mass_bytes)});
+  if (s != GDN_OK) return s;
   gdn::EvictArgs a{layer_end - layer_begin, batch, max_len, budget, sink, recent, max_moves,
                    slot_table, kv_len, next_pos, n_moves, moves, kv_len_out};
   return launched(gdn::launch_kv_evict_plan(pool, layer_begin, a, static_cast<hipStream_t>(stream)),

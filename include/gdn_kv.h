@@ -159,10 +159,14 @@ gdn_status attn_decode_paged(gdn_kv_pool_t pool, int32_t layer, int32_t batch, i
  *             moves
  * moves       device int32 [layer_end - layer_begin][batch][kv_heads][max_moves][2]:
  *             (source, destination) indices, the first n_moves entries written, the
- *             others left as they are; max_moves >= min(budget, max_len - budget)
+ *             others left as they are; max_moves >= min(budget, max_len - budget), and
+ *             layers * batch * kv_heads * max_moves below 2^40
  * kv_len_out  device int32 [batch]: min(n, budget); a skipped request's length is
- *             copied.  Must not overlap kv_len.
- * The pool must have mass and pos. */
+ *             copied
+ * What the call writes (n_moves, moves, kv_len_out and the error word) must not overlap
+ * what it reads (slot_table, kv_len, next_pos, the layers' mass and pos) or each other.
+ * Where layer_begin = layer_end nothing is planned and nothing written, kv_len_out
+ * neither.  The pool must have mass and pos. */
 gdn_status kv_evict_plan(gdn_kv_pool_t pool, int32_t layer_begin, int32_t layer_end,
                          int32_t batch, int32_t max_len, const int32_t *slot_table,
                          const int32_t *kv_len, const int32_t *next_pos, int32_t budget,

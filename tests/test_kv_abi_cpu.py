@@ -255,3 +255,42 @@ def test_attention_refuses_outputs_over_inputs(written, name, read):
 def test_attention_refuses_outputs_over_each_other(a, b, text):
     at = AT[b] - (2560 if a == "mass" else 0)
     assert attention_at(**{a: at})[0] == -1 and B.last_error() == text
+
+
+PLAN_AT = {n: P + 0x200000 * (i + 1) for i, n in enumerate(
+    ("slot_table", "kv_len", "next_pos", "mass", "pos", "err_word", "n_moves", "moves", "out"))}
+# bytes: 2 layers x 2 requests x 2 heads, 32 moves; mass and pos of two layers, 4 slots x 2 heads x 80
+PLAN_SIZE = dict(slot_table=8, kv_len=8, next_pos=8, mass=5120, pos=5120, err_word=4, n_moves=32, moves=2048, out=8)
+
+
+def plan_at(**kw):
+    at = {**PLAN_AT, **kw}
+    st, h = make(mass=at["mass"], pos=at["pos"], err_word=at["err_word"], layers=3)
+    assert st == 0, B.last_error()
+    a = dict(PLAN, lb=1, le=3, **{k: at[k] for k in ("slot_table", "kv_len", "next_pos", "n_moves", "moves", "out")})
+    try:
+        return B._lib.kv_evict_plan(h, *a.values())
+    finally:
+        B._lib.kv_pool_destroy(h)
+
+
+@pytest.mark.parametrize("written,name", [("out", "kv_len_out"), ("n_moves", "n_moves"), ("moves", "moves"),
+                                          ("err_word", "err_word")])
+@pytest.mark.parametrize("read", ["slot_table", "kv_len", "next_pos", "mass", "pos"])
+def test_plan_refuses_outputs_over_inputs(written, name, read):
+    base = 2560 if read in ("mass", "pos") else 0  # the second layer of three is the first one called
+    for off in (0, PLAN_SIZE[written] - 4, 4 - PLAN_SIZE[read]):
+        at = PLAN_AT[written] + off - base
+        assert plan_at(**{read: at}) == -1, off
+        assert B.last_error() == f"{name} overlaps {read}", off
+
+
+@pytest.mark.parametrize("a,b", [("n_moves", "out"), ("moves", "out"), ("moves", "n_moves"), ("err_word", "moves")])
+def test_plan_refuses_outputs_over_each_other(a, b):
+    assert plan_at(**{a: PLAN_AT[b] + PLAN_SIZE[b] - 4}) == -1
+    assert B.last_error() == f"{a} overlaps {b}".replace("out", "kv_len_out")
+
+
+def test_plan_refuses_lists_past_any_memory(pool):
+    assert B._lib.kv_evict_plan(pool, *dict(PLAN, max_moves=1 << 30, batch=1 << 15).values()) == -2
+    assert "2^40" in B.last_error()
