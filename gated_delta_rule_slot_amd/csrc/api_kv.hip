@@ -18,6 +18,13 @@ gdn_status ok() { return gdn::clear_error(); }
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// int32 and fp32 arrays (the kernels read some of them by scalar loads)
+gdn_status check_words(std::initializer_list<const void *> arrays) {
+  for (const void *p : arrays)
+    if (!aligned(p, 4)) return fail(GDN_ERR_ARG, "int32 and fp32 arrays must be 4-byte aligned");
+  return GDN_OK;
+}
+
 // Memory of n >= 1 rows of `row` bytes, one every `stride` (>= row) bytes
 struct Rows {
   const void *base;
@@ -133,9 +140,7 @@ GDN_API gdn_status kv_pool_create(const gdn_kv_desc *d, gdn_kv_pool_t *out) {
     return fail(GDN_ERR_ARG, "k_base, v_base or page_table is NULL");
   if (!aligned(d->k_base, 16) || !aligned(d->v_base, 16))
     return fail(GDN_ERR_UNSUPPORTED, "pool base pointers must be 16-byte aligned");
-  if (!aligned(d->page_table, 4) || !aligned(d->mass, 4) || !aligned(d->pos, 4) ||
-      !aligned(d->err_word, 4))
-    return fail(GDN_ERR_ARG, "page_table, mass, pos and err_word must be 4-byte aligned");
+  if ((s = check_words({d->page_table, d->mass, d->pos, d->err_word})) != GDN_OK) return s;
   if (!(d->k_scale > 0) || !(d->v_scale > 0) || !isfinite(d->k_scale) || !isfinite(d->v_scale))
     return fail(GDN_ERR_ARG, "k_scale and v_scale must be finite and positive");
   if (d->kv_dtype == GDN_BF16 && (d->k_scale != 1.f || d->v_scale != 1.f))
@@ -161,6 +166,7 @@ GDN_API gdn_status kv_append(gdn_kv_pool_t pool, int32_t layer, int32_t n, const
   if (n < 0) return fail(GDN_ERR_RANGE, "n < 0");
   if (n == 0) return ok();
   if (!slot_ids || !index || !k || !v) return fail(GDN_ERR_ARG, "a required pointer is NULL");
+  if ((s = check_words({slot_ids, index, position})) != GDN_OK) return s;
   if (pool->d.pos && !position) return fail(GDN_ERR_ARG, "the pool has pos: position is required");
   const int64_t row = int64_t(pool->d.kv_heads) * pool->d.head_dim;
   if (k_stride < row || v_stride < row)
@@ -198,6 +204,7 @@ GDN_API gdn_status attn_decode_paged(gdn_kv_pool_t pool, int32_t layer, int32_t 
     return fail(GDN_ERR_ARG, "scale * k_scale must be a number of at most 1e30");
   if (batch == 0) return ok();
   if (!slot_table || !kv_len || !q || !out) return fail(GDN_ERR_ARG, "a required pointer is NULL");
+  if ((s = check_words({slot_table, kv_len, kv_begin, lse})) != GDN_OK) return s;
   if (q_stride < int64_t(q_heads) * pool->d.head_dim)
     return fail(GDN_ERR_ARG, "q_stride below q_heads * head_dim");
   if (q_stride % 8 || !aligned(q, 16) || !aligned(out, 16))
@@ -245,6 +252,7 @@ GDN_API gdn_status kv_evict_plan(gdn_kv_pool_t pool, int32_t layer_begin, int32_
   if (batch == 0 || layer_begin == layer_end) return ok();
   if (!slot_table || !kv_len || !next_pos || !n_moves || !kv_len_out || (!moves && most > 0))
     return fail(GDN_ERR_ARG, "a required pointer is NULL");
+  if ((s = check_words({slot_table, kv_len, next_pos, n_moves, moves, kv_len_out})) != GDN_OK) return s;
   const gdn::KvGeom g = gdn::kv_geom(pool, layer_begin);
   const int64_t mass_bytes = (layer_end - layer_begin) * (int64_t(g.slots) * g.kv_heads * g.capacity * 4);
   s = check_apart({flat("kv_len_out", kv_len_out, batch * 4), flat("n_moves", n_moves, lists * 4),
@@ -270,6 +278,7 @@ GDN_API gdn_status kv_evict_apply(gdn_kv_pool_t pool, int32_t layer_begin, int32
     return fail(GDN_ERR_RANGE, "layers * batch * kv_heads * max_moves must be below 2^40");
   if (batch == 0 || layer_begin == layer_end || max_moves == 0) return ok();
   if (!slot_table || !n_moves || !moves) return fail(GDN_ERR_ARG, "a required pointer is NULL");
+  if ((s = check_words({slot_table, n_moves, moves})) != GDN_OK) return s;
   gdn::EvictArgs a{};
   a.layers = layer_end - layer_begin;
   a.batch = batch;

@@ -38,6 +38,8 @@
  * attention treats that page's tokens as not visible, the other calls skip the token.
  * The bits go to the pool's error word (sticky; the caller clears it).
  *
+ * int32 and fp32 arrays are 4-byte aligned, others as stated.
+ *
  * Streams, errors and host-side checks are those of gdn_slot.h: asynchronous on the
  * given stream, everything the host can check is checked before any launch.  Every call
  * can be captured into a graph; replays read the device arrays anew.  Calls that share
@@ -89,7 +91,7 @@ void kv_pool_destroy(gdn_kv_pool_t pool);
  * slot_ids    device int32 [n], index device int32 [n]: token i goes to place index[i]
  *             of slot slot_ids[i] (index outside [0, max_pages * page_size) sets
  *             GDN_ERRW_BAD_SEQLENS and skips the token); the (slot, index) pairs of a
- *             call must be distinct
+ *             call must be distinct.  No input may lie where the call writes
  * k, v        device bf16, token i at k + i * k_stride (elements, a multiple of 8, at
  *             least kv_heads * head_dim; 16-byte aligned), [kv_heads][head_dim] there
  * position    device int32 [n], stored to pos; required iff the pool has pos

@@ -294,3 +294,16 @@ def test_plan_refuses_outputs_over_each_other(a, b):
 def test_plan_refuses_lists_past_any_memory(pool):
     assert B._lib.kv_evict_plan(pool, *dict(PLAN, max_moves=1 << 30, batch=1 << 15).values()) == -2
     assert "2^40" in B.last_error()
+
+
+@pytest.mark.parametrize("fn,base,names", [
+    ("kv_append", APPEND, ["slot_ids", "index", "position"]),
+    ("attn_decode_paged", {**ATTN, "out": P + 0x10000, "ws": P + 0x20000, "kv_begin": P, "lse": P + 0x30000},
+     ["slot_table", "kv_len", "kv_begin", "lse"]),
+    ("kv_evict_plan", PLAN, ["slot_table", "kv_len", "next_pos", "n_moves", "moves", "out"]),
+    ("kv_evict_apply", APPLY, ["slot_table", "n_moves", "moves"])])
+def test_word_arrays_off_their_alignment_are_refused(pool, fn, base, names):
+    for name in names:
+        for off in (1, 2, 3):
+            assert getattr(B._lib, fn)(pool, *dict(base, **{name: base[name] + 0x100000 + off}).values()) == -1
+            assert "4-byte aligned" in B.last_error(), name
