@@ -81,6 +81,11 @@ gdn_status check_shape(const gdn_kv_desc *d) {
   if (d->kv_heads > 65535 ||
       int64_t(d->pages) * d->page_size >= (int64_t(1) << 31) / d->kv_heads)
     return fail(GDN_ERR_UNSUPPORTED, "pages * kv_heads * page_size must be below 2^31");
+  // (the products of all sizes pass 64 bits; offsets into the arrays are counted in them)
+  const __int128 rows = __int128(d->layers) * d->pages * d->kv_heads * d->page_size;
+  const __int128 entries = __int128(d->layers) * d->slots * d->kv_heads * d->max_pages * d->page_size;
+  if (rows * d->head_dim * (d->kv_dtype == GDN_BF16 ? 2 : 1) > INT64_MAX || entries * 4 > INT64_MAX)
+    return fail(GDN_ERR_UNSUPPORTED, "k, v, mass and pos must each be below 2^63 bytes");
   return GDN_OK;
 }
 

@@ -80,8 +80,8 @@ gdn_status kv_pool_bytes(const gdn_kv_desc *desc, size_t *kv_bytes, size_t *mass
 
 /* Validate a descriptor and wrap it in a handle (host memory only; the buffers stay the
  * caller's).  Supported: head_dim in {64, 128, 256}, page_size a power of two in
- * [1, 1024], pages >= 2, slots >= 2, max_pages * page_size < 2^30 and
- * pages * kv_heads * page_size < 2^31.  Thread-safe; the handle is immutable. */
+ * [1, 1024], pages >= 2, slots >= 2, kv_heads <= 65535, max_pages * page_size < 2^30,
+ * pages * kv_heads * page_size < 2^31, and k, v, mass and pos below 2^63 bytes each.  Thread-safe; the handle is immutable. */
 gdn_status kv_pool_create(const gdn_kv_desc *desc, gdn_kv_pool_t *out);
 
 /* Free a handle (not the buffers).  NULL is ignored. */

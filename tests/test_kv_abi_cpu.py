@@ -307,3 +307,25 @@ def test_word_arrays_off_their_alignment_are_refused(pool, fn, base, names):
         for off in (1, 2, 3):
             assert getattr(B._lib, fn)(pool, *dict(base, **{name: base[name] + 0x100000 + off}).values()) == -1
             assert "4-byte aligned" in B.last_error(), name
+
+
+BIG = 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(layers=BIG, slots=BIG, kv_heads=32, pages=1 << 20, page_size=32, max_pages=1 << 24, head_dim=256), -3),
+    # k of 2^63 bytes, and a layer less; mass of 2^61 entries, and a slot less
+    (dict(layers=1 << 24, pages=1 << 20, kv_heads=8, page_size=128, max_pages=1, head_dim=256), -3),
+    (dict(layers=(1 << 24) - 1, pages=1 << 20, kv_heads=8, page_size=128, max_pages=1, head_dim=256), 0),
+    (dict(layers=1 << 10, slots=1 << 19, kv_heads=8, page_size=128, max_pages=1 << 22), -3),
+    (dict(layers=1 << 10, slots=(1 << 19) - 1, kv_heads=8, page_size=128, max_pages=1 << 22), 0),
+])
+def test_sizes_past_63_bits_are_refused(kw, status):
+    d, n, m = desc(**kw), ct.c_size_t(), ct.c_size_t()
+    assert B._lib.kv_pool_bytes(ct.byref(d), ct.byref(n), ct.byref(m)) == status
+    if status == 0:
+        rows = d.layers * d.pages * d.kv_heads * d.page_size
+        assert n.value == rows * d.head_dim * 2 and m.value == d.layers * d.slots * d.kv_heads * d.max_pages * d.page_size
+    st, h = make(**kw)
+    assert st == status
+    B._lib.kv_pool_destroy(h)
