@@ -522,15 +522,15 @@ __global__ __launch_bounds__(kMoveThreads) void kv_evict_apply_kernel(KvGeom g, 
   const int src = a.moves[e], dst = a.moves[e + 1];
   const int count = a.n_moves[unit], slot = a.slot_table[b];
   const bool teller = block == 0 && threadIdx.x == 0;
+  if (slot <= 0 || slot >= g.slots) {
+    if (teller && slot >= g.slots) set_err(g.err, GDN_ERRW_BAD_SLOT);
+    return;
+  }
   if (count < 0 || count > a.max_moves) {
     if (teller) set_err(g.err, GDN_ERRW_BAD_SEQLENS);
     return;
   }
   if (first >= count) return;
-  if (slot <= 0 || slot >= g.slots) {
-    if (teller && slot >= g.slots) set_err(g.err, GDN_ERRW_BAD_SLOT);
-    return;
-  }
   if (int(threadIdx.x) < entries) {
     int rs = -1, rd = -1;
     if (j < count) {

@@ -846,3 +846,18 @@ def test_attention_arrays_side_by_side():
     gdn.attn_decode_paged(pool, 0, slots, lens, qd, out, 300, kv_begin=begin, scale=0.125, flags=1, lse=lse, workspace=ws)
     check_attention(c, q, 0.125, out, lse, mass, c.mass)
     assert torch.equal(qd.cpu(), q) and lens.tolist() == c.lens and int(err.item()) == 0
+
+
+@pytest.mark.parametrize("slots,counts,bit", [([0, -1], [7, -3], 0), ([9, 1], [0, 0], "ERRW_BAD_SLOT"),
+                                              ([0, 9], [-1, 7], "ERRW_BAD_SLOT"), ([1, 0], [7, 0], "ERRW_BAD_SEQLENS")])
+def test_apply_looks_at_the_slot_before_the_count(slots, counts, bit):
+    """A padded request is skipped whatever its count holds, and a slot that is none is told
+    with any count, as in the plan."""
+    import gated_delta_rule_slot_amd as gdn
+
+    c = make_cache(18, [64, 64], None, 1, 64, 16, slots=[1, 2])
+    pool = device_pool(c)
+    moves = torch.full((1, 2, 1, 2, 2), 3, dtype=torch.int32, device="cuda")
+    gdn.kv_evict_apply(pool, 0, 1, i32(slots), i32([[[n] for n in counts]]), moves)
+    assert int(pool.err_word.item()) == (getattr(gdn, bit) if bit else 0)
+    assert torch.equal(pool.k.cpu().view(torch.int16), c.k.view(torch.int16)) and torch.equal(pool.mass.cpu(), c.mass)
