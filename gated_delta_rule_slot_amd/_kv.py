@@ -12,9 +12,10 @@ import torch
 from ._binding import GDN_BF16, GDN_F32, _check, _f32, _i32, _i64, _lib, _sz, _u32, _vp
 
 # the current device and stream as plain numbers (torch.cuda's objects cost more than the
-# launch of a small kernel)
-_current_device = torch._C._cuda_getDevice
-_current_raw_stream = torch._C._cuda_getCurrentRawStream
+# launch of a small kernel); a torch build that lacks these takes the public way
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 GDN_F8_E4M3 = 2
 ERRW_BAD_PAGE = 16

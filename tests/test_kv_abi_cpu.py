@@ -329,3 +329,19 @@ def test_sizes_past_63_bits_are_refused(kw, status):
     st, h = make(**kw)
     assert st == status
     B._lib.kv_pool_destroy(h)
+
+
+def test_binding_loads_without_torch_private_names(monkeypatch):
+    """A torch build without the private device and stream calls (a CPU build) still loads
+    the package, and the public calls stand in for them."""
+    import importlib.util
+    from types import SimpleNamespace
+
+    for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+        monkeypatch.delattr(torch._C, name, raising=False)
+    spec = importlib.util.spec_from_file_location("gated_delta_rule_slot_amd._kv_again", K.__file__)
+    again = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(again)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda index: SimpleNamespace(cuda_stream=40 + index))
+    assert again._on_stream(None, 3) == 43
+    assert again._current_device is torch.cuda.current_device
