@@ -923,19 +923,27 @@ hipError_t launch_d(const KvGeom &g, const AttnDev &p, bool f8, hipStream_t s) {
 // Blocks of a unit of max_len tokens (its first tile may begin before the first one seen).
 int64_t unit_blocks(int max_len) { return std::max<int64_t>(1, (int64_t(max_len) + kTile - 1 + kBlock - 1) / kBlock); }
 
-// Workers of a call: one per compute unit (its 4 waves keep 64 to 128 KB in flight), or fewer
-// where there are not that many blocks.  A second one per compute unit loses where pages hold
-// a tile (128 ragged requests of 2100 tokens, head dim 256: 108.9 against 102.0 us; 16 of
-// 8192 tokens: 39.1 against 33.5 us, a larger part of it joining), and gains with smaller
-// pages, whose short runs of a head otherwise meet on few memory channels at a time
-// (e4m3, 16-token pages, 64 requests of 4096 tokens: 97 against 133 us), once there is work
-// for both.
+// Workers of a call: one per compute unit, or fewer where there are not that many blocks.  Its
+// 4 waves keep a tile of keys and values each in flight: 128 KB with rows of 512 bytes (bf16,
+// head dim 256), 16 KB with rows of 64 (e4m3, head dim 64).  Measured with one and two per
+// compute unit, us, in pages of 4, 16, 32, 64 and 128 tokens:
+//   rows of 64 bytes      two gain wherever there is work for both: 64 requests of 4096 tokens, 8
+//                         heads (66 blocks per compute unit): 93 / 61, 63 / 49, 69 / 49, 62 / 48,
+//                         62 / 48; 17 blocks: 21 / 19.5, 8: 16.3 / 14.7; 4 blocks: 14.4 / 16.7
+//   rows of 128 bytes     the same call in e4m3: 122 / 98, 131 / 90, then 88 / 88; in bf16 108 / 100,
+//                         101 / 88 (lengths of 4000 to 4096), then 86 / 86.  A head's run in a page
+//                         is short there, and the workers meet on few memory channels at a time.
+//                         At 17 blocks two gain in pages of 4 (33 / 29.4) and lose in others (28.6 /
+//                         30.2, 27.3 / 30.0)
+//   256 and 512 bytes     one is as good or better: 164 / 166, 320 / 320; at 17 blocks 45 / 48, 86 / 90;
+//                         pages of 4 tokens of 256 bytes 190 / 179, at 8 blocks 31.1 / 32.5
 int attn_workers(const gdn_kv_pool *p, int batch, int q_heads, int max_len) {
   const int group = q_heads / p->d.kv_heads;
   const int64_t units = int64_t(batch) * p->d.kv_heads * ((group + 15) / 16);
   const int64_t blocks = units * unit_blocks(max_len);
-  const int per_cu = p->d.page_size < kTile && blocks >= 8 * kCUs ? 2 : 1;
-  return int(std::max<int64_t>(1, std::min<int64_t>(kCUs * per_cu, blocks)));
+  const bool small = p->row_bytes <= 64 || (p->d.page_size < 16 && p->row_bytes <= 128);
+  const bool two = blocks >= 8 * kCUs && (small || (blocks >= 32 * kCUs && p->d.page_size * p->row_bytes <= 2048));
+  return int(std::max<int64_t>(1, std::min<int64_t>(kCUs * (two ? 2 : 1), blocks)));
 }
 
 // One block per unit at most: no unit is ever divided.

@@ -861,3 +861,23 @@ def test_apply_looks_at_the_slot_before_the_count(slots, counts, bit):
     gdn.kv_evict_apply(pool, 0, 1, i32(slots), i32([[[n] for n in counts]]), moves)
     assert int(pool.err_word.item()) == (getattr(gdn, bit) if bit else 0)
     assert torch.equal(pool.k.cpu().view(torch.int16), c.k.view(torch.int16)) and torch.equal(pool.mass.cpu(), c.mass)
+
+
+@pytest.mark.parametrize("f8,dim,page,batch,max_len,workers", [
+    (True, 64, 64, 16, 4096, 512), (True, 64, 64, 15, 4096, 256), (True, 128, 16, 32, 8192, 512),
+    (True, 128, 16, 31, 8000, 256), (False, 64, 8, 16, 4096, 512), (True, 128, 64, 32, 8192, 256)])
+def test_attention_with_one_and_two_workgroups_per_compute_unit(f8, dim, page, batch, max_len, workers):
+    """Both sides of the rule for the number of workgroups: by the bytes of a row and of a
+    head's run in a page, and by the blocks of 128 tokens that the bound allows."""
+    import gated_delta_rule_slot_amd as gdn
+
+    r = np.random.default_rng(dim + page + batch)
+    lens = [int(x) for x in r.integers(0, 300, size=batch)]
+    lens[0], lens[-1] = 1500, 1
+    c = make_cache(batch, lens, None, 4, dim, page, f8, capacity=max_len)
+    pool, q, out, lse, sc = run_attention(c, 2, mass=True, max_len=max_len)
+    check_attention(c, q, sc, out, lse, pool.mass, c.mass)
+    # the workspace's parts: units, O and (m, l) of 2 x 16 heads a workgroup
+    units, parts = batch * 4 * 8, workers * 2 * 16
+    pad = lambda n: -(-n // 256) * 256  # noqa: E731
+    assert gdn.attn_workspace_bytes(pool, batch, 8, max_len) == pad(units) + pad(parts * dim * 4) + pad(parts * 8)
