@@ -8,10 +8,8 @@
 #include <mutex>
 #include <new>
 
+#include "api.hpp"
 #include "common.hpp"
-#include "errors.hpp"
-
-#define GDN_API extern "C" __attribute__((visibility("default")))
 
 namespace {
 thread_local char g_err[512] = "";
@@ -33,16 +31,14 @@ gdn_status clear_error() {
 
 namespace {
 
-#define fail(...) gdn::set_error(__VA_ARGS__)
-
-gdn_status ok() { return gdn::clear_error(); }
+using gdn::aligned;
+using gdn::launched;
+using gdn::ok;
 
 // (request, head) units from which the prefill runs in one kernel by default: a
 // workgroup per unit then keeps most compute units busy, while fewer units run
 // faster on the two-kernel path, which spreads each request over its chunks.
 constexpr int64_t kOneKernelMinUnits = 128;
-
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 gdn_status check_shape(const gdn_pool_desc *d) {
   if (!d) return fail(GDN_ERR_ARG, "descriptor is NULL");
@@ -71,11 +67,6 @@ gdn_status check_pool(gdn_pool_t p, int layer) {
   if (layer < 0 || layer >= p->d.layers)
     return fail(GDN_ERR_RANGE, "layer %d outside [0, %d)", layer, p->d.layers);
   return GDN_OK;
-}
-
-gdn_status launched(hipError_t e, const char *what) {
-  if (e != hipSuccess) return fail(GDN_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
-  return ok();
 }
 
 }  // namespace

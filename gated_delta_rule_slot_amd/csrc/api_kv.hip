@@ -6,17 +6,14 @@
 #include <initializer_list>
 #include <new>
 
-#include "errors.hpp"
+#include "api.hpp"
 #include "kv.hpp"
-
-#define GDN_API extern "C" __attribute__((visibility("default")))
-#define fail(...) gdn::set_error(__VA_ARGS__)
 
 namespace {
 
-gdn_status ok() { return gdn::clear_error(); }
-
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+using gdn::aligned;
+using gdn::launched;
+using gdn::ok;
 
 // int32 and fp32 arrays (the kernels read some of them by scalar loads)
 gdn_status check_words(std::initializer_list<const void *> arrays) {
@@ -57,11 +54,6 @@ gdn_status check_apart(std::initializer_list<Array> out, std::initializer_list<A
       if (overlap(x->rows, w->rows.base, w->rows.row)) return fail(GDN_ERR_ARG, "%s overlaps %s", w->name, x->name);
   }
   return GDN_OK;
-}
-
-gdn_status launched(hipError_t e, const char *what) {
-  if (e != hipSuccess) return fail(GDN_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
-  return ok();
 }
 
 gdn_status check_shape(const gdn_kv_desc *d) {

@@ -101,16 +101,6 @@ __device__ __forceinline__ void local_barrier() {
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
-// inclusive sum over the lanes in order
-__device__ __forceinline__ int wave_scan(int v) {
-  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr 1
-  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast 15
-  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast 31
-  return v;
-}
 
 // max / sum over the four 16-lane groups (same head), left in every lane
 __device__ __forceinline__ float rows_max(float v) {
@@ -262,7 +252,7 @@ void attn_decode_kernel(KvGeom g, AttnDev p) {
       if (r >= p.a.batch) four[i].blocks = 0;
       mine += four[i].blocks;
     }
-    inc = wave_scan(mine);
+    inc = int(wave_scan(uint32_t(mine)));
     const int sum = __builtin_amdgcn_readlane(inc, 63);
     inc -= mine;  // of the lanes before
     return sum;

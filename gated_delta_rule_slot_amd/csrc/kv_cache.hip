@@ -116,33 +116,6 @@ struct PlanShared {
   uint32_t lo, hi, need, exact, held;
 };
 
-// f over the wave's lanes (commutative), left in every lane: lane permutes in the VALU
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp_u32(uint32_t v) {
-  return uint32_t(__builtin_amdgcn_update_dpp(0, int(v), CTRL, 0xF, 0xF, true));
-}
-template <typename F>
-__device__ __forceinline__ uint32_t wave_fold(uint32_t v, F f) {
-  v = f(v, dpp_u32<0xB1>(v));   // quad_perm [1,0,3,2]
-  v = f(v, dpp_u32<0x4E>(v));   // quad_perm [2,3,0,1]
-  v = f(v, dpp_u32<0x141>(v));  // row_half_mirror
-  v = f(v, dpp_u32<0x140>(v));  // row_mirror
-  const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-  v = f(r[0], r[1]);
-  const auto q = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-  return f(q[0], q[1]);
-}
-// inclusive sum over the lanes in order
-__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
-  v += uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x111, 0xF, 0xF, false));  // row_shr 1
-  v += uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x112, 0xF, 0xF, false));
-  v += uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x114, 0xF, 0xF, false));
-  v += uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x118, 0xF, 0xF, false));
-  v += uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x142, 0xA, 0xF, false));  // row_bcast 15
-  v += uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x143, 0xC, 0xF, false));  // row_bcast 31
-  return v;
-}
-
 // Sum over the waves before this one of what each wrote before the last barrier.
 template <int WAVES>
 __device__ __forceinline__ uint32_t before(const uint32_t *wave) {
