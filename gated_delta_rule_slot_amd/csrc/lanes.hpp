@@ -1,6 +1,6 @@
-// lanes.hpp -- device helpers shared by the one-token kernels (decode, the draft-tree
-// verify, attention and its cache): state vectors in the pool dtype, lane-group sums,
-// and bf16 conv-row slices.  Internal; not installed.
+// lanes.hpp -- device helpers shared by the one-token kernels (decode and the
+// draft-tree verify): state vectors in the pool dtype, lane-group sums, and
+// bf16 conv-row slices.  Internal; not installed.
 #pragma once
 
 #include "common.hpp"
@@ -72,17 +72,6 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 __device__ __forceinline__ float wave_sum(float v) { return group_sum<64>(v); }
-
-// Inclusive sum over the wave's lanes in order.
-__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
-  v += uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x111, 0xF, 0xF, false));  // row_shr 1
-  v += uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x112, 0xF, 0xF, false));
-  v += uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x114, 0xF, 0xF, false));
-  v += uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x118, 0xF, 0xF, false));
-  v += uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x142, 0xA, 0xF, false));  // row_bcast 15
-  v += uint32_t(__builtin_amdgcn_update_dpp(0, int(v), 0x143, 0xC, 0xF, false));  // row_bcast 31
-  return v;
-}
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
