@@ -187,8 +187,9 @@ def attn_workspace_bytes(pool: KvPool, batch, q_heads, max_len, flags=0) -> int:
 def attn_decode_paged(pool: KvPool, layer, slot_table, kv_len, q, out, max_len, kv_begin=None, scale=1.0,
                       flags=0, lse=None, workspace=None, stream=None):
     """``q`` bf16 [batch, q_heads, head_dim] (rows at any stride), ``out`` the same,
-    contiguous; ``slot_table``, ``kv_len``, ``kv_begin`` int32 [batch]; ``lse`` fp32
-    [batch, q_heads]; ``workspace`` uint8 (attn_workspace_bytes)."""
+    contiguous; ``slot_table``, ``kv_len``, ``kv_begin`` int32 [batch] (the first visible
+    place: not for slots that kv_evict_apply has cut); ``lse`` fp32 [batch, q_heads];
+    ``workspace`` uint8 (attn_workspace_bytes)."""
     dev = _on(pool.device)
     B = slot_table.numel()
     if q.dim() != 3:

@@ -119,8 +119,10 @@ gdn_status attn_workspace_bytes(gdn_kv_pool_t pool, int32_t batch, int32_t q_hea
  *             max_pages * page_size
  * slot_table  device int32 [batch]
  * kv_len      device int32 [batch]: tokens in the cache
- * kv_begin    device int32 [batch] or NULL (= 0): first visible token, for a sliding
- *             window
+ * kv_begin    device int32 [batch] or NULL (= 0): first visible place of the cache.  Places
+ *             are the order of the tokens, and so a sliding window, only in a slot that no
+ *             kv_evict_apply has cut: its moves put late tokens into early places, and the
+ *             pool's pos is not looked at here.  A slot that was cut is attended to whole
  * q           device bf16, request b at q + b * q_stride (elements, a multiple of 8, at
  *             least q_heads * head_dim; 16-byte aligned), [q_heads][head_dim] there
  * scale       |scale * k_scale| at most 1e30
@@ -152,8 +154,9 @@ gdn_status attn_decode_paged(gdn_kv_pool_t pool, int32_t layer, int32_t batch, i
  * pos < sink or pos >= next_pos[b] - recent first, then those of the largest mass; ties
  * (among the protected too, if they alone exceed the budget) go to the lowest index.  A
  * NaN or negative mass counts as 0.  The kept tokens at index >= budget, in order, move to
- * the freed places below budget, in order; attention does not depend on the order of its
- * tokens.  Nothing is moved by this call.
+ * the freed places below budget, in order; attention over all places does not depend on
+ * their order (attn_decode_paged's kv_begin does, and does not go with a slot that was cut).
+ * Nothing is moved by this call.
  * max_len     no request has more tokens (more, or fewer than 0: GDN_ERRW_BAD_SEQLENS,
  *             skipped); at most max_pages * page_size
  * budget      >= 1;  sink, recent >= 0 with sink + recent <= budget

@@ -881,3 +881,22 @@ def test_attention_with_one_and_two_workgroups_per_compute_unit(f8, dim, page, b
     units, parts = batch * 4 * 8, workers * 2 * 16
     pad = lambda n: -(-n // 256) * 256  # noqa: E731
     assert gdn.attn_workspace_bytes(pool, batch, 8, max_len) == pad(units) + pad(parts * dim * 4) + pad(parts * 8)
+
+
+def test_attention_begin_counts_places_also_after_an_eviction():
+    """kv_begin is a place: after a cut, the tokens in the places from it on are seen, whatever
+    their positions, and the whole cache without it."""
+    import gated_delta_rule_slot_amd as gdn
+
+    c = make_cache(88, [200], None, 1, 64, 16, slots=[1])
+    pool = device_pool(c)
+    c.pos = torch.arange(c.cap, dtype=torch.int32).expand(c.mass.shape).contiguous()
+    _, nm, mv, lo = run_plan(c, 100, 4, 50, [200], pool=pool)
+    gdn.kv_evict_apply(pool, 0, 1, i32([1]), nm.cuda(), mv.cuda())
+    assert int(nm.sum()) >= 50 and (pool.pos[0, 1, 0, :60].cpu() >= 150).any()  # recent ones in early places
+    c.k, c.v, c.mass = pool.k.cpu(), pool.v.cpu(), pool.mass.cpu()
+    c.lens = lo.tolist()
+    for begin in (0, 60):
+        c.begins = [begin]
+        _, q, out, lse, sc = run_attention(c, 4, pool=pool)
+        check_attention(c, q, sc, out, lse)
