@@ -203,6 +203,9 @@ __device__ __forceinline__ void f8_to_bf16(u32 x, u32 *lo, u32 *hi) {
 // on, also over the end of a unit: under load a dependent read takes 5 us and more, so a
 // unit that began with its own reads of queries, page ids and keys cost about 8 us each time.
 // kMass: scores are stored for the weights, 1: of up to 8 heads, 2: of up to 16.
+//
+// Registers: up to 255 VGPRs at two waves a SIMD.  The two forms of bf16, head dim 256, pages
+// below 16 tokens and weights spill 4 of them (20 bytes a lane); no other spills.
 template <int D, bool kF8, bool kWide, int kMass>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2)))
 void attn_decode_kernel(KvGeom g, AttnDev p) {

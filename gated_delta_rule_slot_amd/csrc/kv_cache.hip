@@ -572,6 +572,15 @@ hipError_t launch_plan(const KvGeom &g, const EvictArgs &a, hipStream_t s) {
 }
 }  // namespace
 
+// Which form runs goes by the bound max_len, the only length that the host knows.
+//   256 against 1024 threads a list, us: 512 lists of 1088 tokens 7.1 / 12.1, of 2048 7.7 / 11.9,
+//   of 4096 10.9 / 12.5, of 8192 17.6 / 15.7; 128 lists of 2048 6.9 / 8.4, of 4096 8.7 / 8.8, of
+//   6000 10.8 / 9.4; 16 lists of 2048 7.1 / 7.7, of 4096 8.3 / 8.1.  (They meet near 4096: the
+//   border could lie higher.)
+//   keys held against read again in each pass: 128 lists of 20000 15.4 / 27.2, 16 of 36864
+//   18.0 / 32.5; 36 * 1024 keys and the bins are what shared memory takes.
+// A bound far above the lengths costs: 128 lists of 2000 tokens 6.9 with max_len 2048, 8.3 up to
+// 36864, 13.6 past it; 512 lists 7.4, 12.1 (15.2 at 36864, one workgroup per compute unit), 25.0.
 hipError_t launch_kv_evict_plan(const gdn_kv_pool *p, int layer, const EvictArgs &a, hipStream_t s) {
   const KvGeom g = kv_geom(p, layer);
   if (a.max_len <= 2048) return launch_plan<256, true, 1024, 2>(g, a, s);

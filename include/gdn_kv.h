@@ -106,7 +106,9 @@ gdn_status kv_append(gdn_kv_pool_t pool, int32_t layer, int32_t n, const int32_t
 enum { GDN_F_ACCUM_MASS = 1u };
 
 /* Workspace of attn_decode_paged for `batch` requests of up to max_len tokens.  Pure
- * host arithmetic. */
+ * host arithmetic.  With GDN_F_ACCUM_MASS it holds every score, 4 * batch * q_heads *
+ * max_len bytes by the bound, not the lengths (128 requests of 32 heads, 131072 tokens:
+ * 2.1 GB), so a close bound is smaller too. */
 gdn_status attn_workspace_bytes(gdn_kv_pool_t pool, int32_t batch, int32_t q_heads,
                                 int32_t max_len, uint32_t flags, size_t *bytes);
 
@@ -158,7 +160,8 @@ gdn_status attn_decode_paged(gdn_kv_pool_t pool, int32_t layer, int32_t batch, i
  * their order (attn_decode_paged's kv_begin does, and does not go with a slot that was cut).
  * Nothing is moved by this call.
  * max_len     no request has more tokens (more, or fewer than 0: GDN_ERRW_BAD_SEQLENS,
- *             skipped); at most max_pages * page_size
+ *             skipped); at most max_pages * page_size.  It chooses how a list is
+ *             worked on (up to 2048, up to 36864, longer), so a close bound is faster
  * budget      >= 1;  sink, recent >= 0 with sink + recent <= budget
  * n_moves     device int32 [layer_end - layer_begin][batch][kv_heads]: 0 where nothing
  *             moves
@@ -209,7 +212,8 @@ enum { GDN_F_NORM_PLUS_ONE = 1u };
  * gate are bf16 with a stride per token (elements, a multiple of 8, at least
  * groups * dim); residual, residual_out (res_dtype GDN_BF16 or GDN_F32) and out (bf16) are
  * contiguous.  w_dtype (GDN_BF16 or GDN_F32) is the weights' type.  dim is a multiple of
- * 8, at most 32768; every pointer 16-byte aligned.  Everything is computed in fp32 and
+ * 8, at most 32768; every pointer 16-byte aligned.  Everything is computed in fp32 (a row
+ * whose squares sum past 3.4e38 has rms(x) = 0 there, a gate below -87 sigmoid 0) and
  * each output is rounded once, r for the second norm not at all.  residual_out may be
  * residual and out may be y (with y_stride = groups * dim); otherwise outputs must not
  * overlap inputs.  eps > 0. */
