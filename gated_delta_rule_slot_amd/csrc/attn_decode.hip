@@ -32,9 +32,9 @@
 //
 // Measured on MI355X (both kernels; scaling 4 GiB in place runs at 5.9 TB/s there): 4 requests of
 // 90001-131072 tokens, 2 heads of 256, 956 MB: 152 us, 6.3 TB/s; 128 of 150-4099 tokens with
-// weights, 547 MB: 110-114 us, 4.8-5.0 TB/s (join and weights 8.6 us of it); e4m3 in 16-token
-// pages, 64 of 1000-8192 tokens in a 4096-token window, 8 heads of 128, 460 MB: 81-87 us; one
-// of 777 tokens: 10.4 + 3.9 us, a chain of dependent reads (lengths, page ids, keys).
+// weights, 547 MB: 106-114 us, 4.8-5.2 TB/s (join and weights 8.7 us of it); e4m3 in 16-token
+// pages, 64 of 1000-8192 tokens in a 4096-token window, 8 heads of 128, 460 MB: 80-87 us; one
+// of 777 tokens: 10.6 + 3.8 us, a chain of dependent reads (lengths, page ids, keys).
 #include <algorithm>
 #include <type_traits>
 
