@@ -668,11 +668,14 @@ void attn_decode_kernel(KvGeom g, AttnDev p) {
             p.ml[2 * row + 1] = lt;
           }
         } else {
-          const float inv = lt == 0.f ? 0.f : g.v_scale / lt;
+          // (every score -inf: 0, where the sum may be 0 times a NaN or an infinity)
+          const float inv = g.v_scale / lt;
+          const u32 any = lt == 0.f ? 0u : ~0u;
 #pragma unroll
           for (int r = 0; r < kJ; ++r)
             *reinterpret_cast<u32x2 *>(p.a.out + (qrow + c) * D + L::vdim(4 * q, 4 * gr + j0 + r)) =
-                u32x2{cvt_pk_bf16(sum[0][r] * inv, sum[1][r] * inv), cvt_pk_bf16(sum[2][r] * inv, sum[3][r] * inv)};
+                u32x2{any & cvt_pk_bf16(sum[0][r] * inv, sum[1][r] * inv),
+                      any & cvt_pk_bf16(sum[2][r] * inv, sum[3][r] * inv)};
           if (teller) {
             if (p.a.lse) p.a.lse[qrow + c] = lt == 0.f ? kNegInf : (mh + log2f(lt)) * kLn2;
             if (kMass) {
@@ -805,7 +808,7 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(KvGeom g, AttnDev p
       f[w] = factor(hm[w], m);
       l = fmaf(hl[w], f[w], l);
     }
-    const float inv = l == 0.f ? 0.f : g.v_scale / l;
+    const float inv = g.v_scale / l;
     if (int(threadIdx.x) < D / 2) {  // two columns a thread
       float t0 = 0.f, t1 = 0.f;
 #pragma unroll
@@ -813,7 +816,7 @@ __global__ __launch_bounds__(kThreads) void attn_join_kernel(KvGeom g, AttnDev p
         t0 = fmaf(acc[w][2 * threadIdx.x], f[w], t0);
         t1 = fmaf(acc[w][2 * threadIdx.x + 1], f[w], t1);
       }
-      reinterpret_cast<u32 *>(p.a.out + int64_t(qr) * D)[threadIdx.x] = cvt_pk_bf16(t0 * inv, t1 * inv);
+      reinterpret_cast<u32 *>(p.a.out + int64_t(qr) * D)[threadIdx.x] = l == 0.f ? 0u : cvt_pk_bf16(t0 * inv, t1 * inv);
     }
     if (p.a.lse && threadIdx.x == 0) p.a.lse[qr] = l == 0.f ? kNegInf : (m + log2f(l)) * kLn2;
     return;

@@ -900,3 +900,27 @@ def test_attention_begin_counts_places_also_after_an_eviction():
         c.begins = [begin]
         _, q, out, lse, sc = run_attention(c, 4, pool=pool)
         check_attention(c, q, sc, out, lse)
+
+
+@pytest.mark.parametrize("dim,page,lens", [(64, 16, [1, 40, 128]), (128, 64, [3000, 5]), (256, 4, [700])])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_attention_of_nothing_seen_is_zero_whatever_the_values(dim, page, lens, value):
+    """Every score -inf: out = 0 and lse = -inf also where the values are NaN or infinite."""
+    c = make_cache(dim, lens, None, 2, dim, page)
+    c.k[...] = 0.0
+    c.k[..., 0] = float("-inf")
+    c.v[...] = value
+    import gated_delta_rule_slot_amd as gdn
+
+    pool = device_pool(c)
+    B, Hq = len(lens), 6
+    q = torch.zeros(B, Hq, dim, dtype=torch.bfloat16)
+    q[..., 0] = 1.0
+    for flags in (0, 1):
+        out = torch.full((B, Hq, dim), -7.0, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((B, Hq), -7.0, device="cuda")
+        ws = torch.empty(gdn.attn_workspace_bytes(pool, B, Hq, max(lens), flags), dtype=torch.uint8, device="cuda")
+        gdn.attn_decode_paged(pool, 0, i32(c.slots), i32(lens), q.cuda(), out, max(lens), scale=0.125, flags=flags,
+                              lse=lse, workspace=ws)
+        assert not out.float().any() and torch.isneginf(lse).all()
+        assert torch.equal(pool.mass.cpu(), c.mass)
