@@ -924,3 +924,46 @@ def test_attention_of_nothing_seen_is_zero_whatever_the_values(dim, page, lens, 
                               lse=lse, workspace=ws)
         assert not out.float().any() and torch.isneginf(lse).all()
         assert torch.equal(pool.mass.cpu(), c.mass)
+
+
+def test_forms_of_much_shared_memory_in_a_graph():
+    """Attention of head dim 256 (78 KB a workgroup) and a plan of 36864 tokens (156 KB)
+    captured together, replayed with new lengths and weights between eager work."""
+    import gated_delta_rule_slot_amd as gdn
+
+    n, budget = 36864, 30000
+    g = torch.Generator(device="cuda").manual_seed(5)
+    k, v = (torch.randn(1, n // 128 + 1, 1, 128, 256, device="cuda", generator=g).to(torch.bfloat16) for _ in range(2))
+    table = torch.zeros(2, n // 128, dtype=torch.int32, device="cuda")
+    table[1] = torch.randperm(n // 128, device="cuda", generator=g) + 1
+    mass = torch.rand(1, 2, 1, n, device="cuda", generator=g)
+    pos = torch.arange(n, dtype=torch.int32, device="cuda").expand(1, 2, 1, n).contiguous()
+    pool = gdn.kv_pool_create(k, v, table, mass=mass, pos=pos)
+    q = torch.randn(1, 8, 256, device="cuda", generator=g).to(torch.bfloat16)
+    slots, lens, nxt = i32([1]), i32([n]), i32([n])
+    ws = torch.empty(gdn.attn_workspace_bytes(pool, 1, 8, n, 1), dtype=torch.uint8, device="cuda")
+    out = torch.zeros(1, 8, 256, dtype=torch.bfloat16, device="cuda")
+    nm, mv = (torch.zeros(1, 1, 1, *x, dtype=torch.int32, device="cuda") for x in ((), (budget, 2)))
+    lo = torch.zeros_like(lens)
+
+    def step():
+        gdn.attn_decode_paged(pool, 0, slots, lens, q, out, n, scale=0.0625, flags=1, workspace=ws)
+        gdn.kv_evict_plan(pool, 0, 1, slots, lens, nxt, n, budget, 4, 64, nm, mv, lo)
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for turn in range(4):
+        lens.fill_(n - 1001 * turn)
+        mass.copy_(torch.rand(mass.shape, device="cuda", generator=g))
+        m0 = mass.clone()
+        step()
+        want = out.clone(), nm.clone(), mv.clone()
+        m1 = mass.clone()
+        mass.copy_(m0)
+        for t in (out, nm, lo):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(nm, want[1]) and torch.equal(mass, m1), turn
+        assert torch.equal(mv, want[2]) and int(nm) > 0 and int(lo) == min(int(lens), budget)
