@@ -32,6 +32,9 @@ struct Rows {
 bool overlap(const Rows &a, const void *p, int64_t bytes) {
   if (!a.base || !p) return false;
   const __int128 base = reinterpret_cast<uintptr_t>(a.base), lo = reinterpret_cast<uintptr_t>(p);
+  const __int128 last = base + __int128(a.n - 1) * a.stride;  // the last row's first byte
+  if (last + a.row <= lo || lo + bytes <= base) return false;  // (mostly so, and no division)
+  if (a.n == 1) return true;
   const __int128 before = lo - base - a.row;  // the first row that ends behind lo
   const __int128 i = before < 0 ? 0 : before / a.stride + 1;
   return i < a.n && base + i * a.stride < lo + bytes;
