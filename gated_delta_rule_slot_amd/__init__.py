@@ -11,7 +11,8 @@ The entry points mirror include/gdn_slot.h one to one:
 those of include/gdn_kv.h (the full-attention layers' paged cache beside the state pool)
 
   kv_pool_bytes, kv_pool_create, kv_append, attn_workspace_bytes, attn_decode_paged,
-  kv_evict_plan, kv_evict_apply, block_norm
+  kv_evict_plan, kv_evict_apply, block_norm, kv_batch_map, kv_release, rope_frequencies,
+  rope_append, attn_prefill_workspace_bytes, attn_prefill_paged
 
 and the host checkpoint index of include/gdn_ckpt.h (CheckpointIndex,
 ckpt_chain_hashes).
@@ -31,7 +32,9 @@ from ._binding import (  # noqa: F401
     state_pool_create, track_snapshot,
 )
 from ._kv import (  # noqa: F401
-    ACT_NONE, ACT_SIGMOID, ACT_SILU, ATTN_ACCUM_MASS, ERRW_BAD_PAGE, GDN_F8_E4M3, KvPool, NORM_PLUS_ONE,
-    attn_decode_paged, attn_workspace_bytes, block_norm, kv_append, kv_evict_apply, kv_evict_plan,
-    kv_pool_bytes, kv_pool_create,
+    ACT_NONE, ACT_SIGMOID, ACT_SILU, ATTN_ACCUM_MASS, ERRW_BAD_PAGE, ERRW_NO_PAGES, GDN_F8_E4M3, KvPool,
+    NORM_PLUS_ONE, ROPE_BANDS, ROPE_HALF, ROPE_INTERLEAVED, ROPE_LINEAR, ROPE_NTK, ROPE_PLAIN, ROPE_YARN,
+    attn_decode_paged, attn_prefill_paged, attn_prefill_workspace_bytes, attn_workspace_bytes, block_norm,
+    kv_append, kv_batch_map, kv_evict_apply, kv_evict_plan, kv_pool_bytes, kv_pool_create, kv_release,
+    rope_append, rope_frequencies,
 )

@@ -1,5 +1,5 @@
-"""ctypes binding of include/gdn_kv.h: the paged key-value cache, its attention and its
-eviction, and the norm between blocks.  Argument marshalling only, as in _binding.py:
+"""ctypes binding of include/gdn_kv.h: the paged key-value cache, its page tables, its attention
+and its eviction, rotary positions, and the norm between blocks.  Argument marshalling only, as in _binding.py:
 each function carries the C entry point's name and every step runs in the library's
 kernels.  All tensors of a call live on the current HIP device.
 """
@@ -22,6 +22,9 @@ ERRW_BAD_PAGE = 16
 ATTN_ACCUM_MASS = 1
 ACT_NONE, ACT_SILU, ACT_SIGMOID = 0, 1, 2
 NORM_PLUS_ONE = 1
+ERRW_NO_PAGES = 32
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_YARN, ROPE_BANDS = 0, 1, 2, 3, 4
 
 
 class KvDesc(ct.Structure):
@@ -33,6 +36,11 @@ class KvDesc(ct.Structure):
         ("page_table", ct.c_void_p), ("mass", ct.c_void_p), ("pos", ct.c_void_p),
         ("err_word", ct.c_void_p),
     ]
+
+
+class RopeDesc(ct.Structure):
+    _fields_ = [("rot_dim", ct.c_int32), ("scaling", ct.c_int32), ("base", ct.c_double), ("factor", ct.c_double),
+                ("original_len", ct.c_double), ("low", ct.c_double), ("high", ct.c_double)]
 
 
 _lib.kv_pool_bytes.argtypes = [ct.POINTER(KvDesc), ct.POINTER(_sz), ct.POINTER(_sz)]
@@ -48,8 +56,18 @@ _lib.kv_evict_plan.argtypes = [_vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _i32,
 _lib.kv_evict_apply.argtypes = [_vp, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp]
 _lib.block_norm.argtypes = [_i64, _i32, _i32, _vp, _i64, _vp, _vp, _i64, _i32, _f32, _vp, _vp, _i32, _vp,
                             _i32, _f32, _u32, _vp, _vp]
+_lib.kv_batch_map.argtypes = [_vp, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                              _vp, _vp, _vp]
+_lib.kv_release.argtypes = [_vp, _i32, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp]
+_lib.rope_frequencies.argtypes = [ct.POINTER(RopeDesc), ct.POINTER(ct.c_double), ct.POINTER(_f32)]
+_lib.rope_append.argtypes = [_vp, _i32, _i32, _vp, _vp, _vp, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i32,
+                             _i32, _vp, _f32, _vp]
+_lib.attn_prefill_workspace_bytes.argtypes = [_vp, _i32, _i32, _i32, _i32, _i32, ct.POINTER(_sz)]
+_lib.attn_prefill_paged.argtypes = [_vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _i64, _f32, _i32,
+                                    _i32, _vp, _vp, _vp, _sz, _vp]
 for _f in ("kv_pool_bytes", "kv_pool_create", "kv_append", "attn_workspace_bytes", "attn_decode_paged",
-           "kv_evict_plan", "kv_evict_apply", "block_norm"):
+           "kv_evict_plan", "kv_evict_apply", "block_norm", "kv_batch_map", "kv_release", "rope_frequencies",
+           "rope_append", "attn_prefill_workspace_bytes", "attn_prefill_paged"):
     getattr(_lib, _f).restype = ct.c_int
 
 
@@ -235,6 +253,99 @@ def kv_evict_apply(pool: KvPool, layer_begin, layer_end, slot_table, n_moves, mo
         pool.handle, layer_begin, layer_end, B, M, _arg(slot_table, torch.int32, B, "slot_table", dev),
         _arg(n_moves, torch.int32, L * B * pool.kv_heads, "n_moves", dev),
         _arg(moves, torch.int32, 0, "moves", dev), _on_stream(stream, dev)))
+
+
+def kv_batch_map(pool: KvPool, slot_table, kv_len, free_pages, n_free, cu_seqlens, slot_out, kv_len_out,
+                 token_slot, token_index, new_len=None, next_pos=None, next_pos_out=None, token_pos=None,
+                 n_free_out=None, stream=None):
+    """Pages, ``cu_seqlens`` int32 [batch + 1] and token maps ``token_slot``, ``token_index``, ``token_pos``
+    int32 [max_tokens] of a step that gives request b ``new_len[b]`` tokens (default 1) behind its
+    ``kv_len[b]``; ``slot_out``, ``kv_len_out`` (may be ``kv_len``), ``next_pos_out`` (may be ``next_pos``)
+    int32 [batch].  Pages come from ``free_pages[:n_free]``; ``n_free_out`` defaults to ``n_free``."""
+    dev = _on(pool.device)
+    B, T = slot_table.numel(), token_slot.numel()
+    n_free_out = n_free if n_free_out is None else n_free_out
+    i32 = torch.int32
+    _check(_lib.kv_batch_map(
+        pool.handle, B, T, _arg(slot_table, i32, B, "slot_table", dev), _arg(kv_len, i32, B, "kv_len", dev),
+        _arg(new_len, i32, B, "new_len", dev), _arg(next_pos, i32, B, "next_pos", dev), free_pages.numel(),
+        _arg(free_pages, i32, 0, "free_pages", dev), _arg(n_free, i32, 1, "n_free", dev),
+        _arg(n_free_out, i32, 1, "n_free_out", dev), _arg(cu_seqlens, i32, B + 1, "cu_seqlens", dev),
+        _arg(slot_out, i32, B, "slot_out", dev), _arg(kv_len_out, i32, B, "kv_len_out", dev),
+        _arg(next_pos_out, i32, B, "next_pos_out", dev), _arg(token_slot, i32, T, "token_slot", dev),
+        _arg(token_index, i32, T, "token_index", dev), _arg(token_pos, i32, T, "token_pos", dev),
+        _on_stream(stream, dev)))
+
+
+def kv_release(pool: KvPool, slot_table, kv_len, free_pages, n_free, keep=None, n_free_out=None, stream=None):
+    """Give the pages of the places from ``keep[b]`` (default 0) to ``kv_len[b]`` back to
+    ``free_pages``; ``n_free_out`` defaults to ``n_free``."""
+    dev = _on(pool.device)
+    B, i32 = slot_table.numel(), torch.int32
+    n_free_out = n_free if n_free_out is None else n_free_out
+    _check(_lib.kv_release(
+        pool.handle, B, _arg(slot_table, i32, B, "slot_table", dev), _arg(kv_len, i32, B, "kv_len", dev),
+        _arg(keep, i32, B, "keep", dev), free_pages.numel(), _arg(free_pages, i32, 0, "free_pages", dev),
+        _arg(n_free, i32, 1, "n_free", dev), _arg(n_free_out, i32, 1, "n_free_out", dev), _on_stream(stream, dev)))
+
+
+def rope_frequencies(rot_dim, base=10000.0, scaling=ROPE_PLAIN, factor=1.0, original_len=0.0, low=1.0, high=32.0):
+    """(float64 [rot_dim / 2] on the CPU: angle per position of each pair, amplitude)."""
+    d = RopeDesc(rot_dim, scaling, base, factor, original_len, low, high)
+    f = (ct.c_double * max(1, rot_dim // 2))()
+    a = _f32()
+    _check(_lib.rope_frequencies(ct.byref(d), f, ct.byref(a)))
+    return torch.tensor(list(f), dtype=torch.float64), a.value
+
+
+def rope_append(pool: KvPool, layer, slot_ids, index, position, q, q_out, k, v, freqs, layout=ROPE_HALF,
+                amplitude=1.0, stream=None):
+    """Turn ``q`` bf16 [n, q_heads, head_dim] into ``q_out`` (may be ``q``; both may be None) and ``k``
+    bf16 [n, kv_heads, head_dim] by ``position`` int32 [n], and store ``k`` and ``v`` at places ``index``
+    of slots ``slot_ids``; rows at any stride.  ``freqs`` float64 [rot_dim / 2] on the device."""
+    dev = _on(pool.device)
+    n = slot_ids.numel()
+    kp, ks = _rows(k, n, pool.kv_heads, pool.head_dim, "k", dev)
+    vp, vs = _rows(v, n, pool.kv_heads, pool.head_dim, "v", dev)
+    H, qp, qs, op, os_ = 0, None, 0, None, 0
+    if q is not None:
+        if q.dim() != 3 or q_out is None:
+            raise ValueError("q must be [n, q_heads, head_dim], and q_out be given with it")
+        H = q.shape[1]
+        qp, qs = _rows(q, n, H, pool.head_dim, "q", dev)
+        op, os_ = _rows(q_out, n, H, pool.head_dim, "q_out", dev)
+    _check(_lib.rope_append(
+        pool.handle, layer, n, _arg(slot_ids, torch.int32, n, "slot_ids", dev),
+        _arg(index, torch.int32, n, "index", dev), _arg(position, torch.int32, n, "position", dev), H, qp, qs, op,
+        os_, kp, ks, vp, vs, 2 * freqs.numel(), layout, _arg(freqs, torch.float64, 0, "freqs", dev), amplitude,
+        _on_stream(stream, dev)))
+
+
+def attn_prefill_workspace_bytes(pool: KvPool, batch, tokens, q_heads, max_len, mass_tokens=0) -> int:
+    n = _sz()
+    _check(_lib.attn_prefill_workspace_bytes(pool.handle, batch, tokens, q_heads, max_len, mass_tokens,
+                                             ct.byref(n)))
+    return n.value
+
+
+def attn_prefill_paged(pool: KvPool, layer, cu_seqlens, slot_table, kv_len, q, out, max_len, kv_begin=None,
+                       window=0, scale=1.0, mass_tokens=0, lse=None, workspace=None, stream=None):
+    """``q`` bf16 [tokens, q_heads, head_dim] (rows at any stride), ``out`` the same, contiguous;
+    ``cu_seqlens`` int32 [batch + 1]; ``slot_table``, ``kv_len`` (with the new tokens), ``kv_begin`` int32
+    [batch]; ``lse`` fp32 [tokens, q_heads]; ``workspace`` uint8 (attn_prefill_workspace_bytes)."""
+    dev = _on(pool.device)
+    B = slot_table.numel()
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, q_heads, head_dim]")
+    T, H = q.shape[:2]
+    qp, qs = _rows(q, T, H, pool.head_dim, "q", dev)
+    _check(_lib.attn_prefill_paged(
+        pool.handle, layer, B, T, H, max_len, _arg(cu_seqlens, torch.int32, B + 1, "cu_seqlens", dev),
+        _arg(slot_table, torch.int32, B, "slot_table", dev), _arg(kv_len, torch.int32, B, "kv_len", dev),
+        _arg(kv_begin, torch.int32, B, "kv_begin", dev), qp, qs, scale, window, mass_tokens,
+        _arg(out, torch.bfloat16, T * H * pool.head_dim, "out", dev), _arg(lse, torch.float32, T * H, "lse", dev),
+        _arg(workspace, torch.uint8, 0, "workspace", dev), workspace.numel() if workspace is not None else 0,
+        _on_stream(stream, dev)))
 
 
 def block_norm(y, out, w_post=None, gate=None, act=ACT_NONE, scale=1.0, residual=None, residual_out=None,

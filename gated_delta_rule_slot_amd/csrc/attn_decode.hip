@@ -185,16 +185,6 @@ __device__ __forceinline__ Words<W> load_words(const char *p) {
   }
   return r;
 }
-// four e4m3 values as two words of bf16 pairs (exact)
-__device__ __forceinline__ void f8_to_bf16(u32 x, u32 *lo, u32 *hi) {
-  typedef float f2 __attribute__((ext_vector_type(2)));
-  const f2 a = __builtin_amdgcn_cvt_pk_f32_fp8(int(x), false);
-  const f2 b = __builtin_amdgcn_cvt_pk_f32_fp8(int(x), true);
-  // an e4m3 value has 4 significant bits, so its fp32 form's low half is zero
-  *lo = __builtin_amdgcn_perm(__float_as_uint(a[1]), __float_as_uint(a[0]), 0x07060302u);
-  *hi = __builtin_amdgcn_perm(__float_as_uint(b[1]), __float_as_uint(b[0]), 0x07060302u);
-}
-
 // kWide: pages hold 16 tokens or more, so each half of a tile has adjacent rows and one
 // wave-uniform page id; otherwise each token's row is looked up (128 requests of 2048 tokens,
 // 4 heads of 128: 4-token pages 96.8 us, 16-token pages 91.3 us).

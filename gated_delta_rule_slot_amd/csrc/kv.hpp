@@ -83,6 +83,20 @@ __device__ __forceinline__ void set_err(int32_t *err, int bit) {
   if (err) atomicOr(err, bit);
 }
 
+// Four values / scale as e4m3, limited to its largest value, rounded once to nearest even (the
+// limits keep NaN: both comparisons are false)
+__device__ __forceinline__ uint32_t f8_pack4(const float *x, float scale) {
+  float f[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float t = x[e] / scale;
+    t = t > 448.f ? 448.f : t;
+    f[e] = t < -448.f ? -448.f : t;
+  }
+  const int w = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
+  return uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], w, true));
+}
+
 struct AppendArgs {
   int n;
   const int32_t *slot_ids, *index, *position;
@@ -115,6 +129,53 @@ struct AttnArgs {
   void *workspace;
 };
 hipError_t launch_attn_decode(const gdn_kv_pool *p, int layer, const AttnArgs &a, hipStream_t s);
+
+struct ChunkArgs {
+  int batch, tokens, q_heads, max_len, window, mass_tokens;
+  const int32_t *cu_seqlens, *slot_table, *kv_len, *kv_begin;
+  const uint16_t *q;
+  int64_t q_stride;
+  float scale;
+  uint16_t *out;
+  float *lse;
+  void *workspace;
+};
+// whether the call's rows, tiles and workgroups can be counted
+bool chunk_fits(const gdn_kv_pool *p, int batch, int tokens, int q_heads, int max_len);
+size_t chunk_workspace(const gdn_kv_pool *p, int batch, int tokens, int q_heads, int max_len, int mass_tokens);
+hipError_t launch_attn_prefill(const gdn_kv_pool *p, int layer, const ChunkArgs &a, hipStream_t s);
+
+struct RopeArgs {
+  int n, q_heads;
+  const int32_t *slot_ids, *index, *position;
+  const uint16_t *q;
+  int64_t q_stride;
+  uint16_t *q_out;
+  int64_t q_out_stride;
+  const uint16_t *k, *v;
+  int64_t k_stride, v_stride;
+  int rot_dim, layout;
+  const double *freqs;
+  float amplitude;
+};
+hipError_t launch_rope_append(const gdn_kv_pool *p, int layer, const RopeArgs &a, hipStream_t s);
+
+struct MapArgs {
+  int batch, max_tokens, free_capacity;
+  const int32_t *slot_table, *kv_len, *new_len, *next_pos, *free_pages, *n_free;
+  int32_t *page_table;
+  int32_t *n_free_out, *cu_seqlens, *slot_out, *kv_len_out, *next_pos_out;
+  int32_t *token_slot, *token_index, *token_pos;
+};
+hipError_t launch_kv_batch_map(const gdn_kv_pool *p, const MapArgs &a, hipStream_t s);
+
+struct ReleaseArgs {
+  int batch, free_capacity;
+  const int32_t *slot_table, *kv_len, *keep, *n_free;
+  int32_t *page_table;
+  int32_t *free_pages, *n_free_out;
+};
+hipError_t launch_kv_release(const gdn_kv_pool *p, const ReleaseArgs &a, hipStream_t s);
 
 struct NormArgs {
   int64_t tokens;

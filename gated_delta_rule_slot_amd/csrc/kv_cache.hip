@@ -16,8 +16,7 @@ namespace {
 // non-temporal loads (16.1 us) were slower, non-temporal stores the same.
 constexpr int kAppendThreads = 256;
 
-// 8 bf16 values / scale, limited to e4m3's largest value, rounded once to nearest even
-// (the limits keep NaN: both comparisons are false)
+// 8 bf16 values / scale as e4m3
 __device__ __forceinline__ u32x2 quantise8(const u32x4 &x, float scale) {
   u32x2 r;
 #pragma unroll
@@ -26,12 +25,9 @@ __device__ __forceinline__ u32x2 quantise8(const u32x4 &x, float scale) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const uint32_t w = x[2 * p + (e >> 1)];
-      float t = __uint_as_float((e & 1) ? (w & 0xffff0000u) : (w << 16)) / scale;
-      t = t > 448.f ? 448.f : t;
-      f[e] = t < -448.f ? -448.f : t;
+      f[e] = __uint_as_float((e & 1) ? (w & 0xffff0000u) : (w << 16));
     }
-    int w = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
-    r[p] = uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], w, true));
+    r[p] = f8_pack4(f, scale);
   }
   return r;
 }

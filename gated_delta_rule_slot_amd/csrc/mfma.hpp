@@ -112,6 +112,16 @@ __device__ __forceinline__ float bf16_elem(const u32x4 &v, int e) {
   return __uint_as_float((e & 1) ? (w & 0xffff0000u) : (w << 16));
 }
 
+// four e4m3 values as two words of bf16 pairs (exact)
+__device__ __forceinline__ void f8_to_bf16(uint32_t x, uint32_t *lo, uint32_t *hi) {
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  const f2 a = __builtin_amdgcn_cvt_pk_f32_fp8(int(x), false);
+  const f2 b = __builtin_amdgcn_cvt_pk_f32_fp8(int(x), true);
+  // an e4m3 value has 4 significant bits, so its fp32 form's low half is zero
+  *lo = __builtin_amdgcn_perm(__float_as_uint(a[1]), __float_as_uint(a[0]), 0x07060302u);
+  *hi = __builtin_amdgcn_perm(__float_as_uint(b[1]), __float_as_uint(b[0]), 0x07060302u);
+}
+
 // 2^x on the hardware unit; a result below 2^-126 comes out as zero, which only
 // drops decay products that are negligible next to the unit-scale terms they join
 __device__ __forceinline__ float fexp2(float x) { return __builtin_amdgcn_exp2f(x); }

@@ -17,6 +17,14 @@
  *   block_norm         norm after a block, gate, residual scale and sum, norm before
  *                      the next block, in one pass (also the recurrence's gated norm)
  *
+ * and, for prompts and their chunks (single tokens too),
+ *
+ *   kv_batch_map       page tables, token maps and cu_seqlens of a step from the requests'
+ *                      lengths, pages taken from a free list
+ *   kv_release         pages given back to it
+ *   rope_append        rotary positions of queries and keys, keys and values stored
+ *   attn_prefill_paged attention of a chunk of new tokens per request over its pages
+ *
  * Formulas, with t over the visible tokens begin <= t < len of the request, h a query
  * head and g = h / (q_heads / kv_heads) its key-value head:
  *
@@ -192,6 +200,147 @@ gdn_status kv_evict_plan(gdn_kv_pool_t pool, int32_t layer_begin, int32_t layer_
 gdn_status kv_evict_apply(gdn_kv_pool_t pool, int32_t layer_begin, int32_t layer_end,
                           int32_t batch, int32_t max_moves, const int32_t *slot_table,
                           const int32_t *n_moves, const int32_t *moves, void *stream);
+
+/* the free list of a kv_batch_map is too short for a request */
+enum { GDN_ERRW_NO_PAGES = 32 };
+
+/* Prepare a step of `batch` requests: request b gets new_len[b] new tokens at places
+ * kv_len[b] ... of its slot.
+ * batch       at most 65535;  max_tokens: size of the token arrays, at most 2^26 - 2
+ * slot_table, kv_len   device int32 [batch]
+ * new_len     device int32 [batch] or NULL (= 1 each)
+ * next_pos    device int32 [batch] or NULL (= kv_len): position of the first new token
+ * free_pages  device int32 [free_capacity]: the first n_free[0] entries are free pages
+ * n_free      device int32 [1];  n_free_out: device int32 [1], may be n_free
+ * The running sums of max(new_len, 0), limited to max_tokens, go to cu_seqlens [batch + 1].
+ * A request is served if its slot is live (slots must be distinct), no number is negative,
+ * kv_len + new_len is at most max_pages * page_size, its tokens end within max_tokens, its
+ * positions below 2^31 (else GDN_ERRW_BAD_SEQLENS), and the pages that it and all such requests
+ * before it lack are at most n_free, or it lacks none (else GDN_ERRW_NO_PAGES).  What it lacks,
+ * entries ceil(kv_len / page_size) ... of its row of the pool's page table (which is written,
+ * const as the descriptor's pointer is), comes from the end of the free list, in the order of
+ * the requests and places: the first page taken is free_pages[n_free - 1].
+ *   slot_out     [batch]  its slot, or 0 if it is not served: the slot_table of the calls that
+ *                follow, which skip such a request
+ *   kv_len_out   [batch]  kv_len + new_len, or kv_len as it is; may be kv_len
+ *   next_pos_out [batch] or NULL, the same of next_pos; may be next_pos
+ *   token_slot, token_index, token_pos (or NULL)  [max_tokens]  slot, place and position of
+ *                every token; 0, 0, 0 for tokens of requests that are not served and behind
+ *                the last request
+ * All device int32.  Apart from the two pairs named, what the call writes must not overlap what
+ * it reads (page_table is only written) or each other. */
+gdn_status kv_batch_map(gdn_kv_pool_t pool, int32_t batch, int32_t max_tokens, const int32_t *slot_table,
+                        const int32_t *kv_len, const int32_t *new_len, const int32_t *next_pos,
+                        int32_t free_capacity, const int32_t *free_pages, const int32_t *n_free,
+                        int32_t *n_free_out, int32_t *cu_seqlens, int32_t *slot_out, int32_t *kv_len_out,
+                        int32_t *next_pos_out, int32_t *token_slot, int32_t *token_index,
+                        int32_t *token_pos, void *stream);
+
+/* Give pages back: entries ceil(keep / page_size) .. ceil(kv_len / page_size) - 1 of each request's
+ * row of the page table are put at the end of the free list, in order, and set to 0.
+ * keep        device int32 [batch] or NULL (= 0): places that stay (the new length after a
+ *             kv_evict_apply, or a prefix whose pages other requests have too)
+ * Slots must be distinct and no page be in two rows.  An entry that is no page sets
+ * GDN_ERRW_BAD_PAGE and is left out; so does a page that the list (free_capacity) has no room
+ * for, which stays in the table.  A negative number or kv_len past max_pages * page_size sets
+ * GDN_ERRW_BAD_SEQLENS and skips the request.  n_free_out may be n_free; nothing else that the
+ * call writes (free_pages, page table, n_free_out) may overlap what it reads. */
+gdn_status kv_release(gdn_kv_pool_t pool, int32_t batch, const int32_t *slot_table, const int32_t *kv_len,
+                      const int32_t *keep, int32_t free_capacity, int32_t *free_pages,
+                      const int32_t *n_free, int32_t *n_free_out, void *stream);
+
+/* which values of a head are a pair: i and i + rot_dim / 2, or 2 i and 2 i + 1 */
+enum { GDN_ROPE_HALF = 0, GDN_ROPE_INTERLEAVED = 1 };
+
+/* how the angles are scaled for contexts longer than trained on; theta_i = base^(-2 i / rot_dim) */
+enum {
+  GDN_ROPE_PLAIN = 0,   /* theta_i */
+  GDN_ROPE_LINEAR = 1,  /* theta_i / factor */
+  GDN_ROPE_NTK = 2,     /* theta_i of the base  base * factor^(rot_dim / (rot_dim - 2)) */
+  GDN_ROPE_YARN = 3,    /* between theta_i / factor and theta_i by a ramp over i, from where a pair turns
+                           `high` times over original_len (rounded down) to where it turns `low` times
+                           (rounded up), within [0, rot_dim - 1]; amplitude 0.1 ln(factor) + 1 */
+  GDN_ROPE_BANDS = 4    /* the same by a ramp over the turns, from `low` to `high`; amplitude 1 */
+};
+typedef struct {
+  int32_t rot_dim, scaling;
+  double base, factor, original_len, low, high; /* the last three for YARN and BANDS */
+} gdn_rope_desc;
+
+/* Angles per position of the rot_dim / 2 pairs, and the factor of the turned values.  Host memory,
+ * host arithmetic; copy freqs to the device for rope_append.  rot_dim even, in [2, 256] (4 and
+ * more for NTK); base > 1, factor >= 1, original_len > 0 and high > low > 0, all finite. */
+gdn_status rope_frequencies(const gdn_rope_desc *desc, double *freqs, float *amplitude);
+
+/* Turn the queries and keys of n tokens by their positions, and store keys and values as
+ * kv_append does: per pair (x, y) and a = position * freqs[i],
+ *   (x, y) -> amplitude * (x cos a - y sin a, y cos a + x sin a)
+ * and the values of a head from rot_dim on as they are.
+ * slot_ids, index, position   as in kv_append; position is always required and may be negative
+ * q           device bf16, token i at q + i * q_stride, [q_heads][head_dim] there; q_heads may be 0
+ *             (no queries)
+ * q_out       device bf16: q itself with q_out_stride = q_stride (turned in place), or memory of its
+ *             own at any stride.  Tokens whose slot id is no slot are left as they are; a token with
+ *             a bad index or page has its queries turned
+ * k, v        device bf16, [kv_heads][head_dim] per token
+ * rot_dim     a multiple of 16 up to head_dim;  layout: GDN_ROPE_HALF or GDN_ROPE_INTERLEAVED
+ * freqs       device double [rot_dim / 2];  amplitude: finite
+ * Strides are in elements, multiples of 8 and at least a token's values; rows 16-byte aligned.
+ * Angles are worked out in fp64 (to 2^-24 of a turn for any position whose angle is below 2^28
+ * turns), the rest in fp32; each output is rounded once (a stored key: from fp32, after
+ * the division by k_scale in a GDN_F8_E4M3 pool).  q_out must not overlap q otherwise, k, v or the
+ * int32 arrays; no input may lie where the call writes in the pool. */
+gdn_status rope_append(gdn_kv_pool_t pool, int32_t layer, int32_t n, const int32_t *slot_ids,
+                       const int32_t *index, const int32_t *position, int32_t q_heads, const uint16_t *q,
+                       int64_t q_stride, uint16_t *q_out, int64_t q_out_stride, const uint16_t *k,
+                       int64_t k_stride, const uint16_t *v, int64_t v_stride, int32_t rot_dim,
+                       int32_t layout, const double *freqs, float amplitude, void *stream);
+
+/* Workspace of attn_prefill_paged for `tokens` new tokens of `batch` requests, of up to max_len
+ * tokens each with what is cached.  Pure host arithmetic; may be 0. */
+gdn_status attn_prefill_workspace_bytes(gdn_kv_pool_t pool, int32_t batch, int32_t tokens,
+                                        int32_t q_heads, int32_t max_len, int32_t mass_tokens,
+                                        size_t *bytes);
+
+/* Attention of a chunk of new tokens per request over one layer's cache (the chunk's own keys
+ * and values are stored before).  Request b's new tokens are cu_seqlens[b] .. cu_seqlens[b + 1] - 1
+ * of q; with n of them, token i stands at place t = kv_len[b] - n + i and sees the places
+ *   max(kv_begin[b], t - window + 1) .. t      (from kv_begin[b] on if window is 0)
+ * Formulas, head groups and slots as in attn_decode_paged; one token per request is the same as there.
+ * tokens      rows of q and out; cu_seqlens[batch] may be less, and the rows behind it are left as
+ *             they are
+ * q_heads     as in attn_decode_paged
+ * max_len     host int: no request has more tokens with the new ones (one that has, or fewer than new
+ *             ones, or a negative begin, sets GDN_ERRW_BAD_SEQLENS and is skipped).  It decides how
+ *             the length is split when there are few rows, so a close bound is faster
+ * cu_seqlens  device int32 [batch + 1], not falling, from 0 or more; a request whose range is not
+ *             within [0, tokens] sets GDN_ERRW_BAD_SEQLENS and its rows are left as they are
+ * slot_table, kv_len   device int32 [batch]; kv_begin: device int32 [batch] or NULL (= 0)
+ * q           device bf16, token i at q + i * q_stride (elements, a multiple of 8, at least q_heads *
+ *             head_dim; 16-byte aligned), [q_heads][head_dim] there
+ * window      >= 0; 0: none.  It and kv_begin count places: see attn_decode_paged for slots that were
+ *             cut
+ * mass_tokens >= 0: the last that many new tokens of each request add their weights to the pool's
+ *             mass (which it must have; live slots must be distinct then), so that an eviction right
+ *             after a prompt has something to go by; 0: none do.  Only visible places' entries change
+ * out         device bf16 [tokens][q_heads][head_dim], 16-byte aligned
+ * lse         device fp32 [tokens][q_heads] or NULL
+ * workspace   attn_prefill_workspace_bytes(...) bytes, 256-byte aligned; its contents are not read
+ *             across calls
+ * What the call writes (out, lse, workspace, with mass_tokens the layer's mass, and the error
+ * word) must not overlap what it reads or each other.
+ * A token that sees nothing (its request is skipped, or no place is visible, or every score is -inf)
+ * gets out = 0 and lse = -inf and adds no weight.  Places that a token does not see never reach its
+ * result, whatever their rows hold (a chunk with NaN or infinite values is walked twice).  Infinite
+ * values and scores, and the range of the values' sum, are as in attn_decode_paged.  Weights are
+ * rounded to bf16 for the product with the values.  The result does not depend on the order in
+ * which the workgroups run. */
+gdn_status attn_prefill_paged(gdn_kv_pool_t pool, int32_t layer, int32_t batch, int32_t tokens,
+                              int32_t q_heads, int32_t max_len, const int32_t *cu_seqlens,
+                              const int32_t *slot_table, const int32_t *kv_len, const int32_t *kv_begin,
+                              const uint16_t *q, int64_t q_stride, float scale, int32_t window,
+                              int32_t mass_tokens, uint16_t *out, float *lse, void *workspace,
+                              size_t workspace_bytes, void *stream);
 
 /* gate activations of block_norm */
 enum { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1, GDN_ACT_SIGMOID = 2 };
