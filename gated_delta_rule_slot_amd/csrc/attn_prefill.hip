@@ -671,7 +671,7 @@ int64_t chunk_tiles(int batch, int tokens, int group) { return int64_t(tokens) *
 // Parts that a tile's places are divided into: workgroups for two on every compute unit, of 512
 // places or more each (by the bound max_len).
 int chunk_parts(const gdn_kv_pool *p, int64_t tiles, int max_len) {
-  const int64_t groups = tiles * p->d.kv_heads;
+  const int64_t groups = std::max<int64_t>(1, tiles * p->d.kv_heads);
   const int64_t want = (2 * kCUs + groups - 1) / groups;
   return int(std::max<int64_t>(1, std::min<int64_t>(want, max_len / 512)));
 }
