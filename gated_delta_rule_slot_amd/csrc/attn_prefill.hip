@@ -25,6 +25,7 @@
 // instructions again.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "kv.hpp"
 #include "lanes.hpp"
@@ -33,6 +34,9 @@
 namespace gdn {
 namespace {
 
+#ifndef GDN_NQ
+#define GDN_NQ 1
+#endif
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kCUs = 256;
@@ -41,7 +45,7 @@ constexpr float kLn2 = 0.693147180559945309417f;
 constexpr float kNegInf = -__builtin_inff();
 constexpr float kGrowth = 8.f;  // log2 of how far the maximum may pass the reference
 
-constexpr int kRows = 32 * kWaves;  // rows of a workgroup
+constexpr int kRows = 32 * kWaves;  // rows of a workgroup, for each block of its waves
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4t __attribute__((ext_vector_type(4)));
@@ -53,8 +57,9 @@ struct ChunkDev {
   ChunkArgs a;
   int group, tiles, parts;
   float c;          // |scale * k_scale| in log2 units
-  uint32_t flip;    // the scale's sign, for two bf16 queries
-  float *o, *ml;    // parts > 1: [tile][kv head][part][kRows] rows of O, and of m and l
+  uint32_t flip, keep;  // for two bf16 queries: the scale's sign, and 0 if it is 0 (c is 1 then)
+  int rows;         // of a tile
+  float *o, *ml;    // parts > 1: [tile][kv head][part][rows] rows of O, and of m and l
   float *lse;       // [tokens][q_heads], or NULL
 };
 
@@ -73,8 +78,32 @@ __device__ __forceinline__ f32x16 mfma32(const bf16x8 &a, const bf16x8 &b, const
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
+// ---- values that are not finite ---------------------------------------------
+// 0 * NaN is NaN, so a row whose weight of a place is 0 because it does not see it would take that
+// place's NaN or infinite values.  Where a workgroup's result is not finite, its tile is walked
+// again with every such value as 0, which gives the finite part of the sums, then with 1 in the
+// place of inf and NaN and 0 elsewhere, then with 1 in the place of -inf and NaN: a sum above 0
+// says that the row sees one with a weight above 0.
+enum { kAsIs, kFinite, kUp, kDown };
+__device__ __forceinline__ u32x4 sorted(u32x4 x, int kind) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t r = 0;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint32_t v = (x[i] >> (16 * e)) & 0xffffu, a = v & 0x7fffu;
+      const bool mark = a > 0x7f80u || v == (kind == kUp ? 0x7f80u : 0xff80u);
+      r |= (kind == kFinite ? (a < 0x7f80u ? v : 0u) : mark ? 0x3f80u : 0u) << (16 * e);
+    }
+    x[i] = r;
+  }
+  return x;
+}
+// a sum with an infinite (or NaN) value added
+__device__ __forceinline__ float beyond(float sum, int kind) { return sum + (kind == kUp ? -kNegInf : kNegInf); }
+
 // ---- which rows a tile has -------------------------------------------------
-// The tiles of request b begin at cu[b] * group / kRows + b: at least as many as it needs, and
+// The tiles of request b begin at cu[b] * group / rows + b: at least as many as it needs, and
 // found from cu alone, so that no list of tiles has to be made first.
 struct Chunk {
   int b, bos, n, rows0;  // request, its first token and number of tokens, the tile's first row
@@ -83,7 +112,7 @@ struct Chunk {
 };
 __device__ __forceinline__ Chunk chunk_of(const KvGeom &g, const ChunkDev &p, int tile, bool tell) {
   const table_t cu = (table_t)p.a.cu_seqlens;
-  auto first = [&](int b) { return int64_t(cu[b]) * p.group / kRows + b; };
+  auto first = [&](int b) { return int64_t(cu[b]) * p.group / p.rows + b; };
   int lo = 0, hi = p.a.batch;  // the last request whose tiles begin at `tile` or before
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -94,7 +123,7 @@ __device__ __forceinline__ Chunk chunk_of(const KvGeom &g, const ChunkDev &p, in
   r.b = lo;
   r.bos = cu[lo];
   const int eos = cu[lo + 1];
-  const int64_t at = (tile - first(lo)) * kRows;
+  const int64_t at = (tile - first(lo)) * p.rows;
   const bool ok = r.bos >= 0 && eos >= r.bos && eos <= p.a.tokens;
   r.n = ok ? eos - r.bos : 0;
   r.any = ok && at >= 0 && at < int64_t(r.n) * p.group;
@@ -134,19 +163,19 @@ struct Tile {
   static constexpr int kLanes = SB / 16;         // lanes that load a row
   static constexpr int kLoadRows = 64 / kLanes;  // rows of a wave's load
   static constexpr int kLoads = KT / (kWaves * kLoadRows);
-  static constexpr int kScratch = 16 * 32 * 4;   // weights of 16 places, per wave
-  static constexpr int kShared = 4 * kBytes + kWaves * kScratch + 16;
+  static constexpr int kShared = 4 * kBytes + 16;
 };
 
 // kWide: pages hold 16 tokens or more, so that the rows of a wave's load lie in one page.
-template <int D, bool kF8, bool kWide>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2)))
+// NQ: blocks of 32 rows of a wave.
+template <int D, bool kF8, bool kWide, int NQ>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(NQ == 1 ? 2 : 1)))
 void attn_prefill_kernel(KvGeom g, ChunkDev p) {
   using T = Tile<D, kF8>;
-  constexpr int KT = T::KT, KB = KT / 32, KS = D / 16, DB = D / 32, NL = T::kLoads;
+  constexpr int KT = T::KT, KB = KT / 32, KS = D / 16, DB = D / 32, NL = T::kLoads, ROWS = kRows * NQ;
   extern __shared__ __attribute__((aligned(16))) char lds[];
   // a tile (by its number's parity) that has a page outside the pool
-  int *const sbad = reinterpret_cast<int *>(lds + 4 * T::kBytes + kWaves * T::kScratch);
+  int *const sbad = reinterpret_cast<int *>(lds + 4 * T::kBytes);
 
   const int lane = threadIdx.x & 63, c = lane & 31, half = lane >> 5;
   const int wave = uniform(threadIdx.x >> 6);
@@ -160,34 +189,42 @@ void attn_prefill_kernel(KvGeom g, ChunkDev p) {
   if (!ch.any) return;
 
   const int G = p.group, all = ch.n * G;
-  const int row0 = ch.rows0 + 32 * wave;
+  const int row0 = ch.rows0 + 32 * NQ * wave;
   const bool wlive = ch.live && row0 < all;
-  const int row = min(row0 + c, all - 1);  // (rows behind the last repeat it and are not stored)
-  const int token = row / G, head = h * G + (row - token * G);
-  const int place0 = ch.len - ch.n;        // of the first new token
-  const int place = place0 + token, from = seen_from(p, ch.begin, place);
-  const int wfirst = place0 + min(row0, all - 1) / G, wlast = place0 + min(row0 + 31, all - 1) / G;
+  const int place0 = ch.len - ch.n;  // of the first new token
+  int place[NQ], from[NQ];
+#pragma unroll
+  for (int n = 0; n < NQ; ++n) {
+    // (rows behind the last repeat it and are not stored)
+    place[n] = place0 + min(row0 + 32 * n + c, all - 1) / G;
+    from[n] = seen_from(p, ch.begin, place[n]);
+  }
+  const int wfirst = place0 + min(row0, all - 1) / G, wlast = place0 + min(row0 + 32 * NQ - 1, all - 1) / G;
   const int wfrom = seen_from(p, ch.begin, wfirst), wfrom_last = seen_from(p, ch.begin, wlast);
 
   // tiles of the workgroup: what its rows see, and this part of it
   int t0 = 0, t1 = 0;
   if (ch.live) {
-    const int gfirst = place0 + ch.rows0 / G, glast = place0 + min(ch.rows0 + kRows - 1, all - 1) / G;
+    const int gfirst = place0 + ch.rows0 / G, glast = place0 + min(ch.rows0 + ROWS - 1, all - 1) / G;
     const int lo = seen_from(p, ch.begin, gfirst) / KT, hi = glast / KT + 1;
     const int per = (max(hi - lo, 0) + p.parts - 1) / p.parts;
     t0 = lo + part * per;
     t1 = min(hi, t0 + per);
   }
 
-  bf16x8 q[KS];
+  bf16x8 q[NQ][KS];
   if (wlive && t0 < t1) {
-    const uint16_t *src = p.a.q + (ch.bos + token) * p.a.q_stride + int64_t(head) * D + 8 * half;
 #pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      u32x4 w = *reinterpret_cast<const u32x4 *>(src + 16 * s);
+    for (int n = 0; n < NQ; ++n) {
+      const int row = min(row0 + 32 * n + c, all - 1), token = row / G, head = h * G + (row - token * G);
+      const uint16_t *src = p.a.q + (ch.bos + token) * p.a.q_stride + int64_t(head) * D + 8 * half;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] ^= p.flip;
-      q[s] = __builtin_bit_cast(bf16x8, w);
+      for (int s = 0; s < KS; ++s) {
+        u32x4 w = *reinterpret_cast<const u32x4 *>(src + 16 * s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = (w[i] ^ p.flip) & p.keep;
+        q[n][s] = __builtin_bit_cast(bf16x8, w);
+      }
     }
   }
 
@@ -196,6 +233,7 @@ void attn_prefill_kernel(KvGeom g, ChunkDev p) {
   auto load_row = [&](int j) { return (j * kWaves + wave) * T::kLoadRows; };  // first row of load j
   const table_t table = (table_t)(g.page_table + int64_t(max(ch.slot, 0)) * g.max_pages);
   const int page_mask = (1 << g.page_shift) - 1;
+  const int loff = (kWide ? lrow * T::RB : 0) + ((lpiece ^ twist<D>(wave * T::kLoadRows + lrow)) << 4);
   int ids[kWide ? NL : 1];
   auto load_ids = [&](int t) {
     if constexpr (kWide) {
@@ -239,8 +277,10 @@ void attn_prefill_kernel(KvGeom g, ChunkDev p) {
       char *to = lds + (t & 1) * 2 * T::kBytes;
 #pragma unroll
       for (int j = 0; j < NL; ++j) {
-        const int r = load_row(j) + lrow;
-        const uint32_t off = uint32_t(kWide ? lrow * T::RB : 0) + ((lpiece ^ twist<D>(r)) << 4);
+        // (the twist of the rows of load j differs from load 0's in one bit at most)
+        constexpr int kStep = kWaves * T::kLoadRows;
+        static_assert(kStep % 16 == 0 || kStep == 8, "twist");
+        const uint32_t off = uint32_t(loff) ^ (kStep == 8 ? (j & 1) * 32 : 0);
         char *dst = to + load_row(j) * T::RB;
         typedef __attribute__((address_space(1))) const void *gp;
         typedef __attribute__((address_space(3))) void *lp;
@@ -258,6 +298,17 @@ void attn_prefill_kernel(KvGeom g, ChunkDev p) {
         if (hidden >> j & 1) *reinterpret_cast<u32x4 *>(to + load_row(j) * T::RB + lane * 16) = u32x4{0, 0, 0, 0};
     }
   };
+  // the wave's values of the tile replaced as the walk asks for
+  auto sort_rows = [&](int t, int kind) {
+    if constexpr (!kF8) {
+      char *to = lds + (t & 1) * 2 * T::kBytes + T::kBytes;
+#pragma unroll
+      for (int j = 0; j < NL; ++j) {
+        u32x4 *at = reinterpret_cast<u32x4 *>(to + load_row(j) * T::RB + lane * 16);
+        *at = sorted(*at, kind);
+      }
+    }
+  };
   // e4m3: through registers, 16 values a lane
   u32x4 kraw[kF8 ? NL : 1], vraw[kF8 ? NL : 1];
   auto fetch = [&](u32x4 *raw, const char *base) {
@@ -267,7 +318,7 @@ void attn_prefill_kernel(KvGeom g, ChunkDev p) {
         raw[j] = *reinterpret_cast<const u32x4 *>(base + src[j] + (kWide ? lrow * T::SB : 0) + 16 * lpiece);
     }
   };
-  auto put = [&](const u32x4 *raw, char *to, bool zero) {
+  auto put = [&](const u32x4 *raw, char *to, bool zero, int kind) {
     if constexpr (kF8) {
 #pragma unroll
       for (int j = 0; j < NL; ++j) {
@@ -282,6 +333,7 @@ void attn_prefill_kernel(KvGeom g, ChunkDev p) {
           w[0] = a; w[1] = b;
           f8_to_bf16(x[2 * e + 1], &a, &b);
           w[2] = a; w[3] = b;
+          if (kind != kAsIs) w = sorted(w, kind);
           *reinterpret_cast<u32x4 *>(to + r * T::RB + (((2 * lpiece + e) ^ twist<D>(r)) << 4)) = w;
         }
       }
@@ -289,36 +341,43 @@ void attn_prefill_kernel(KvGeom g, ChunkDev p) {
   };
 
   // ---- the walk ----
-  const int kpiece = half ^ twist<D>(c);  // of step 0; step s is 2 s further
-  const int vrow = (lane >> 2) & 3, vpair = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
-  char *const scratch = lds + 4 * T::kBytes + wave * T::kScratch;
+  // keys: row c of a block of 32, piece half of step 0; step s is 2 s further, which the twist
+  // turns into an exclusive or.  Values: row vrow of the half's four, 4 adjacent values of the
+  // block of 32 columns
+  const int vrow = 4 * half + ((lane >> 2) & 3), vpair = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
+  const int kaddr = c * T::RB + ((half ^ twist<D>(c)) << 4);
+  const int vaddr = vrow * T::RB + ((vpair ^ twist<D>(vrow)) << 4) + 8 * (lane & 1);
+  constexpr int kAhead = 4;
 
-  f32x16 o[DB];
-  float m, l;
-  bool careful = false;
-  for (;;) {
+  f32x16 o[NQ][DB];
+  float m[NQ], l[NQ];
+  auto walk = [&](int kind) {
 #pragma unroll
-    for (int b = 0; b < DB; ++b) o[b] = f32x16{};
-    m = kNegInf;
-    l = 0.f;
+    for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+      for (int b = 0; b < DB; ++b) o[n][b] = f32x16{};
+      m[n] = kNegInf;
+      l[n] = 0.f;
+    }
     if (threadIdx.x < 2) sbad[threadIdx.x] = -1;
     __syncthreads();
-    if (t0 < t1) {
-      load_ids(t0);
-      locate(t0);
-      ask(t0);
-      if constexpr (kF8) {
-        char *to = lds + (t0 & 1) * 2 * T::kBytes;
-        fetch(kraw, g.k);
-        fetch(vraw, g.v);
-        put(kraw, to, false);
-        put(vraw, to + T::kBytes, clear);
-      }
-      load_ids(t0 + 1);
+    if (t0 >= t1) return;
+    load_ids(t0);
+    locate(t0);
+    ask(t0);
+    if constexpr (kF8) {
+      char *to = lds + (t0 & 1) * 2 * T::kBytes;
+      fetch(kraw, g.k);
+      fetch(vraw, g.v);
+      put(kraw, to, false, kAsIs);
+      put(vraw, to + T::kBytes, clear, kind);
     }
-    for (int t = t0; t < t1; ++t) {
+    load_ids(t0 + 1);
+    // tile t is there, and the next one on its way
+    auto stage = [&](int t) {
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       if (!kF8 && clear) clear_rows(t);
+      if (!kF8 && kind != kAsIs) sort_rows(t, kind);
       __syncthreads();
       const bool more = t + 1 < t1;
       if (more) {
@@ -330,184 +389,236 @@ void attn_prefill_kernel(KvGeom g, ChunkDev p) {
         }
         load_ids(t + 2);
       }
-      const char *kt = lds + (t & 1) * 2 * T::kBytes, *vt = kt + T::kBytes;
-      const int p0 = t * KT;
-      const bool work = wlive && p0 <= wlast && p0 + KT > wfrom;
-      f32x16 s[KB];
-      if (work) {
+    };
+    auto finish = [&](int t) {
+      if (kF8 && t + 1 < t1) {
+        char *to = lds + ((t + 1) & 1) * 2 * T::kBytes;
+        put(kraw, to, false, kAsIs);
+        put(vraw, to + T::kBytes, clear, kind);
+      }
+    };
+    auto skip = [&](int a, int b) {
+#pragma unroll 1
+      for (int t = a; t < b; ++t) {
+        stage(t);
+        finish(t);
+      }
+    };
+    // the tiles that the wave's rows see
+    const int w0 = wlive ? min(t1, max(t0, wfrom / KT)) : t1, w1 = wlive ? max(w0, min(t1, wlast / KT + 1)) : t1;
+    skip(t0, w0);
+#pragma unroll 1
+    for (int t = w0; t < w1; ++t) {
+      stage(t);
+            const int p0 = t * KT;
+      {
+        f32x16 s[NQ][KB];
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) s[kb] = f32x16{};
+        for (int n = 0; n < NQ; ++n)
 #pragma unroll
-        for (int st = 0; st < KS; ++st)
+          for (int kb = 0; kb < KB; ++kb) s[n][kb] = f32x16{};
+        int ka = kaddr + (t & 1) * 2 * T::kBytes, va = vaddr + (t & 1) * 2 * T::kBytes + T::kBytes;
+        asm volatile("" : "+v"(ka), "+v"(va));  // (addresses are worked out here, not kept over the walk)
+        auto kread = [&](int i) {
+          return *reinterpret_cast<const bf16x8 *>(lds + (ka ^ (32 * (i / KB))) + 32 * (i % KB) * T::RB);
+        };
+        auto vread = [&](int i) {
+          s16x4t v[2];
 #pragma unroll
-          for (int kb = 0; kb < KB; ++kb) {
-            const bf16x8 a = *reinterpret_cast<const bf16x8 *>(kt + (32 * kb + c) * T::RB + ((kpiece ^ (2 * st)) << 4));
-            s[kb] = mfma32(a, q[st], s[kb]);
-          }
+          for (int e = 0; e < 2; ++e)
+            v[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4t *)(
+                lds + (va ^ (64 * (i % DB) + 32 * e)) + (16 * (i / DB) + 8 * e) * T::RB));
+          return __builtin_bit_cast(bf16x8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
+        };
+        bf16x8 ring[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) ring[i] = kread(i);
+#pragma unroll
+        for (int i = 0; i < KS * KB; ++i) {
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int n = 0; n < NQ; ++n) s[n][i % KB] = mfma32(ring[i % kAhead], q[n][i / KB], s[n][i % KB]);
+          if (i + kAhead < KS * KB) ring[i % kAhead] = kread(i + kAhead);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) ring[i] = vread(i);
+        __builtin_amdgcn_sched_barrier(0);
         const bool flagged = sbad[t & 1] == t;
         const bool partial = p0 < wfrom_last || p0 + KT - 1 > wfirst || flagged;
-        uint32_t see[KB];  // bits: the lane's scores whose place the row sees
         if (partial) {
 #pragma unroll
-          for (int kb = 0; kb < KB; ++kb) {
-            see[kb] = 0;
+          for (int n = 0; n < NQ; ++n)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int at = p0 + 32 * kb + 8 * (e >> 2) + 4 * half + (e & 3);
-              bool on = at <= place && at >= from;
-              if (flagged && on) {
-                const int id = g.page_table[int64_t(ch.slot) * g.max_pages + (at >> g.page_shift)];
-                on = id > 0 && id < g.pages;
+            for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const int at = p0 + 32 * kb + 8 * (e >> 2) + 4 * half + (e & 3);
+                if (at > place[n] || at < from[n]) s[n][kb][e] = kNegInf;
               }
-              if (!on) s[kb][e] = kNegInf;
-              see[kb] |= on ? 1u << e : 0u;
-            }
+          if (flagged) {
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const int at = p0 + 32 * kb + 8 * (e >> 2) + 4 * half + (e & 3);
+                const int id = g.page_table[int64_t(ch.slot) * g.max_pages + (min(at, ch.len - 1) >> g.page_shift)];
+                if (id <= 0 || id >= g.pages)
+#pragma unroll
+                  for (int n = 0; n < NQ; ++n) s[n][kb][e] = kNegInf;
+              }
           }
         }
-        float top = s[0][0];
+        float mr[NQ];
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
+        for (int n = 0; n < NQ; ++n) {
+          float top = s[n][0][0];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) top = fmaxf(top, s[kb][e]);
-        top = halves_max(top);
-        top = top == kNegInf ? kNegInf : top * p.c;
-        if (__any(top > m + kGrowth)) {
-          const float to = fmaxf(m, top), f = fexp2(m - ref(to));
-          l *= f;
+          for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) top = fmaxf(top, s[n][kb][e]);
+          top = halves_max(top) * p.c;
+          if (__any(top > m[n] + kGrowth)) {
+            const float to = fmaxf(m[n], top), f = fexp2(m[n] - ref(to));
+            l[n] *= f;
+#pragma unroll
+            for (int b = 0; b < DB; ++b)
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[n][b][e] *= f;
+            m[n] = to;
+          }
+          mr[n] = ref(m[n]);
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              s[n][kb][e] = fexp2(fmaf(s[n][kb][e], p.c, -mr[n]));
+              sum[e & 3] += s[n][kb][e];
+            }
+          l[n] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        }
+#pragma unroll
+          for (int ks = 0; ks < 2 * KB; ++ks) {
+            bf16x8 pf[NQ];
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+              u32x4 w;
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                w[i] = cvt_pk_bf16(s[n][ks >> 1][8 * (ks & 1) + 2 * i], s[n][ks >> 1][8 * (ks & 1) + 2 * i + 1]);
+              pf[n] = __builtin_bit_cast(bf16x8, w);
+            }
+#pragma unroll
+            for (int b = 0; b < DB; ++b) {
+              constexpr int all_v = 2 * KB * DB;
+              const int i = ks * DB + b;
+              __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+              for (int n = 0; n < NQ; ++n) o[n][b] = mfma32(ring[i % kAhead], pf[n], o[n][b]);
+              if (i + kAhead < all_v) ring[i % kAhead] = vread(i + kAhead);
+            }
+          }
+      }
+      finish(t);
+    }
+    skip(w1, t1);
+  };
+  // ---- results ----
+  // (arguments and rows are read and worked out anew: they would take registers over the walk)
+  auto store = [&](int kind) {
+    const char __attribute__((address_space(4))) *args =
+        (const char __attribute__((address_space(4))) *)__builtin_amdgcn_kernarg_segment_ptr();
+    int first = row0 + c;
+    asm volatile("" : "+s"(args), "+v"(first));
+    static_assert(sizeof(KvGeom) % alignof(ChunkDev) == 0 && alignof(ChunkDev) == 8, "kernel arguments");
+    const auto &p = *(const ChunkDev __attribute__((address_space(4))) *)(args + sizeof(KvGeom));
+#pragma unroll
+    for (int n = 0; n < NQ; ++n) {
+      const float ln = halves_sum(l[n]);
+      const int row = first + 32 * n, mine = row - ch.rows0;  // row of the request, of the tile
+      if (row < all) {
+        if (p.parts > 1) {
+          const int64_t at = (((int64_t(tile) * g.kv_heads + h) * p.parts + part) * ROWS) + mine;
+          if (half == 0 && kind <= kFinite) {
+            p.ml[2 * at] = ln == 0.f ? kNegInf : m[n];
+            p.ml[2 * at + 1] = ln;
+          }
+          float *to = p.o + at * D + 4 * half;
+          if (ln != 0.f)
+#pragma unroll
+            for (int b = 0; b < DB; ++b)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                f32x4 v = {o[n][b][4 * i], o[n][b][4 * i + 1], o[n][b][4 * i + 2], o[n][b][4 * i + 3]};
+                if (kind > kFinite) {
+                  const f32x4 old = ld4(to + 32 * b + 8 * i);
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) v[e] = v[e] > 0.f ? beyond(old[e], kind) : old[e];
+                }
+                st4(to + 32 * b + 8 * i, v);
+              }
+          continue;
+        }
+        const int token = row / p.group;
+        const int64_t orow = int64_t(ch.bos + token) * p.a.q_heads + h * p.group + (row - token * p.group);
+        if (p.lse && half == 0 && kind <= kFinite)
+          p.lse[orow] = ln == 0.f ? kNegInf : (m[n] + __builtin_amdgcn_logf(ln)) * kLn2;
+        const float f = ln == 0.f ? 0.f : g.v_scale / ln;
+        uint16_t *to = p.a.out + orow * D + 8 * half;
+#pragma unroll
+        for (int b = 0; b < DB; ++b)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            // columns 16 i + 8 h + 0..3 and + 4..7 of the block: the halves swap what the other stores
+            u32x4 w;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t x = cvt_pk_bf16(o[n][b][8 * i + 2 * e] * f, o[n][b][8 * i + 2 * e + 1] * f);
+              const uint32_t y = cvt_pk_bf16(o[n][b][8 * i + 4 + 2 * e] * f, o[n][b][8 * i + 5 + 2 * e] * f);
+              const auto r = __builtin_amdgcn_permlane32_swap(x, y, false, false);
+              w[e] = r[0];
+              w[2 + e] = r[1];
+            }
+            u32x4 *at = reinterpret_cast<u32x4 *>(to + 32 * b + 16 * i);
+            if (kind > kFinite) {
+              const u32x4 old = *at;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float lo = __uint_as_float(w[e] << 16), hi = __uint_as_float(w[e] & 0xffff0000u);
+                const float a = __uint_as_float(old[e] << 16), b = __uint_as_float(old[e] & 0xffff0000u);
+                w[e] = pack_bf16x2(lo > 0.f ? beyond(a, kind) : a, hi > 0.f ? beyond(b, kind) : b);
+              }
+            }
+            *at = w;
+          }
+      }
+    }
+  };
+
+#pragma unroll 1
+  for (int kind = kAsIs;;) {
+    walk(kind);
+    if (kind == kAsIs) {
+      // a NaN may come from a value that the row does not see (0 * NaN)
+      float bad = 0.f;
+      if (wlive) {
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
 #pragma unroll
           for (int b = 0; b < DB; ++b)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[b][e] *= f;
-          m = to;
-        }
-        const float mr = ref(m);
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float w = fexp2(fmaf(s[kb][e], p.c, -mr));
-            if (partial && !(see[kb] >> e & 1)) w = 0.f;
-            s[kb][e] = w;
-            sum[e & 3] += w;
-          }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        if (!(careful && partial)) {
-#pragma unroll
-          for (int ks = 0; ks < 2 * KB; ++ks) {
-            u32x4 w;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              w[i] = cvt_pk_bf16(s[ks >> 1][8 * (ks & 1) + 2 * i], s[ks >> 1][8 * (ks & 1) + 2 * i + 1]);
-            const bf16x8 pf = __builtin_bit_cast(bf16x8, w);
-#pragma unroll
-            for (int b = 0; b < DB; ++b) {
-              s16x4t v[2];
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int r = 16 * ks + 8 * e + 4 * half + vrow;
-                const int piece = (4 * b | vpair) ^ twist<D>(r);
-                v[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4t *)(
-                    const_cast<char *>(vt) + r * T::RB + (piece << 4) + 8 * (lane & 1)));
-              }
-              const bf16x8 a =
-                  __builtin_bit_cast(bf16x8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
-              o[b] = mfma32(a, pf, o[b]);
-            }
-          }
-        } else {
-          // values that some rows do not see may be NaN or infinite: each place for itself, by
-          // the rows that see it
-          float *w = reinterpret_cast<float *>(scratch);
-#pragma unroll
-          for (int ks = 0; ks < 2 * KB; ++ks) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              w[(8 * (e >> 2) + 4 * half + (e & 3)) * 32 + c] = s[ks >> 1][8 * (ks & 1) + e];
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup", "local");
-            __builtin_amdgcn_wave_barrier();
-#pragma unroll 1
-            for (int i = 0; i < 16; ++i) {
-              const float wi = w[i * 32 + c];
-              const int r = 16 * ks + i;
-              if (wi != 0.f) {
-#pragma unroll
-                for (int b = 0; b < DB; ++b)
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) {
-                    const u32x2 x = *reinterpret_cast<const u32x2 *>(
-                        vt + r * T::RB + (((4 * b + e) ^ twist<D>(r)) << 4) + 8 * half);
-#pragma unroll
-                    for (int f = 0; f < 4; ++f) {
-                      const uint32_t y = x[f >> 1];
-                      o[b][4 * e + f] =
-                          fmaf(wi, __uint_as_float((f & 1) ? (y & 0xffff0000u) : (y << 16)), o[b][4 * e + f]);
-                    }
-                  }
-              }
-            }
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup", "local");
-            __builtin_amdgcn_wave_barrier();
-          }
-        }
+            for (int e = 0; e < 16; ++e) bad = fmaf(o[n][b][e], 0.f, bad);
       }
-      if (kF8 && more) {
-        char *to = lds + ((t + 1) & 1) * 2 * T::kBytes;
-        put(kraw, to, false);
-        put(vraw, to + T::kBytes, clear);
+      if (__syncthreads_or(bad != 0.f)) {
+        kind = kFinite;
+        continue;
       }
     }
-    if (careful) break;
-    // a NaN may come from a value that the row does not see: walk again, carefully
-    float bad = 0.f;
-    if (wlive) {
-#pragma unroll
-      for (int b = 0; b < DB; ++b)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) bad = fmaf(o[b][e], 0.f, bad);
-    }
-    if (!__syncthreads_or(bad != 0.f)) break;
-    careful = true;
+    store(kind);
+    if (kind == kAsIs || kind == kDown) break;
+    ++kind;
   }
-
-  // ---- results ----
-  l = halves_sum(l);
-  if (row0 + c >= all) return;
-  if (p.parts > 1) {
-    const int64_t at = (((int64_t(tile) * g.kv_heads + h) * p.parts + part) * kRows) + 32 * wave + c;
-    if (half == 0) {
-      p.ml[2 * at] = l == 0.f ? kNegInf : m;
-      p.ml[2 * at + 1] = l;
-    }
-    if (l == 0.f) return;
-    float *to = p.o + at * D + 4 * half;
-#pragma unroll
-    for (int b = 0; b < DB; ++b)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        st4(to + 32 * b + 8 * i, f32x4{o[b][4 * i], o[b][4 * i + 1], o[b][4 * i + 2], o[b][4 * i + 3]});
-    return;
-  }
-  const int64_t orow = int64_t(ch.bos + token) * p.a.q_heads + head;
-  if (p.lse && half == 0) p.lse[orow] = l == 0.f ? kNegInf : (m + __builtin_amdgcn_logf(l)) * kLn2;
-  const float f = l == 0.f ? 0.f : g.v_scale / l;
-  uint16_t *to = p.a.out + orow * D + 8 * half;
-#pragma unroll
-  for (int b = 0; b < DB; ++b)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      // columns 16 i + 8 h + 0..3 and + 4..7 of the block: the halves swap what the other stores
-      uint32_t w[4];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const uint32_t x = cvt_pk_bf16(o[b][8 * i + 2 * e] * f, o[b][8 * i + 2 * e + 1] * f);
-        const uint32_t y = cvt_pk_bf16(o[b][8 * i + 4 + 2 * e] * f, o[b][8 * i + 5 + 2 * e] * f);
-        const auto r = __builtin_amdgcn_permlane32_swap(x, y, false, false);
-        w[e] = r[0];
-        w[2 + e] = r[1];
-      }
-      *reinterpret_cast<u32x4 *>(to + 32 * b + 16 * i) = u32x4{w[0], w[1], w[2], w[3]};
-    }
 }
 
 // Rows whose places were divided: the parts' O, m and l joined.  One workgroup per tile and
@@ -520,17 +631,17 @@ __global__ __launch_bounds__(kThreads) void attn_prefill_join_kernel(KvGeom g, C
   const Chunk ch = chunk_of(g, p, tile, false);
   if (!ch.any) return;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const int rows = min(kRows, ch.n * p.group - ch.rows0);
+  const int rows = min(p.rows, ch.n * p.group - ch.rows0);
   constexpr int N = D / 64;  // columns of a lane
   for (int i = wave; i < rows; i += kWaves) {
-    const int64_t at = (int64_t(tile) * g.kv_heads + h) * p.parts * kRows + i;
+    const int64_t at = (int64_t(tile) * g.kv_heads + h) * p.parts * p.rows + i;
     float m = kNegInf;
-    for (int part = 0; part < p.parts; ++part) m = fmaxf(m, p.ml[2 * (at + int64_t(part) * kRows)]);
+    for (int part = 0; part < p.parts; ++part) m = fmaxf(m, p.ml[2 * (at + int64_t(part) * p.rows)]);
     float l = 0.f, o[N];
 #pragma unroll
     for (int e = 0; e < N; ++e) o[e] = 0.f;
     for (int part = 0; part < p.parts; ++part) {
-      const int64_t r = at + int64_t(part) * kRows;
+      const int64_t r = at + int64_t(part) * p.rows;
       const float pm = p.ml[2 * r], pl = p.ml[2 * r + 1];
       if (pl == 0.f) continue;
       const float f = fexp2(pm - m);
@@ -634,7 +745,7 @@ void attn_prefill_mass_kernel(KvGeom g, ChunkDev p, int blocks) {
     for (int st = 0; st < KS; ++st) {
       u32x4 w = *reinterpret_cast<const u32x4 *>(src + 16 * st);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] ^= p.flip;
+      for (int i = 0; i < 4; ++i) w[i] = (w[i] ^ p.flip) & p.keep;
       const bf16x8 q = __builtin_bit_cast(bf16x8, w);
 #pragma unroll
       for (int kb = 0; kb < KB; ++kb) s[kb] = mfma32(k[kb][st], q, s[kb]);
@@ -666,7 +777,8 @@ void attn_prefill_mass_kernel(KvGeom g, ChunkDev p, int blocks) {
 
 size_t pad256(size_t n) { return (n + 255) & ~size_t(255); }
 
-int64_t chunk_tiles(int batch, int tokens, int group) { return int64_t(tokens) * group / kRows + batch; }
+int64_t chunk_tiles(int batch, int tokens, int group, int rows) { return int64_t(tokens) * group / rows + batch; }
+int chunk_rows() { return kRows * GDN_NQ; }
 
 // Parts that a tile's places are divided into: workgroups for two on every compute unit, of 512
 // places or more each (by the bound max_len).
@@ -682,10 +794,10 @@ struct ChunkSpace {
 };
 ChunkSpace chunk_space(const gdn_kv_pool *p, int batch, int tokens, int q_heads, int max_len, int mass_tokens) {
   ChunkSpace r{};
-  const int64_t tiles = chunk_tiles(batch, tokens, q_heads / p->d.kv_heads);
+  const int64_t tiles = chunk_tiles(batch, tokens, q_heads / p->d.kv_heads, chunk_rows());
   const int parts = chunk_parts(p, tiles, max_len);
   if (parts > 1) {
-    const size_t rows = size_t(tiles) * p->d.kv_heads * parts * kRows;
+    const size_t rows = size_t(tiles) * p->d.kv_heads * parts * chunk_rows();
     r.o = pad256(rows * p->d.head_dim * 4);
     r.ml = pad256(rows * 8);
   }
@@ -697,7 +809,7 @@ template <int D, bool kF8>
 hipError_t launch_dt(const KvGeom &g, const ChunkDev &p, hipStream_t s) {
   const bool wide = (1 << g.page_shift) >= 16;
   const int64_t units = int64_t(p.tiles) * g.kv_heads;
-  const auto kernel = wide ? attn_prefill_kernel<D, kF8, true> : attn_prefill_kernel<D, kF8, false>;
+  const auto kernel = wide ? attn_prefill_kernel<D, kF8, true, GDN_NQ> : attn_prefill_kernel<D, kF8, false, GDN_NQ>;
   constexpr int shared = Tile<D, kF8>::kShared;
   hipLaunchKernelGGL(kernel, flat_grid(units * p.parts), dim3(kThreads), shared, s, g, p);
   hipError_t e = hipGetLastError();
@@ -726,7 +838,7 @@ bool chunk_fits(const gdn_kv_pool *p, int batch, int tokens, int q_heads, int ma
   const int64_t group = q_heads / p->d.kv_heads, limit = int64_t(1) << 31;
   const int64_t blocks = int64_t(max_len) / MassTile<256>::kPlaces + 1;
   // rows of a request and tiles are counted in 31 bits, workgroups in 40
-  return int64_t(tokens) * group < limit - kRows && chunk_tiles(batch, tokens, int(group)) < limit / p->d.kv_heads &&
+  return int64_t(tokens) * group < limit - kRows && chunk_tiles(batch, tokens, int(group), kRows) < limit / p->d.kv_heads &&
          int64_t(batch) * p->d.kv_heads < (int64_t(1) << 40) / blocks;
 }
 
@@ -740,10 +852,13 @@ hipError_t launch_attn_prefill(const gdn_kv_pool *pool, int layer, const ChunkAr
   ChunkDev p{};
   p.a = a;
   p.group = a.q_heads / pool->d.kv_heads;
-  p.tiles = int(chunk_tiles(a.batch, a.tokens, p.group));
+  p.rows = chunk_rows();
+  p.tiles = int(chunk_tiles(a.batch, a.tokens, p.group, p.rows));
   p.parts = chunk_parts(pool, p.tiles, a.max_len);
   p.c = fabsf(a.scale) * pool->d.k_scale * kLog2e;
   p.flip = std::signbit(a.scale) ? 0x80008000u : 0u;
+  p.keep = p.c == 0.f ? 0u : ~0u;  // (a score of -inf must stay -inf where it is multiplied by c)
+  p.c = p.c == 0.f ? 1.f : p.c;
   const ChunkSpace w = chunk_space(pool, a.batch, a.tokens, a.q_heads, a.max_len, a.mass_tokens);
   char *at = static_cast<char *>(a.workspace);
   p.o = reinterpret_cast<float *>(at);
