@@ -34,9 +34,6 @@
 namespace gdn {
 namespace {
 
-#ifndef GDN_NQ
-#define GDN_NQ 1
-#endif
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
 constexpr int kCUs = 256;
@@ -45,21 +42,27 @@ constexpr float kLn2 = 0.693147180559945309417f;
 constexpr float kNegInf = -__builtin_inff();
 constexpr float kGrowth = 8.f;  // log2 of how far the maximum may pass the reference
 
-constexpr int kRows = 32 * kWaves;  // rows of a workgroup, for each block of its waves
+constexpr int kRows = 32 * kWaves;  // rows of a tile
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4t __attribute__((ext_vector_type(4)));
 // (constant address space: these arrays do not change during the call, so wave-uniform reads
 // are scalar loads)
-typedef const int32_t __attribute__((address_space(4))) *table_t;
+#ifdef __HIP_DEVICE_COMPILE__
+#define GDN_CONSTANT __attribute__((address_space(4)))
+#else
+#define GDN_CONSTANT
+#endif
+typedef const int32_t GDN_CONSTANT *table_t;
 
 struct ChunkDev {
   ChunkArgs a;
-  int group, tiles, parts;
+  int group, tiles;
+  int parts, piece; // a tile's blocks are divided into pieces of this many; at most `parts`
   float c;          // |scale * k_scale| in log2 units
   uint32_t flip, keep;  // for two bf16 queries: the scale's sign, and 0 if it is 0 (c is 1 then)
-  int rows;         // of a tile
-  float *o, *ml;    // parts > 1: [tile][kv head][part][rows] rows of O, and of m and l
+  uint32_t inverse;     // ceil(2^32 / group), for a group of 2 or more
+  float *o, *ml;    // parts > 1: [part][token][q_heads] rows of O, and m and l
   float *lse;       // [tokens][q_heads], or NULL
 };
 
@@ -99,38 +102,54 @@ __device__ __forceinline__ u32x4 sorted(u32x4 x, int kind) {
   }
   return x;
 }
+// the same for four e4m3 values: what is NaN becomes 0 or 1, other values themselves or 0
+__device__ __forceinline__ uint32_t sorted_f8(uint32_t x, int kind) {
+  uint32_t r = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t v = (x >> (8 * e)) & 0xffu;
+    const bool nan = (v & 0x7fu) == 0x7fu;
+    r |= (kind == kFinite ? (nan ? 0u : v) : nan ? 0x38u : 0u) << (8 * e);
+  }
+  return r;
+}
 // a sum with an infinite (or NaN) value added
 __device__ __forceinline__ float beyond(float sum, int kind) { return sum + (kind == kUp ? -kNegInf : kNegInf); }
 
 // ---- which rows a tile has -------------------------------------------------
-// The tiles of request b begin at cu[b] * group / rows + b: at least as many as it needs, and
+// The tiles of request b begin at cu[b] * group / kRows + b: at least as many as it needs, and
 // found from cu alone, so that no list of tiles has to be made first.
 struct Chunk {
   int b, bos, n, rows0;  // request, its first token and number of tokens, the tile's first row
   int slot, len, begin;
   bool any, live;        // whether the tile has rows, whether they see anything at all
 };
-__device__ __forceinline__ Chunk chunk_of(const KvGeom &g, const ChunkDev &p, int tile, bool tell) {
-  const table_t cu = (table_t)p.a.cu_seqlens;
-  auto first = [&](int b) { return int64_t(cu[b]) * p.group / p.rows + b; };
+__device__ __forceinline__ int64_t first_tile(const ChunkDev &p, int b) {
+  return int64_t(((table_t)p.a.cu_seqlens)[b]) * p.group / kRows + b;
+}
+__device__ __forceinline__ int request_of(const ChunkDev &p, int tile) {
   int lo = 0, hi = p.a.batch;  // the last request whose tiles begin at `tile` or before
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (first(mid) <= tile) lo = mid;
+    if (first_tile(p, mid) <= tile) lo = mid;
     else hi = mid;
   }
+  return lo;
+}
+__device__ __forceinline__ Chunk chunk_of(const KvGeom &g, const ChunkDev &p, int tile, int b, bool tell) {
+  const table_t cu = (table_t)p.a.cu_seqlens;
   Chunk r;
-  r.b = lo;
-  r.bos = cu[lo];
-  const int eos = cu[lo + 1];
-  const int64_t at = (tile - first(lo)) * p.rows;
+  r.b = b;
+  r.bos = cu[b];
+  const int eos = cu[b + 1];
+  const int64_t at = (tile - first_tile(p, b)) * kRows;
   const bool ok = r.bos >= 0 && eos >= r.bos && eos <= p.a.tokens;
   r.n = ok ? eos - r.bos : 0;
   r.any = ok && at >= 0 && at < int64_t(r.n) * p.group;
   r.rows0 = r.any ? int(at) : 0;
-  r.slot = ((table_t)p.a.slot_table)[lo];
-  r.len = ((table_t)p.a.kv_len)[lo];
-  r.begin = p.a.kv_begin ? ((table_t)p.a.kv_begin)[lo] : 0;
+  r.slot = ((table_t)p.a.slot_table)[b];
+  r.len = ((table_t)p.a.kv_len)[b];
+  r.begin = p.a.kv_begin ? ((table_t)p.a.kv_begin)[b] : 0;
   const bool lens = r.len >= r.n && r.len <= p.a.max_len && r.begin >= 0;
   r.live = r.any && r.slot > 0 && r.slot < g.slots && lens;
   if (tell) {
@@ -140,9 +159,27 @@ __device__ __forceinline__ Chunk chunk_of(const KvGeom &g, const ChunkDev &p, in
   }
   return r;
 }
+// a row's token: row / group (the product with the inverse is right or one too many below 2^31)
+__device__ __forceinline__ int token_of(const ChunkDev &p, int row) {
+  const int t = int(__umulhi(uint32_t(row), p.inverse));
+  return p.group == 1 ? row : t - (t * p.group > row ? 1 : 0);
+}
 // first place that the query at `place` sees
 __device__ __forceinline__ int seen_from(const ChunkDev &p, int begin, int place) {
   return p.a.window ? max(begin, place - p.a.window + 1) : begin;
+}
+
+// The blocks of KT places that a tile's rows see: lo and how many.
+struct Span {
+  int lo, n;
+};
+template <int KT>
+__device__ __forceinline__ Span span_of(const ChunkDev &p, const Chunk &ch) {
+  if (!ch.live) return Span{0, 0};
+  const int all = ch.n * p.group, place0 = ch.len - ch.n;
+  const int first = place0 + token_of(p, ch.rows0), last = place0 + token_of(p, min(ch.rows0 + kRows - 1, all - 1));
+  const int lo = seen_from(p, ch.begin, first) / KT;
+  return Span{lo, max(0, last / KT + 1 - lo)};
 }
 
 // ---- shared memory ---------------------------------------------------------
@@ -166,147 +203,160 @@ struct Tile {
   static constexpr int kShared = 4 * kBytes + 16;
 };
 
-// kWide: pages hold 16 tokens or more, so that the rows of a wave's load lie in one page.
-// NQ: blocks of 32 rows of a wave.
-template <int D, bool kF8, bool kWide, int NQ>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(NQ == 1 ? 2 : 1)))
-void attn_prefill_kernel(KvGeom g, ChunkDev p) {
-  using T = Tile<D, kF8>;
-  constexpr int KT = T::KT, KB = KT / 32, KS = D / 16, DB = D / 32, NL = T::kLoads, ROWS = kRows * NQ;
-  extern __shared__ __attribute__((aligned(16))) char lds[];
-  // a tile (by its number's parity) that has a page outside the pool
-  int *const sbad = reinterpret_cast<int *>(lds + 4 * T::kBytes);
+// The kernel's arguments as they lie in memory: what a part of the kernel needs is read there, not
+// held in registers through the others.
+struct ChunkArgsAll {
+  KvGeom g;
+  ChunkDev p;
+};
+typedef const ChunkArgsAll GDN_CONSTANT *args_t;
+__device__ __forceinline__ args_t fresh(args_t a) {
+  asm volatile("" : "+s"(a));
+  return a;
+}
 
+// kWide: pages hold 16 tokens or more, so that the rows of a wave's load lie in one page.
+//
+// A workgroup has one piece of one tile's blocks, for one key-value head.  The first pieces come
+// first, and of them those of a request's last tiles, which see the most places: workgroups that
+// run at the same time read the same keys, and the last ones to start are short.
+template <int D, bool kF8, bool kWide>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2)))
+void attn_prefill_kernel(ChunkArgsAll) {
+  using T = Tile<D, kF8>;
+  constexpr int KT = T::KT, KB = KT / 32, KS = D / 16, DB = D / 32, NL = T::kLoads;
+  constexpr int kAhead = kF8 && D == 256 ? 3 : 4;  // fragments asked for before they are used
+  extern __shared__ __attribute__((aligned(16))) char lds[];
+  const args_t args = (args_t)__builtin_amdgcn_kernarg_segment_ptr();
+  // a block (by its number's parity) that has a page outside the pool
+  int *const sbad = reinterpret_cast<int *>(lds + 4 * T::kBytes);
   const int lane = threadIdx.x & 63, c = lane & 31, half = lane >> 5;
   const int wave = uniform(threadIdx.x >> 6);
-  const int64_t item = flat_block();
-  const int h = int(item % g.kv_heads);
-  const int64_t rest = item / g.kv_heads;
-  const int part = int(rest % p.parts);
-  const int tile = p.tiles - 1 - int(rest / p.parts);  // the last tiles see the most places
-  if (tile < 0) return;
-  const Chunk ch = chunk_of(g, p, tile, h == 0 && part == 0 && threadIdx.x == 0);
-  if (!ch.any) return;
 
-  const int G = p.group, all = ch.n * G;
-  const int row0 = ch.rows0 + 32 * NQ * wave;
+  const KvGeom g = args->g;
+  const ChunkDev p = args->p;
+  const int64_t item = flat_block();
+  const int h = uniform(int(item % g.kv_heads));
+  const int64_t rest = item / g.kv_heads;
+  const int part = uniform(int(rest / p.tiles)), tile = p.tiles - 1 - uniform(int(rest % p.tiles));
+  if (part >= p.parts) return;
+  const Chunk ch = chunk_of(g, p, tile, request_of(p, tile), h == 0 && part == 0 && threadIdx.x == 0);
+  if (!ch.any) return;
+  const Span span = span_of<KT>(p, ch);
+  if (part > 0 && part * p.piece >= span.n) return;
+  const bool whole = span.n <= p.piece;
+  const int t0 = span.lo + part * p.piece, t1 = min(span.lo + span.n, t0 + p.piece);
+
+  const int all = ch.n * p.group;
+  const int row0 = ch.rows0 + 32 * wave;
   const bool wlive = ch.live && row0 < all;
   const int place0 = ch.len - ch.n;  // of the first new token
-  int place[NQ], from[NQ];
-#pragma unroll
-  for (int n = 0; n < NQ; ++n) {
-    // (rows behind the last repeat it and are not stored)
-    place[n] = place0 + min(row0 + 32 * n + c, all - 1) / G;
-    from[n] = seen_from(p, ch.begin, place[n]);
-  }
-  const int wfirst = place0 + min(row0, all - 1) / G, wlast = place0 + min(row0 + 32 * NQ - 1, all - 1) / G;
+  const int row = min(row0 + c, all - 1);  // (rows behind the last repeat it and are not stored)
+  const int token = token_of(p, row), place = place0 + token;
+  const int wfirst = place0 + token_of(p, min(row0, all - 1)), wlast = place0 + token_of(p, min(row0 + 31, all - 1));
   const int wfrom = seen_from(p, ch.begin, wfirst), wfrom_last = seen_from(p, ch.begin, wlast);
 
-  // tiles of the workgroup: what its rows see, and this part of it
-  int t0 = 0, t1 = 0;
-  if (ch.live) {
-    const int gfirst = place0 + ch.rows0 / G, glast = place0 + min(ch.rows0 + ROWS - 1, all - 1) / G;
-    const int lo = seen_from(p, ch.begin, gfirst) / KT, hi = glast / KT + 1;
-    const int per = (max(hi - lo, 0) + p.parts - 1) / p.parts;
-    t0 = lo + part * per;
-    t1 = min(hi, t0 + per);
-  }
-
-  bf16x8 q[NQ][KS];
+  bf16x8 q[KS];
   if (wlive && t0 < t1) {
+    const int head = h * p.group + (row - token * p.group);
+    const uint16_t *src = p.a.q + (ch.bos + token) * p.a.q_stride + int64_t(head) * D + 8 * half;
 #pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-      const int row = min(row0 + 32 * n + c, all - 1), token = row / G, head = h * G + (row - token * G);
-      const uint16_t *src = p.a.q + (ch.bos + token) * p.a.q_stride + int64_t(head) * D + 8 * half;
+    for (int s = 0; s < KS; ++s) {
+      u32x4 w = *reinterpret_cast<const u32x4 *>(src + 16 * s);
 #pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        u32x4 w = *reinterpret_cast<const u32x4 *>(src + 16 * s);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = (w[i] ^ p.flip) & p.keep;
-        q[n][s] = __builtin_bit_cast(bf16x8, w);
-      }
+      for (int i = 0; i < 4; ++i) w[i] = (w[i] ^ p.flip) & p.keep;
+      q[s] = __builtin_bit_cast(bf16x8, w);
     }
   }
 
   // ---- loads ----
-  const int lrow = lane / T::kLanes, lpiece = lane % T::kLanes;
   auto load_row = [&](int j) { return (j * kWaves + wave) * T::kLoadRows; };  // first row of load j
   const table_t table = (table_t)(g.page_table + int64_t(max(ch.slot, 0)) * g.max_pages);
   const int page_mask = (1 << g.page_shift) - 1;
-  const int loff = (kWide ? lrow * T::RB : 0) + ((lpiece ^ twist<D>(wave * T::kLoadRows + lrow)) << 4);
+  // a lane's place in a load: its row, and the piece of the row that belongs there
+  auto lane_row = [&]() { return int(threadIdx.x & 63) / T::kLanes; };
+  const int lpiece = lane % T::kLanes;
+  const int loff = (kWide ? lane_row() * T::SB : 0) + ((kF8 ? lpiece : lpiece ^ twist<D>(wave * T::kLoadRows + lane_row())) << 4);
   int ids[kWide ? NL : 1];
   auto load_ids = [&](int t) {
     if constexpr (kWide) {
 #pragma unroll
-      for (int j = 0; j < NL; ++j) ids[j] = table[min(t * KT + load_row(j), ch.len - 1) >> g.page_shift];
+      for (int j = 0; j < NL; ++j) ids[j] = table[uint32_t(min(t * KT + load_row(j), ch.len - 1)) >> g.page_shift];
     }
   };
-  uint32_t hidden;       // loads (bits j) of the tile to come whose lane's row is no place of the request
-  bool clear;            // whether any of the wave has one
-  int64_t src[NL];       // byte offsets of the tile to come in the layer's keys and values
-  auto locate = [&](int t) {
-    hidden = 0;
+  bool edge;  // whether the block to come has rows that are no places of the request
+  uint32_t src[NL];  // its rows in the layer's keys and values
+  auto locate = [&](int t, int j) {
+    const int at = t * KT + load_row(j) + (kWide ? 0 : lane_row());
+    int id;
+    if constexpr (kWide) id = ids[j];
+    else id = g.page_table[int64_t(ch.slot) * g.max_pages + (min(at, ch.len - 1) >> g.page_shift)];
+    const bool wrong = id <= 0 || id >= g.pages;
+    id = wrong ? 0 : id;
+    src[j] = uint32_t(((id * g.kv_heads + h) << g.page_shift) + (at & page_mask));
+    return wrong;
+  };
+  auto locate_all = [&](int t) {
     bool bad = false;
 #pragma unroll
-    for (int j = 0; j < NL; ++j) {
-      const int first = t * KT + load_row(j), at = first + lrow;
-      int id;
-      if constexpr (kWide) id = ids[j];
-      else id = g.page_table[int64_t(ch.slot) * g.max_pages + (min(at, ch.len - 1) >> g.page_shift)];
-      const bool wrong = id <= 0 || id >= g.pages;
-      id = wrong ? 0 : id;
-      bad = bad || wrong;
-      hidden |= (wrong || at >= ch.len || at < ch.begin) ? 1u << j : 0u;
-      if constexpr (kWide)
-        src[j] = (int64_t((id * g.kv_heads + h) << g.page_shift) + (first & page_mask)) * T::SB;
-      else
-        src[j] = (int64_t((id * g.kv_heads + h) << g.page_shift) + (at & page_mask)) * T::SB;
-    }
-    if (__any(bad)) {
-      if (lane == 0) {
+    for (int j = 0; j < NL; ++j) bad |= locate(t, j);
+    return bad;
+  };
+  // the block's rows have all been located; bad: one of the lane's is in no page
+  auto located = [&](int t, bool bad) {
+    if (kWide ? bad : __any(bad)) {
+      bad = true;
+      if ((threadIdx.x & 63) == 0) {
         sbad[t & 1] = t;
         set_err(g.err, GDN_ERRW_BAD_PAGE);
       }
+    } else {
+      bad = false;
     }
-    clear = __any(hidden != 0);
+    edge = bad || t * KT < ch.begin || (t + 1) * KT > ch.len;
+  };
+  // whether the lane's row of load j of block t is no place of the request (the rare blocks)
+  auto hidden = [&](int t, int j) {
+    const int at = t * KT + load_row(j) + lane_row();
+    const int id = g.page_table[int64_t(ch.slot) * g.max_pages + (min(at, ch.len - 1) >> g.page_shift)];
+    return id <= 0 || id >= g.pages || at >= ch.len || at < ch.begin;
   };
   // bf16: from memory to shared memory; a lane's 16 bytes land at its place in the wave's 1 KB,
   // so it asks for the piece that belongs there
-  auto ask = [&](int t) {
+  auto ask = [&](int t, int j, bool values) {
     if constexpr (!kF8) {
-      char *to = lds + (t & 1) * 2 * T::kBytes;
-#pragma unroll
-      for (int j = 0; j < NL; ++j) {
-        // (the twist of the rows of load j differs from load 0's in one bit at most)
-        constexpr int kStep = kWaves * T::kLoadRows;
-        static_assert(kStep % 16 == 0 || kStep == 8, "twist");
-        const uint32_t off = uint32_t(loff) ^ (kStep == 8 ? (j & 1) * 32 : 0);
-        char *dst = to + load_row(j) * T::RB;
-        typedef __attribute__((address_space(1))) const void *gp;
-        typedef __attribute__((address_space(3))) void *lp;
-        __builtin_amdgcn_global_load_lds((gp)(g.k + src[j] + off), (lp)dst, 16, 0, 0);
-        __builtin_amdgcn_global_load_lds((gp)(g.v + src[j] + off), (lp)(dst + T::kBytes), 16, 0, 0);
+      // (the twist of the rows of load j differs from load 0's in one bit at most)
+      constexpr int kStep = kWaves * T::kLoadRows;
+      static_assert(kStep % 16 == 0 || kStep == 8, "twist");
+      const uint32_t off = uint32_t(loff) ^ (kStep == 8 ? (j & 1) * 32 : 0);
+      char *dst = lds + (t & 1) * 2 * T::kBytes + load_row(j) * T::RB + (values ? T::kBytes : 0);
+      const char *from = (values ? g.v : g.k) + uint64_t(src[j]) * T::SB;
+      typedef __attribute__((address_space(3))) void *lp;
+      if constexpr (kWide) {  // one page: a scalar base, and 32 bits of the lane's
+        const auto rows = __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(from), 0, 1024, 0x00027000);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rows, (lp)dst, 16, int(off), 0, 0, 0);
+      } else {
+        __builtin_amdgcn_global_load_lds((__attribute__((address_space(1))) const char *)from + off, (lp)dst, 16, 0, 0);
       }
     }
   };
-  // rows that are no places of the request hold anything: zeros keep 0 * NaN out of the product
-  auto clear_rows = [&](int t) {
-    if constexpr (!kF8) {
-      char *to = lds + (t & 1) * 2 * T::kBytes + T::kBytes;
+  auto ask_all = [&](int t) {
 #pragma unroll
-      for (int j = 0; j < NL; ++j)
-        if (hidden >> j & 1) *reinterpret_cast<u32x4 *>(to + load_row(j) * T::RB + lane * 16) = u32x4{0, 0, 0, 0};
+    for (int j = 0; j < NL; ++j) {
+      ask(t, j, false);
+      ask(t, j, true);
     }
   };
-  // the wave's values of the tile replaced as the walk asks for
-  auto sort_rows = [&](int t, int kind) {
-    if constexpr (!kF8) {
-      char *to = lds + (t & 1) * 2 * T::kBytes + T::kBytes;
-#pragma unroll
-      for (int j = 0; j < NL; ++j) {
-        u32x4 *at = reinterpret_cast<u32x4 *>(to + load_row(j) * T::RB + lane * 16);
-        *at = sorted(*at, kind);
-      }
+  // Rows that are no places of the request hold anything: zeros keep 0 * NaN out of the product.
+  // Other walks than the first replace values.
+  auto change_rows = [&](int t, int kind) {
+    char *to = lds + (t & 1) * 2 * T::kBytes + T::kBytes;
+#pragma unroll 1
+    for (int j = 0; j < NL; ++j) {
+      u32x4 *at = reinterpret_cast<u32x4 *>(to + load_row(j) * T::RB + int(threadIdx.x & 63) * 16);
+      u32x4 x = *at;
+      if (kind != kAsIs) x = sorted(x, kind);
+      *at = hidden(t, j) ? u32x4{0, 0, 0, 0} : x;
     }
   };
   // e4m3: through registers, 16 values a lane
@@ -314,28 +364,34 @@ void attn_prefill_kernel(KvGeom g, ChunkDev p) {
   auto fetch = [&](u32x4 *raw, const char *base) {
     if constexpr (kF8) {
 #pragma unroll
-      for (int j = 0; j < NL; ++j)
-        raw[j] = *reinterpret_cast<const u32x4 *>(base + src[j] + (kWide ? lrow * T::SB : 0) + 16 * lpiece);
+      for (int j = 0; j < NL; ++j) raw[j] = *reinterpret_cast<const u32x4 *>(base + uint64_t(src[j]) * T::SB + loff);
     }
   };
-  auto put = [&](const u32x4 *raw, char *to, bool zero, int kind) {
+  auto put = [&](const u32x4 *raw, char *to) {
     if constexpr (kF8) {
 #pragma unroll
       for (int j = 0; j < NL; ++j) {
-        const int r = load_row(j) + lrow;
-        u32x4 x = raw[j];
-        if (zero && (hidden >> j & 1)) x = u32x4{0, 0, 0, 0};
+        const int r = load_row(j) + lane_row();
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           u32x4 w;
           uint32_t a, b;
-          f8_to_bf16(x[2 * e], &a, &b);
+          f8_to_bf16(raw[j][2 * e], &a, &b);
           w[0] = a; w[1] = b;
-          f8_to_bf16(x[2 * e + 1], &a, &b);
+          f8_to_bf16(raw[j][2 * e + 1], &a, &b);
           w[2] = a; w[3] = b;
-          if (kind != kAsIs) w = sorted(w, kind);
           *reinterpret_cast<u32x4 *>(to + r * T::RB + (((2 * lpiece + e) ^ twist<D>(r)) << 4)) = w;
         }
+      }
+    }
+  };
+  auto change_raw = [&](int t, int kind) {  // what change_rows does, before the values are put
+    if constexpr (kF8) {
+#pragma unroll
+      for (int j = 0; j < NL; ++j) {
+        const bool no = hidden(t, j);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) vraw[j][i] = no ? 0u : kind == kAsIs ? vraw[j][i] : sorted_f8(vraw[j][i], kind);
       }
     }
   };
@@ -346,254 +402,238 @@ void attn_prefill_kernel(KvGeom g, ChunkDev p) {
   // block of 32 columns
   const int vrow = 4 * half + ((lane >> 2) & 3), vpair = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
   const int kaddr = c * T::RB + ((half ^ twist<D>(c)) << 4);
-  const int vaddr = vrow * T::RB + ((vpair ^ twist<D>(vrow)) << 4) + 8 * (lane & 1);
-  constexpr int kAhead = 4;
+  const int vaddr = vrow * T::RB + ((vpair ^ twist<D>(vrow)) << 4) + 8 * (lane & 1) + T::kBytes;
 
-  f32x16 o[NQ][DB];
-  float m[NQ], l[NQ];
+  f32x16 o[DB];
+  float m, l;
   auto walk = [&](int kind) {
 #pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-#pragma unroll
-      for (int b = 0; b < DB; ++b) o[n][b] = f32x16{};
-      m[n] = kNegInf;
-      l[n] = 0.f;
-    }
+    for (int b = 0; b < DB; ++b) o[b] = f32x16{};
+    m = kNegInf;
+    l = 0.f;
+    __syncthreads();  // (the last walk's blocks have been read)
     if (threadIdx.x < 2) sbad[threadIdx.x] = -1;
     __syncthreads();
     if (t0 >= t1) return;
-    load_ids(t0);
-    locate(t0);
-    ask(t0);
-    if constexpr (kF8) {
-      char *to = lds + (t0 & 1) * 2 * T::kBytes;
-      fetch(kraw, g.k);
-      fetch(vraw, g.v);
-      put(kraw, to, false, kAsIs);
-      put(vraw, to + T::kBytes, clear, kind);
-    }
-    load_ids(t0 + 1);
-    // tile t is there, and the next one on its way
-    auto stage = [&](int t) {
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      if (!kF8 && clear) clear_rows(t);
-      if (!kF8 && kind != kAsIs) sort_rows(t, kind);
-      __syncthreads();
-      const bool more = t + 1 < t1;
-      if (more) {
-        locate(t + 1);
-        ask(t + 1);
-        if constexpr (kF8) {
-          fetch(kraw, g.k);
-          fetch(vraw, g.v);
-        }
-        load_ids(t + 2);
+    auto convert = [&](int t) {
+      if constexpr (kF8) {
+        char *to = lds + (t & 1) * 2 * T::kBytes;
+        put(kraw, to);
+        if (edge || kind != kAsIs) change_raw(t, kind);
+        put(vraw, to + T::kBytes);
       }
     };
-    auto finish = [&](int t) {
-      if (kF8 && t + 1 < t1) {
-        char *to = lds + ((t + 1) & 1) * 2 * T::kBytes;
-        put(kraw, to, false, kAsIs);
-        put(vraw, to + T::kBytes, clear, kind);
-      }
+    load_ids(t0);
+    located(t0, locate_all(t0));
+    ask_all(t0);
+    fetch(kraw, g.k);
+    fetch(vraw, g.v);
+    convert(t0);
+    load_ids(t0 + 1);
+    // block t is there
+    auto arrive = [&](int t) {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      if (!kF8 && (edge || kind != kAsIs)) [[unlikely]] change_rows(t, kind);
+      __syncthreads();
     };
     auto skip = [&](int a, int b) {
 #pragma unroll 1
       for (int t = a; t < b; ++t) {
-        stage(t);
-        finish(t);
+        arrive(t);
+        if (t + 1 < t1) {
+          located(t + 1, locate_all(t + 1));
+          ask_all(t + 1);
+          fetch(kraw, g.k);
+          fetch(vraw, g.v);
+          load_ids(t + 2);
+          convert(t + 1);
+        }
       }
     };
-    // the tiles that the wave's rows see
+    // the blocks that the wave's rows see
     const int w0 = wlive ? min(t1, max(t0, wfrom / KT)) : t1, w1 = wlive ? max(w0, min(t1, wlast / KT + 1)) : t1;
     skip(t0, w0);
 #pragma unroll 1
     for (int t = w0; t < w1; ++t) {
-      stage(t);
-            const int p0 = t * KT;
-      {
-        f32x16 s[NQ][KB];
+      arrive(t);
+      const int p0 = t * KT;
+      const int next = min(t + 1, t1 - 1);  // (the last block is asked for again: no branch among the products)
+      f32x16 s[KB];
 #pragma unroll
-        for (int n = 0; n < NQ; ++n)
+      for (int kb = 0; kb < KB; ++kb) s[kb] = f32x16{};
+      int ka = kaddr + (t & 1) * 2 * T::kBytes, va = vaddr + (t & 1) * 2 * T::kBytes;
+      asm volatile("" : "+v"(ka), "+v"(va));  // (addresses are worked out here, not kept over the walk)
+      auto kread = [&](int i) {
+        return *reinterpret_cast<const bf16x8 *>(lds + (ka ^ (32 * (i / KB))) + 32 * (i % KB) * T::RB);
+      };
+      auto vread = [&](int i) {
+        s16x4t v[2];
 #pragma unroll
-          for (int kb = 0; kb < KB; ++kb) s[n][kb] = f32x16{};
-        int ka = kaddr + (t & 1) * 2 * T::kBytes, va = vaddr + (t & 1) * 2 * T::kBytes + T::kBytes;
-        asm volatile("" : "+v"(ka), "+v"(va));  // (addresses are worked out here, not kept over the walk)
-        auto kread = [&](int i) {
-          return *reinterpret_cast<const bf16x8 *>(lds + (ka ^ (32 * (i / KB))) + 32 * (i % KB) * T::RB);
-        };
-        auto vread = [&](int i) {
-          s16x4t v[2];
+        for (int e = 0; e < 2; ++e)
+          v[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4t *)(
+              lds + (va ^ (64 * (i % DB) + 32 * e)) + (16 * (i / DB) + 8 * e) * T::RB));
+        return __builtin_bit_cast(bf16x8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
+      };
+      const int flag = sbad[t & 1];
+      bf16x8 ring[kAhead];
 #pragma unroll
-          for (int e = 0; e < 2; ++e)
-            v[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4t *)(
-                lds + (va ^ (64 * (i % DB) + 32 * e)) + (16 * (i / DB) + 8 * e) * T::RB));
-          return __builtin_bit_cast(bf16x8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
-        };
-        bf16x8 ring[kAhead];
+      for (int i = 0; i < kAhead; ++i) ring[i] = kread(i);
+      // the next block's loads go out between the products, whose issue they do not hold up
+      constexpr int kEvery = KS * KB / (2 * NL);  // products between two loads
+      bool bad = false;
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i) ring[i] = kread(i);
-#pragma unroll
-        for (int i = 0; i < KS * KB; ++i) {
-          __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-          for (int n = 0; n < NQ; ++n) s[n][i % KB] = mfma32(ring[i % kAhead], q[n][i / KB], s[n][i % KB]);
-          if (i + kAhead < KS * KB) ring[i % kAhead] = kread(i + kAhead);
-        }
+      for (int i = 0; i < KS * KB; ++i) {
         __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) ring[i] = vread(i);
-        __builtin_amdgcn_sched_barrier(0);
-        const bool flagged = sbad[t & 1] == t;
-        const bool partial = p0 < wfrom_last || p0 + KT - 1 > wfirst || flagged;
-        if (partial) {
-#pragma unroll
-          for (int n = 0; n < NQ; ++n)
-#pragma unroll
-            for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const int at = p0 + 32 * kb + 8 * (e >> 2) + 4 * half + (e & 3);
-                if (at > place[n] || at < from[n]) s[n][kb][e] = kNegInf;
-              }
-          if (flagged) {
-#pragma unroll
-            for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const int at = p0 + 32 * kb + 8 * (e >> 2) + 4 * half + (e & 3);
-                const int id = g.page_table[int64_t(ch.slot) * g.max_pages + (min(at, ch.len - 1) >> g.page_shift)];
-                if (id <= 0 || id >= g.pages)
-#pragma unroll
-                  for (int n = 0; n < NQ; ++n) s[n][kb][e] = kNegInf;
-              }
+        s[i % KB] = mfma32(ring[i % kAhead], q[i / KB], s[i % KB]);
+        if (i + kAhead < KS * KB) ring[i % kAhead] = kread(i + kAhead);
+        if (i % kEvery == 0) {
+          const int j = i / kEvery / 2;
+          if (i / kEvery % 2 == 0) {
+            bad |= locate(next, j);
+            ask(t + 1, j, false);
+          } else {
+            ask(t + 1, j, true);
           }
         }
-        float mr[NQ];
+      }
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int n = 0; n < NQ; ++n) {
-          float top = s[n][0][0];
+      for (int i = 0; i < kAhead; ++i) ring[i] = vread(i);
+      __builtin_amdgcn_sched_barrier(0);
+      located(next, bad);
+      fetch(kraw, g.k);
+      fetch(vraw, g.v);
+      load_ids(next + 1);
+      const bool flagged = uniform(flag) == t;
+      if (p0 < wfrom_last || p0 + KT - 1 > wfirst || flagged) [[unlikely]] {  // seen in part
+        const int from = seen_from(p, ch.begin, place);
 #pragma unroll
-          for (int kb = 0; kb < KB; ++kb)
+        for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) top = fmaxf(top, s[n][kb][e]);
-          top = halves_max(top) * p.c;
-          if (__any(top > m[n] + kGrowth)) {
-            const float to = fmaxf(m[n], top), f = fexp2(m[n] - ref(to));
-            l[n] *= f;
-#pragma unroll
-            for (int b = 0; b < DB; ++b)
-#pragma unroll
-              for (int e = 0; e < 16; ++e) o[n][b][e] *= f;
-            m[n] = to;
+          for (int e = 0; e < 16; ++e) {
+            const int at = p0 + 32 * kb + 8 * (e >> 2) + 4 * half + (e & 3);
+            if (at > place || at < from) s[kb][e] = kNegInf;
           }
-          mr[n] = ref(m[n]);
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        if (flagged) {
 #pragma unroll
           for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              s[n][kb][e] = fexp2(fmaf(s[n][kb][e], p.c, -mr[n]));
-              sum[e & 3] += s[n][kb][e];
+              const int at = p0 + 32 * kb + 8 * (e >> 2) + 4 * half + (e & 3);
+              const int id = g.page_table[int64_t(ch.slot) * g.max_pages + (min(at, ch.len - 1) >> g.page_shift)];
+              if (id <= 0 || id >= g.pages) s[kb][e] = kNegInf;
             }
-          l[n] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         }
-#pragma unroll
-          for (int ks = 0; ks < 2 * KB; ++ks) {
-            bf16x8 pf[NQ];
-#pragma unroll
-            for (int n = 0; n < NQ; ++n) {
-              u32x4 w;
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                w[i] = cvt_pk_bf16(s[n][ks >> 1][8 * (ks & 1) + 2 * i], s[n][ks >> 1][8 * (ks & 1) + 2 * i + 1]);
-              pf[n] = __builtin_bit_cast(bf16x8, w);
-            }
-#pragma unroll
-            for (int b = 0; b < DB; ++b) {
-              constexpr int all_v = 2 * KB * DB;
-              const int i = ks * DB + b;
-              __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-              for (int n = 0; n < NQ; ++n) o[n][b] = mfma32(ring[i % kAhead], pf[n], o[n][b]);
-              if (i + kAhead < all_v) ring[i % kAhead] = vread(i + kAhead);
-            }
-          }
       }
-      finish(t);
-    }
-    skip(w1, t1);
-  };
-  // ---- results ----
-  // (arguments and rows are read and worked out anew: they would take registers over the walk)
-  auto store = [&](int kind) {
-    const char __attribute__((address_space(4))) *args =
-        (const char __attribute__((address_space(4))) *)__builtin_amdgcn_kernarg_segment_ptr();
-    int first = row0 + c;
-    asm volatile("" : "+s"(args), "+v"(first));
-    static_assert(sizeof(KvGeom) % alignof(ChunkDev) == 0 && alignof(ChunkDev) == 8, "kernel arguments");
-    const auto &p = *(const ChunkDev __attribute__((address_space(4))) *)(args + sizeof(KvGeom));
+      float top = s[0][0];
 #pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-      const float ln = halves_sum(l[n]);
-      const int row = first + 32 * n, mine = row - ch.rows0;  // row of the request, of the tile
-      if (row < all) {
-        if (p.parts > 1) {
-          const int64_t at = (((int64_t(tile) * g.kv_heads + h) * p.parts + part) * ROWS) + mine;
-          if (half == 0 && kind <= kFinite) {
-            p.ml[2 * at] = ln == 0.f ? kNegInf : m[n];
-            p.ml[2 * at + 1] = ln;
-          }
-          float *to = p.o + at * D + 4 * half;
-          if (ln != 0.f)
+      for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-            for (int b = 0; b < DB; ++b)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                f32x4 v = {o[n][b][4 * i], o[n][b][4 * i + 1], o[n][b][4 * i + 2], o[n][b][4 * i + 3]};
-                if (kind > kFinite) {
-                  const f32x4 old = ld4(to + 32 * b + 8 * i);
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) v[e] = v[e] > 0.f ? beyond(old[e], kind) : old[e];
-                }
-                st4(to + 32 * b + 8 * i, v);
-              }
-          continue;
-        }
-        const int token = row / p.group;
-        const int64_t orow = int64_t(ch.bos + token) * p.a.q_heads + h * p.group + (row - token * p.group);
-        if (p.lse && half == 0 && kind <= kFinite)
-          p.lse[orow] = ln == 0.f ? kNegInf : (m[n] + __builtin_amdgcn_logf(ln)) * kLn2;
-        const float f = ln == 0.f ? 0.f : g.v_scale / ln;
-        uint16_t *to = p.a.out + orow * D + 8 * half;
+        for (int e = 0; e < 16; ++e) top = fmaxf(top, s[kb][e]);
+      top = halves_max(top) * p.c;
+      if (__any(top > m + kGrowth)) {
+        const float to = fmaxf(m, top), f = fexp2(m - ref(to));
+        l *= f;
 #pragma unroll
         for (int b = 0; b < DB; ++b)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            // columns 16 i + 8 h + 0..3 and + 4..7 of the block: the halves swap what the other stores
-            u32x4 w;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint32_t x = cvt_pk_bf16(o[n][b][8 * i + 2 * e] * f, o[n][b][8 * i + 2 * e + 1] * f);
-              const uint32_t y = cvt_pk_bf16(o[n][b][8 * i + 4 + 2 * e] * f, o[n][b][8 * i + 5 + 2 * e] * f);
-              const auto r = __builtin_amdgcn_permlane32_swap(x, y, false, false);
-              w[e] = r[0];
-              w[2 + e] = r[1];
-            }
-            u32x4 *at = reinterpret_cast<u32x4 *>(to + 32 * b + 16 * i);
-            if (kind > kFinite) {
-              const u32x4 old = *at;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float lo = __uint_as_float(w[e] << 16), hi = __uint_as_float(w[e] & 0xffff0000u);
-                const float a = __uint_as_float(old[e] << 16), b = __uint_as_float(old[e] & 0xffff0000u);
-                w[e] = pack_bf16x2(lo > 0.f ? beyond(a, kind) : a, hi > 0.f ? beyond(b, kind) : b);
-              }
-            }
-            *at = w;
-          }
+          for (int e = 0; e < 16; ++e) o[b][e] *= f;
+        m = to;
       }
+      const float mr = ref(m);
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          s[kb][e] = fexp2(fmaf(s[kb][e], p.c, -mr));
+          sum[e & 3] += s[kb][e];
+        }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+#pragma unroll
+      for (int ks = 0; ks < 2 * KB; ++ks) {
+        u32x4 w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w[i] = cvt_pk_bf16(s[ks >> 1][8 * (ks & 1) + 2 * i], s[ks >> 1][8 * (ks & 1) + 2 * i + 1]);
+        const bf16x8 pf = __builtin_bit_cast(bf16x8, w);
+#pragma unroll
+        for (int b = 0; b < DB; ++b) {
+          const int i = ks * DB + b;
+          if (b == 0 && D == 256) asm volatile("" : "+v"(va));
+          __builtin_amdgcn_sched_barrier(0);
+          o[b] = mfma32(ring[i % kAhead], pf, o[b]);
+          if (i + kAhead < 2 * KB * DB) ring[i % kAhead] = vread(i + kAhead);
+        }
+      }
+      convert(t + 1);
     }
+    skip(w1, t1);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  };
+
+  // ---- results ----
+  auto store = [&](int kind) {
+    int row = row0 + c;
+    asm volatile("" : "+v"(row));
+    const args_t again = fresh(args);
+    const auto &p = again->p;
+    const float ln = halves_sum(l);
+    if (row >= ch.n * p.group) return;
+    const int token = row / p.group;
+    const int64_t orow = int64_t(ch.bos + token) * p.a.q_heads + h * p.group + (row - token * p.group);
+    if (!whole) {
+      const int64_t at = int64_t(part) * p.a.tokens * p.a.q_heads + orow;
+      if (half == 0 && kind <= kFinite) {
+        p.ml[2 * at] = ln == 0.f ? kNegInf : m;
+        p.ml[2 * at + 1] = ln;
+      }
+      if (ln == 0.f) return;
+      float *to = p.o + at * D + 4 * half;
+#pragma unroll
+      for (int b = 0; b < DB; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          f32x4 v = {o[b][4 * i], o[b][4 * i + 1], o[b][4 * i + 2], o[b][4 * i + 3]};
+          if (kind > kFinite) {
+            const f32x4 old = ld4(to + 32 * b + 8 * i);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = v[e] > 0.f ? beyond(old[e], kind) : old[e];
+          }
+          st4(to + 32 * b + 8 * i, v);
+        }
+      return;
+    }
+    if (p.lse && half == 0 && kind <= kFinite)
+      p.lse[orow] = ln == 0.f ? kNegInf : (m + __builtin_amdgcn_logf(ln)) * kLn2;
+    const float f = ln == 0.f ? 0.f : again->g.v_scale / ln;
+    uint16_t *to = p.a.out + orow * D + 8 * half;
+#pragma unroll
+    for (int b = 0; b < DB; ++b)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        // columns 16 i + 8 h + 0..3 and + 4..7 of the block: the halves swap what the other stores
+        u32x4 w;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t x = cvt_pk_bf16(o[b][8 * i + 2 * e] * f, o[b][8 * i + 2 * e + 1] * f);
+          const uint32_t y = cvt_pk_bf16(o[b][8 * i + 4 + 2 * e] * f, o[b][8 * i + 5 + 2 * e] * f);
+          const auto r = __builtin_amdgcn_permlane32_swap(x, y, false, false);
+          w[e] = r[0];
+          w[2 + e] = r[1];
+        }
+        u32x4 *at = reinterpret_cast<u32x4 *>(to + 32 * b + 16 * i);
+        if (kind > kFinite) {
+          const u32x4 old = *at;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float lo = __uint_as_float(w[e] << 16), hi = __uint_as_float(w[e] & 0xffff0000u);
+            const float x = __uint_as_float(old[e] << 16), y = __uint_as_float(old[e] & 0xffff0000u);
+            w[e] = pack_bf16x2(lo > 0.f ? beyond(x, kind) : x, hi > 0.f ? beyond(y, kind) : y);
+          }
+        }
+        *at = w;
+      }
   };
 
 #pragma unroll 1
@@ -604,13 +644,17 @@ void attn_prefill_kernel(KvGeom g, ChunkDev p) {
       float bad = 0.f;
       if (wlive) {
 #pragma unroll
-        for (int n = 0; n < NQ; ++n)
+        for (int b = 0; b < DB; ++b)
 #pragma unroll
-          for (int b = 0; b < DB; ++b)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) bad = fmaf(o[n][b][e], 0.f, bad);
+          for (int e = 0; e < 16; ++e) bad = fmaf(o[b][e], 0.f, bad);
       }
-      if (__syncthreads_or(bad != 0.f)) {
+      // (flags: static shared memory would move the blocks off address 0)
+      const bool any = __any(bad != 0.f);
+      if (lane == 0) sbad[2 + (wave & 1)] = 0;
+      __syncthreads();
+      if (any && lane == 0) sbad[2] = 1;
+      __syncthreads();
+      if (uniform(sbad[2])) {
         kind = kFinite;
         continue;
       }
@@ -621,45 +665,65 @@ void attn_prefill_kernel(KvGeom g, ChunkDev p) {
   }
 }
 
-// Rows whose places were divided: the parts' O, m and l joined.  One workgroup per tile and
-// key-value head, a wave per row.
-template <int D>
+// Tiles that were divided: the pieces' O, m and l joined.  A wave has kJoinRows rows, one after the
+// other; its lanes first have a piece's m and l each, then D / 64 columns of the row.
+template <int D, int kJoinRows>
 __global__ __launch_bounds__(kThreads) void attn_prefill_join_kernel(KvGeom g, ChunkDev p) {
+  constexpr int N = D / 64, GROUPS = kRows / (kWaves * kJoinRows), kPieces = 4;
+  typedef float fN __attribute__((ext_vector_type(N)));
   const int64_t item = flat_block();
-  const int h = int(item % g.kv_heads), tile = int(item / g.kv_heads);
+  const int64_t unit = item / GROUPS;
+  const int h = int(unit % g.kv_heads), tile = int(unit / g.kv_heads);
   if (tile >= p.tiles) return;
-  const Chunk ch = chunk_of(g, p, tile, false);
+  const Chunk ch = chunk_of(g, p, tile, request_of(p, tile), false);
   if (!ch.any) return;
+  const int pieces = (span_of<Tile<D, false>::KT>(p, ch).n + p.piece - 1) / p.piece;
+  if (pieces < 2) return;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const int rows = min(p.rows, ch.n * p.group - ch.rows0);
-  constexpr int N = D / 64;  // columns of a lane
-  for (int i = wave; i < rows; i += kWaves) {
-    const int64_t at = (int64_t(tile) * g.kv_heads + h) * p.parts * p.rows + i;
-    float m = kNegInf;
-    for (int part = 0; part < p.parts; ++part) m = fmaxf(m, p.ml[2 * (at + int64_t(part) * p.rows)]);
-    float l = 0.f, o[N];
+  const int64_t stride = int64_t(p.a.tokens) * p.a.q_heads;  // rows of a part
+#pragma unroll 1
+  for (int i = 0; i < kJoinRows; ++i) {
+    const int row = ch.rows0 + (int(item % GROUPS) * kWaves + wave) * kJoinRows + i;
+    if (row >= ch.n * p.group) return;
+    const int token = token_of(p, row);
+    const int64_t orow = int64_t(ch.bos + token) * p.a.q_heads + h * p.group + (row - token * p.group);
+    float top = kNegInf, l = 0.f;
+    fN o = {};
+    for (int base = 0; base < pieces; base += 64) {
+      const int n = min(64, pieces - base);
+      const float *e = p.ml + 2 * (orow + (base + min(lane, n - 1)) * stride);
+      const float m = lane < n ? e[0] : kNegInf, pl = lane < n ? e[1] : 0.f;
+      float mm = fmaxf(m, top);  // (the sums so far have the maximum top)
 #pragma unroll
-    for (int e = 0; e < N; ++e) o[e] = 0.f;
-    for (int part = 0; part < p.parts; ++part) {
-      const int64_t r = at + int64_t(part) * p.rows;
-      const float pm = p.ml[2 * r], pl = p.ml[2 * r + 1];
-      if (pl == 0.f) continue;
-      const float f = fexp2(pm - m);
-      l = fmaf(pl, f, l);
-      const float *src = p.o + r * D + lane * N;
+      for (int d = 32; d; d >>= 1) mm = fmaxf(mm, __shfl_xor(mm, d));
+      const float f = pl == 0.f ? 0.f : fexp2(m - mm), old = top == kNegInf ? 0.f : fexp2(top - mm);
+      l = fmaf(l, old, wave_sum(pl * f));
+      o *= old;
+      top = mm;
+      const float *src = p.o + (orow + base * stride) * D + lane * N;
+      for (int k = 0; k < n; k += kPieces) {
+        fN v[kPieces];
 #pragma unroll
-      for (int e = 0; e < N; ++e) o[e] = fmaf(src[e], f, o[e]);
+        for (int u = 0; u < kPieces; ++u) v[u] = *reinterpret_cast<const fN *>(src + min(k + u, n - 1) * stride * D);
+#pragma unroll
+        for (int u = 0; u < kPieces; ++u) {
+          // (a lane past the last has l = 0; a piece of l = 0 has not written its O)
+          const int at = min(k + u, 63);
+          const float fk = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), at));
+          const float lk = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(pl), at));
+#pragma unroll
+          for (int c = 0; c < N; ++c) o[c] = lk == 0.f || k + u > 63 ? o[c] : fmaf(v[u][c], fk, o[c]);
+        }
+      }
     }
-    const int row = ch.rows0 + i, token = row / p.group, head = h * p.group + (row - token * p.group);
-    const int64_t orow = int64_t(ch.bos + token) * p.a.q_heads + head;
-    if (p.lse && lane == 0) p.lse[orow] = l == 0.f ? kNegInf : (m + __builtin_amdgcn_logf(l)) * kLn2;
+    if (p.lse && lane == 0) p.lse[orow] = l == 0.f ? kNegInf : (top + __builtin_amdgcn_logf(l)) * kLn2;
     const float f = l == 0.f ? 0.f : g.v_scale / l;
     uint16_t *to = p.a.out + orow * D + lane * N;
     if constexpr (N == 1) {
       to[0] = f32_to_bf16(o[0] * f);
     } else {
 #pragma unroll
-      for (int e = 0; e < N / 2; ++e) reinterpret_cast<uint32_t *>(to)[e] = cvt_pk_bf16(o[2 * e] * f, o[2 * e + 1] * f);
+      for (int c = 0; c < N / 2; ++c) reinterpret_cast<uint32_t *>(to)[c] = cvt_pk_bf16(o[2 * c] * f, o[2 * c + 1] * f);
     }
   }
 }
@@ -777,27 +841,42 @@ void attn_prefill_mass_kernel(KvGeom g, ChunkDev p, int blocks) {
 
 size_t pad256(size_t n) { return (n + 255) & ~size_t(255); }
 
-int64_t chunk_tiles(int batch, int tokens, int group, int rows) { return int64_t(tokens) * group / rows + batch; }
-int chunk_rows() { return kRows * GDN_NQ; }
+int64_t chunk_tiles(int batch, int tokens, int group) { return int64_t(tokens) * group / kRows + batch; }
 
-// Parts that a tile's places are divided into: workgroups for two on every compute unit, of 512
-// places or more each (by the bound max_len).
-int chunk_parts(const gdn_kv_pool *p, int64_t tiles, int max_len) {
-  const int64_t groups = std::max<int64_t>(1, tiles * p->d.kv_heads);
-  const int64_t want = (2 * kCUs + groups - 1) / groups;
-  return int(std::max<int64_t>(1, std::min<int64_t>(want, max_len / 512)));
-}
-
-// Parts of the workspace, in order.
-struct ChunkSpace {
-  size_t o, ml, lse;
+// How a call's tiles are divided.
+struct ChunkPlan {
+  int64_t tiles;
+  int parts, piece;
+  size_t o, ml, lse;  // parts of the workspace, in order
 };
-ChunkSpace chunk_space(const gdn_kv_pool *p, int batch, int tokens, int q_heads, int max_len, int mass_tokens) {
-  ChunkSpace r{};
-  const int64_t tiles = chunk_tiles(batch, tokens, q_heads / p->d.kv_heads, chunk_rows());
-  const int parts = chunk_parts(p, tiles, max_len);
-  if (parts > 1) {
-    const size_t rows = size_t(tiles) * p->d.kv_heads * parts * chunk_rows();
+ChunkPlan chunk_plan(const gdn_kv_pool *p, int batch, int tokens, int q_heads, int max_len, int mass_tokens) {
+  ChunkPlan r{};
+  if (batch == 0 || tokens == 0) return r;
+  const int KT = p->d.head_dim == 256 ? 32 : 64, group = q_heads / p->d.kv_heads;
+  r.tiles = chunk_tiles(batch, tokens, group);
+  const int most = max_len / KT + 1;  // blocks of a tile
+  constexpr int64_t slots = 2 * kCUs;
+  const int64_t tiles = (int64_t(tokens) * group + kRows - 1) / kRows + (batch - 1) / 2, units = tiles * p->d.kv_heads;
+  const int64_t each = tokens / batch, cached = std::max<int64_t>(0, max_len - each);
+  const int64_t mean = (cached + each / 2) / KT + 1;
+  int parts = 1;
+  if (units >= 8 * slots) {
+    parts = 1;
+  } else if (batch > 1 || 4 * mean < 3 * most) {
+    const int64_t per = std::max<int64_t>(1, units * mean * 3 / (4 * slots));
+    parts = int(std::min<int64_t>((most + per - 1) / per, most / 8));
+  } else {
+    int64_t best = INT64_MAX;
+    for (int n = 1; n <= 512 && n <= std::max(1, most / 8); ++n) {
+      const int64_t cost = ((units * n + slots - 1) / slots) * ((most + n - 1) / n + 3) * 64 + units * n;
+      if (cost < best) best = cost, parts = n;
+    }
+  }
+  r.parts = std::max(1, parts);
+  r.piece = (most + r.parts - 1) / r.parts;
+  r.parts = (most + r.piece - 1) / r.piece;
+  if (r.parts > 1) {
+    const size_t rows = size_t(r.parts) * tokens * q_heads;
     r.o = pad256(rows * p->d.head_dim * 4);
     r.ml = pad256(rows * 8);
   }
@@ -809,12 +888,15 @@ template <int D, bool kF8>
 hipError_t launch_dt(const KvGeom &g, const ChunkDev &p, hipStream_t s) {
   const bool wide = (1 << g.page_shift) >= 16;
   const int64_t units = int64_t(p.tiles) * g.kv_heads;
-  const auto kernel = wide ? attn_prefill_kernel<D, kF8, true, GDN_NQ> : attn_prefill_kernel<D, kF8, false, GDN_NQ>;
+  const auto kernel = wide ? attn_prefill_kernel<D, kF8, true> : attn_prefill_kernel<D, kF8, false>;
   constexpr int shared = Tile<D, kF8>::kShared;
-  hipLaunchKernelGGL(kernel, flat_grid(units * p.parts), dim3(kThreads), shared, s, g, p);
+  hipLaunchKernelGGL(kernel, flat_grid(units * p.parts), dim3(kThreads), shared, s, ChunkArgsAll{g, p});
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && p.parts > 1) {
-    hipLaunchKernelGGL((attn_prefill_join_kernel<D>), flat_grid(units), dim3(kThreads), 0, s, g, p);
+    if (units > 256)
+      hipLaunchKernelGGL((attn_prefill_join_kernel<D, 8>), flat_grid(units * (kRows / kWaves / 8)), dim3(kThreads), 0, s, g, p);
+    else
+      hipLaunchKernelGGL((attn_prefill_join_kernel<D, 1>), flat_grid(units * (kRows / kWaves)), dim3(kThreads), 0, s, g, p);
     e = hipGetLastError();
   }
   if (e == hipSuccess && p.a.mass_tokens > 0) {
@@ -838,12 +920,12 @@ bool chunk_fits(const gdn_kv_pool *p, int batch, int tokens, int q_heads, int ma
   const int64_t group = q_heads / p->d.kv_heads, limit = int64_t(1) << 31;
   const int64_t blocks = int64_t(max_len) / MassTile<256>::kPlaces + 1;
   // rows of a request and tiles are counted in 31 bits, workgroups in 40
-  return int64_t(tokens) * group < limit - kRows && chunk_tiles(batch, tokens, int(group), kRows) < limit / p->d.kv_heads &&
+  return int64_t(tokens) * group < limit - kRows && chunk_tiles(batch, tokens, int(group)) < limit / p->d.kv_heads &&
          int64_t(batch) * p->d.kv_heads < (int64_t(1) << 40) / blocks;
 }
 
 size_t chunk_workspace(const gdn_kv_pool *p, int batch, int tokens, int q_heads, int max_len, int mass_tokens) {
-  const ChunkSpace w = chunk_space(p, batch, tokens, q_heads, max_len, mass_tokens);
+  const ChunkPlan w = chunk_plan(p, batch, tokens, q_heads, max_len, mass_tokens);
   return w.o + w.ml + w.lse;
 }
 
@@ -852,18 +934,19 @@ hipError_t launch_attn_prefill(const gdn_kv_pool *pool, int layer, const ChunkAr
   ChunkDev p{};
   p.a = a;
   p.group = a.q_heads / pool->d.kv_heads;
-  p.rows = chunk_rows();
-  p.tiles = int(chunk_tiles(a.batch, a.tokens, p.group, p.rows));
-  p.parts = chunk_parts(pool, p.tiles, a.max_len);
+  const ChunkPlan w = chunk_plan(pool, a.batch, a.tokens, a.q_heads, a.max_len, a.mass_tokens);
+  p.inverse = uint32_t(((uint64_t(1) << 32) + p.group - 1) / p.group);
+  p.tiles = int(w.tiles);
+  p.parts = w.parts;
+  p.piece = w.piece;
   p.c = fabsf(a.scale) * pool->d.k_scale * kLog2e;
   p.flip = std::signbit(a.scale) ? 0x80008000u : 0u;
   p.keep = p.c == 0.f ? 0u : ~0u;  // (a score of -inf must stay -inf where it is multiplied by c)
   p.c = p.c == 0.f ? 1.f : p.c;
-  const ChunkSpace w = chunk_space(pool, a.batch, a.tokens, a.q_heads, a.max_len, a.mass_tokens);
   char *at = static_cast<char *>(a.workspace);
   p.o = reinterpret_cast<float *>(at);
-  p.ml = reinterpret_cast<float *>(at + w.o);
-  p.lse = a.lse ? a.lse : a.mass_tokens > 0 ? reinterpret_cast<float *>(at + w.o + w.ml) : nullptr;
+  p.ml = reinterpret_cast<float *>(at += w.o);
+  p.lse = a.lse ? a.lse : a.mass_tokens > 0 ? reinterpret_cast<float *>(at + w.ml) : nullptr;
   const bool f8 = pool->d.kv_dtype == GDN_F8_E4M3;
   switch (pool->d.head_dim) {
     case 64: return launch_d<64>(g, p, f8, s);
