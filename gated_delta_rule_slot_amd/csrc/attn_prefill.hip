@@ -42,7 +42,9 @@ constexpr float kLn2 = 0.693147180559945309417f;
 constexpr float kNegInf = -__builtin_inff();
 constexpr float kGrowth = 8.f;  // log2 of how far the maximum may pass the reference
 
-constexpr int kRows = 32 * kWaves;  // rows of a tile
+constexpr int kRowBits = 7, kRows = 1 << kRowBits;  // rows of a tile, 32 of each wave
+
+constexpr int kMostTiles = 32768;  // in one dimension of the grid
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef short s16x4t __attribute__((ext_vector_type(4)));
@@ -120,29 +122,33 @@ __device__ __forceinline__ float beyond(float sum, int kind) { return sum + (kin
 // The tiles of request b begin at cu[b] * group / kRows + b: at least as many as it needs, and
 // found from cu alone, so that no list of tiles has to be made first.
 struct Chunk {
-  int b, bos, n, rows0;  // request, its first token and number of tokens, the tile's first row
+  int bos, n, rows0;     // the request's first token and number of tokens, the tile's first row
   int slot, len, begin;
   bool any, live;        // whether the tile has rows, whether they see anything at all
 };
-__device__ __forceinline__ int64_t first_tile(const ChunkDev &p, int b) {
-  return int64_t(((table_t)p.a.cu_seqlens)[b]) * p.group / kRows + b;
-}
-__device__ __forceinline__ int request_of(const ChunkDev &p, int tile) {
-  int lo = 0, hi = p.a.batch;  // the last request whose tiles begin at `tile` or before
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (first_tile(p, mid) <= tile) lo = mid;
-    else hi = mid;
+// The last request b for which begins(b, cu[b]) holds (it holds up to some request), or 0.  Called by
+// whole waves: a lane looks at a request, so up to 64 requests take one step of reads and 4096
+// two (a step costs a workgroup most of a microsecond).
+template <typename F>
+__device__ __forceinline__ int last_request(const ChunkDev &p, F begins) {
+  const int lane = threadIdx.x & 63;
+  int b = 0;  // it is one of n from here
+  for (int n = p.a.batch; n > 1;) {
+    const int step = (n + 63) >> 6, at = b + lane * step;
+    const bool in = lane * step < n;
+    const bool yes = begins(at, p.a.cu_seqlens[in ? at : b]);
+    const int i = uniform(max(0, int(__builtin_popcountll(__ballot(in && yes))) - 1));
+    n = min(step, n - i * step);
+    b += i * step;
   }
-  return lo;
+  return b;
 }
 __device__ __forceinline__ Chunk chunk_of(const KvGeom &g, const ChunkDev &p, int tile, int b, bool tell) {
   const table_t cu = (table_t)p.a.cu_seqlens;
   Chunk r;
-  r.b = b;
   r.bos = cu[b];
   const int eos = cu[b + 1];
-  const int64_t at = (tile - first_tile(p, b)) * kRows;
+  const int64_t at = (tile - ((int64_t(r.bos) * p.group) >> kRowBits) - b) * kRows;
   const bool ok = r.bos >= 0 && eos >= r.bos && eos <= p.a.tokens;
   r.n = ok ? eos - r.bos : 0;
   r.any = ok && at >= 0 && at < int64_t(r.n) * p.group;
@@ -225,7 +231,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2)))
 void attn_prefill_kernel(ChunkArgsAll) {
   using T = Tile<D, kF8>;
   constexpr int KT = T::KT, KB = KT / 32, KS = D / 16, DB = D / 32, NL = T::kLoads;
-  constexpr int kAhead = kF8 && D == 256 ? 3 : 4;  // fragments asked for before they are used
+  constexpr int kAhead = D == 256 ? 3 : 4;  // fragments asked for before they are used
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const args_t args = (args_t)__builtin_amdgcn_kernarg_segment_ptr();
   // a block (by its number's parity) that has a page outside the pool
@@ -235,12 +241,12 @@ void attn_prefill_kernel(ChunkArgsAll) {
 
   const KvGeom g = args->g;
   const ChunkDev p = args->p;
-  const int64_t item = flat_block();
-  const int h = uniform(int(item % g.kv_heads));
-  const int64_t rest = item / g.kv_heads;
-  const int part = uniform(int(rest / p.tiles)), tile = p.tiles - 1 - uniform(int(rest % p.tiles));
-  if (part >= p.parts) return;
-  const Chunk ch = chunk_of(g, p, tile, request_of(p, tile), h == 0 && part == 0 && threadIdx.x == 0);
+  // (tiles in both of the grid's last two dimensions where none is divided)
+  const int h = blockIdx.x, part = p.parts > 1 ? int(blockIdx.z) : 0;
+  const int tile = p.tiles - 1 - int(blockIdx.y + (p.parts > 1 ? 0 : blockIdx.z * kMostTiles));
+  if (tile < 0) return;
+  const int b = last_request(p, [&](int b, int cu) { return ((int64_t(cu) * p.group) >> kRowBits) + b <= tile; });
+  const Chunk ch = chunk_of(g, p, tile, b, h == 0 && part == 0 && threadIdx.x == 0);
   if (!ch.any) return;
   const Span span = span_of<KT>(p, ch);
   if (part > 0 && part * p.piece >= span.n) return;
@@ -665,28 +671,32 @@ void attn_prefill_kernel(ChunkArgsAll) {
   }
 }
 
-// Tiles that were divided: the pieces' O, m and l joined.  A wave has kJoinRows rows, one after the
-// other; its lanes first have a piece's m and l each, then D / 64 columns of the row.
-template <int D, int kJoinRows>
-__global__ __launch_bounds__(kThreads) void attn_prefill_join_kernel(KvGeom g, ChunkDev p) {
-  constexpr int N = D / 64, GROUPS = kRows / (kWaves * kJoinRows), kPieces = 4;
+// Rows of tiles that were divided: the pieces' O, m and l joined.  A wave has `heads` query heads of
+// a token, one after the other; its lanes first have a piece's m and l each, then D / 64 columns of
+// the row.
+template <int D>
+__global__ __launch_bounds__(kThreads) void attn_prefill_join_kernel(KvGeom g, ChunkDev p, int heads) {
+  constexpr int N = D / 64, kPieces = 4;
   typedef float fN __attribute__((ext_vector_type(N)));
-  const int64_t item = flat_block();
-  const int64_t unit = item / GROUPS;
-  const int h = int(unit % g.kv_heads), tile = int(unit / g.kv_heads);
-  if (tile >= p.tiles) return;
-  const Chunk ch = chunk_of(g, p, tile, request_of(p, tile), false);
-  if (!ch.any) return;
-  const int pieces = (span_of<Tile<D, false>::KT>(p, ch).n + p.piece - 1) / p.piece;
-  if (pieces < 2) return;
-  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int groups = (p.a.q_heads + heads - 1) / heads;
+  const int64_t item = flat_block() * kWaves + uniform(threadIdx.x >> 6);
+  const int token = int(item / groups), first = int(item - int64_t(token) * groups) * heads;
+  if (token >= p.a.tokens) return;
+  const int b = last_request(p, [&](int, int cu) { return cu <= token; });
+  const table_t cu = (table_t)p.a.cu_seqlens;
+  const int bos = cu[b];
+  if (token < bos || token >= cu[b + 1]) return;
+  const int lane = threadIdx.x & 63;
   const int64_t stride = int64_t(p.a.tokens) * p.a.q_heads;  // rows of a part
 #pragma unroll 1
-  for (int i = 0; i < kJoinRows; ++i) {
-    const int row = ch.rows0 + (int(item % GROUPS) * kWaves + wave) * kJoinRows + i;
-    if (row >= ch.n * p.group) return;
-    const int token = token_of(p, row);
-    const int64_t orow = int64_t(ch.bos + token) * p.a.q_heads + h * p.group + (row - token * p.group);
+  for (int head = first; head < min(first + heads, p.a.q_heads); ++head) {
+    const int row = (token - bos) * p.group + head % p.group;
+    const int tile = int((int64_t(bos) * p.group) >> kRowBits) + b + (row >> kRowBits);
+    const Chunk ch = chunk_of(g, p, tile, b, false);
+    if (!ch.any) return;
+    const int pieces = (span_of<Tile<D, false>::KT>(p, ch).n + p.piece - 1) / p.piece;
+    if (pieces < 2) continue;
+    const int64_t orow = int64_t(token) * p.a.q_heads + head;
     float top = kNegInf, l = 0.f;
     fN o = {};
     for (int base = 0; base < pieces; base += 64) {
@@ -856,23 +866,19 @@ ChunkPlan chunk_plan(const gdn_kv_pool *p, int batch, int tokens, int q_heads, i
   r.tiles = chunk_tiles(batch, tokens, group);
   const int most = max_len / KT + 1;  // blocks of a tile
   constexpr int64_t slots = 2 * kCUs;
-  const int64_t tiles = (int64_t(tokens) * group + kRows - 1) / kRows + (batch - 1) / 2, units = tiles * p->d.kv_heads;
-  const int64_t each = tokens / batch, cached = std::max<int64_t>(0, max_len - each);
-  const int64_t mean = (cached + each / 2) / KT + 1;
-  int parts = 1;
-  if (units >= 8 * slots) {
-    parts = 1;
-  } else if (batch > 1 || 4 * mean < 3 * most) {
-    const int64_t per = std::max<int64_t>(1, units * mean * 3 / (4 * slots));
-    parts = int(std::min<int64_t>((most + per - 1) / per, most / 8));
-  } else {
-    int64_t best = INT64_MAX;
-    for (int n = 1; n <= 512 && n <= std::max(1, most / 8); ++n) {
-      const int64_t cost = ((units * n + slots - 1) / slots) * ((most + n - 1) / n + 3) * 64 + units * n;
-      if (cost < best) best = cost, parts = n;
-    }
+  // As if all requests were alike (the host knows no more).  With as many tiles as workgroups that
+  // run at once none is divided.  Fewer are divided into as many pieces as fill the compute units: once
+  // where all tiles see about as many places (by the bound), a little or half more often where lengths
+  // differ or a tile sees half as many on the average, as the short ones leave room.  A piece has 4
+  // blocks or more.
+  const int64_t each = (int64_t(tokens) + batch - 1) / batch, tiles = batch * ((each * group + kRows - 1) / kRows);
+  const int64_t units = tiles * p->d.kv_heads;
+  if (units < slots) {
+    const bool rising = each > max_len / 2;
+    const int64_t want = rising ? (3 * slots / 2 + units - 1) / units : (batch > 1 ? 23 * slots / 20 : slots) / units;
+    r.parts = int(std::min<int64_t>(want, most / 4));
   }
-  r.parts = std::max(1, parts);
+  r.parts = std::max(1, r.parts);
   r.piece = (most + r.parts - 1) / r.parts;
   r.parts = (most + r.piece - 1) / r.piece;
   if (r.parts > 1) {
@@ -890,13 +896,15 @@ hipError_t launch_dt(const KvGeom &g, const ChunkDev &p, hipStream_t s) {
   const int64_t units = int64_t(p.tiles) * g.kv_heads;
   const auto kernel = wide ? attn_prefill_kernel<D, kF8, true> : attn_prefill_kernel<D, kF8, false>;
   constexpr int shared = Tile<D, kF8>::kShared;
-  hipLaunchKernelGGL(kernel, flat_grid(units * p.parts), dim3(kThreads), shared, s, ChunkArgsAll{g, p});
+  const dim3 grid(unsigned(g.kv_heads), unsigned(std::min(p.tiles, kMostTiles)),
+                  unsigned(p.parts > 1 ? p.parts : (p.tiles + kMostTiles - 1) / kMostTiles));
+  hipLaunchKernelGGL(kernel, grid, dim3(kThreads), shared, s, ChunkArgsAll{g, p});
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && p.parts > 1) {
-    if (units > 256)
-      hipLaunchKernelGGL((attn_prefill_join_kernel<D, 8>), flat_grid(units * (kRows / kWaves / 8)), dim3(kThreads), 0, s, g, p);
-    else
-      hipLaunchKernelGGL((attn_prefill_join_kernel<D, 1>), flat_grid(units * (kRows / kWaves)), dim3(kThreads), 0, s, g, p);
+    const int heads = std::max<int64_t>(1, std::min<int64_t>(p.a.q_heads, int64_t(p.a.tokens) * p.a.q_heads >> 13));
+    const int64_t waves = int64_t(p.a.tokens) * ((p.a.q_heads + heads - 1) / heads);
+    hipLaunchKernelGGL((attn_prefill_join_kernel<D>), flat_grid((waves + kWaves - 1) / kWaves), dim3(kThreads), 0, s, g, p,
+                       heads);
     e = hipGetLastError();
   }
   if (e == hipSuccess && p.a.mass_tokens > 0) {
