@@ -739,18 +739,22 @@ __global__ __launch_bounds__(kThreads) void attn_prefill_join_kernel(KvGeom g, C
 }
 
 // ---- the last queries' weights, added to mass -------------------------------
-// One workgroup per request, key-value head and 4 * KP places; a wave keeps the keys of its KP
-// places in registers and walks the rows of the last queries 32 at a time, so every entry of
-// mass has one owner and one order of summation.  A weight is exp(s - lse).
-template <int D>
-struct MassTile {
-  static constexpr int KP = D == 256 ? 32 : 64;
-  static constexpr int kPlaces = KP * kWaves;
-};
+// One workgroup per request, key-value head and 4 * kMassPlaces places; a wave keeps the keys of its
+// places in registers and walks the rows of the last queries, kMassRows at a time, which the waves
+// share in shared memory (in the layout of a block of keys), asked for one step ahead.  So every
+// entry of mass has one owner and one order of summation.  A weight is exp(s - lse).
+//
+// (512 queries over 131584 places, 16 heads of 256: 0.73 ms; reading the rows by each wave for
+// itself 2.25 ms, bound by its scattered reads.  64 places a wave instead of 32: 83 against 65 us for
+// two 4099-token prompts, as there are too few waves.)
+constexpr int kMassRows = 64, kMassPlaces = 32;
+
 template <int D, bool kF8>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2)))
 void attn_prefill_mass_kernel(KvGeom g, ChunkDev p, int blocks) {
-  constexpr int KP = MassTile<D>::KP, KB = KP / 32, KS = D / 16;
+  constexpr int KP = kMassPlaces, KB = KP / 32, KS = D / 16, NB = kMassRows / 32, RB = 2 * D, PLACES = KP * kWaves;
+  constexpr int LANES = RB / 16, LROWS = 64 / LANES, LOADS = kMassRows / (kWaves * LROWS);
+  extern __shared__ __attribute__((aligned(16))) char lds[];
   const int64_t item = flat_block();
   const int h = int(item % g.kv_heads);
   const int64_t rest = item / g.kv_heads;
@@ -766,10 +770,10 @@ void attn_prefill_mass_kernel(KvGeom g, ChunkDev p, int blocks) {
   const int place0 = len - n, first = n - late;
   const int lane = threadIdx.x & 63, c = lane & 31, half = lane >> 5;
   const int wave = uniform(threadIdx.x >> 6);
-  const int lowest = seen_from(p, begin, place0 + first) / MassTile<D>::kPlaces * MassTile<D>::kPlaces;
-  const int p0 = lowest + int(rest % blocks) * MassTile<D>::kPlaces + wave * KP;
-  if (p0 >= len) return;
-  const int G = p.group;
+  const int g0 = seen_from(p, begin, place0 + first) / PLACES * PLACES + int(rest % blocks) * PLACES;
+  if (g0 >= len) return;
+  const int p0 = g0 + wave * KP;
+  const int G = p.group, all = n * G;
 
   // a place's key: row c of block kb
   bf16x8 k[KB][KS];
@@ -782,58 +786,107 @@ void attn_prefill_mass_kernel(KvGeom g, ChunkDev p, int blocks) {
     const char *src = g.k + int64_t(max(row, 0)) * (kF8 ? D : 2 * D);
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
+      u32x4 w;
       if constexpr (kF8) {
         const u32x2 x = *reinterpret_cast<const u32x2 *>(src + 16 * s + 8 * half);
-        u32x4 w;
         uint32_t lo, hi;
         f8_to_bf16(x[0], &lo, &hi);
         w[0] = lo; w[1] = hi;
         f8_to_bf16(x[1], &lo, &hi);
         w[2] = lo; w[3] = hi;
-        k[kb][s] = __builtin_bit_cast(bf16x8, w);
       } else {
-        k[kb][s] = *reinterpret_cast<const bf16x8 *>(src + 32 * s + 16 * half);
+        w = *reinterpret_cast<const u32x4 *>(src + 32 * s + 16 * half);
       }
+      // (the scale's sign and 0, on this side of the product)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = (w[i] ^ p.flip) & p.keep;
+      k[kb][s] = __builtin_bit_cast(bf16x8, w);
     }
   }
 
+  // rows of the queries that see any of the workgroup's places
+  const int r0 = max(first, g0 - place0) * G;
+  int r1 = all;
+  if (p.a.window) r1 = int(min(int64_t(all), max(int64_t(0), int64_t(g0) + PLACES - 1 + p.a.window - place0) * G));
+  float lse[NB];
+  auto ask = [&](int r, int buffer) {
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j) {
+      const int at = (j * kWaves + wave) * LROWS, i = at + lane / LANES;
+      const int row = min(r + i, all - 1), token = token_of(p, row), head = h * G + (row - token * G);
+      const uint16_t *src = p.a.q + int64_t(bos + token) * p.a.q_stride + int64_t(head) * D;
+      const int piece = (lane % LANES) ^ twist<D>(i);
+      __builtin_amdgcn_global_load_lds((__attribute__((address_space(1))) const char *)src + 16 * piece,
+                                       (__attribute__((address_space(3))) void *)(lds + buffer * kMassRows * RB + at * RB),
+                                       16, 0, 0);
+    }
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const int row = min(r + 32 * nb + c, all - 1), token = token_of(p, row);
+      lse[nb] = p.lse[int64_t(bos + token) * p.a.q_heads + h * G + (row - token * G)];
+    }
+  };
   f32x16 sum[KB];
 #pragma unroll
   for (int kb = 0; kb < KB; ++kb) sum[kb] = f32x16{};
-  const int all = n * G;
-  // the first row that sees the wave's first place, and the last that sees its last
-  int r0 = max(first, p0 - place0) * G;
-  int r1 = all;
-  if (p.a.window) r1 = int(min(int64_t(all), max(int64_t(0), int64_t(p0) + KP - 1 + p.a.window - place0) * G));
+  const int qaddr = c * RB + ((half ^ twist<D>(c)) << 4);
+  if (r0 < r1) ask(r0, 0);
+  int buffer = 0;
 #pragma unroll 1
-  for (int r = r0; r < r1; r += 32) {
-    const int row = min(r + c, all - 1), token = row / G, head = h * G + (row - token * G);
-    const int place = place0 + token, from = seen_from(p, begin, place);
-    const int64_t qrow = int64_t(bos + token);
-    const uint16_t *src = p.a.q + qrow * p.a.q_stride + int64_t(head) * D + 8 * half;
-    const float lse = p.lse[qrow * p.a.q_heads + head];
-    f32x16 s[KB];
+  for (int r = r0; r < r1; r += kMassRows, buffer ^= 1) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    float shift[NB];
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb) s[kb] = f32x16{};
-#pragma unroll
-    for (int st = 0; st < KS; ++st) {
-      u32x4 w = *reinterpret_cast<const u32x4 *>(src + 16 * st);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = (w[i] ^ p.flip) & p.keep;
-      const bf16x8 q = __builtin_bit_cast(bf16x8, w);
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb) s[kb] = mfma32(k[kb][st], q, s[kb]);
-    }
-    const bool mine = r + c < r1 && lse != kNegInf;
-    const float shift = lse * kLog2e;
+    for (int nb = 0; nb < NB; ++nb) shift[nb] = lse[nb] == kNegInf ? kNegInf : -lse[nb] * kLog2e;
+    if (r + kMassRows < r1) ask(r + kMassRows, buffer ^ 1);
+    const int first_place = place0 + token_of(p, r), last_place = place0 + token_of(p, min(r + kMassRows, r1) - 1);
+    if (p0 > last_place || p0 + KP <= seen_from(p, begin, first_place)) continue;  // the wave's places are not seen
+    int qa = qaddr + buffer * kMassRows * RB;
+    asm volatile("" : "+v"(qa));
+    f32x16 s[KB][NB];
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int at = p0 + 32 * kb + 8 * (e >> 2) + 4 * half + (e & 3);
-        const float w = fexp2(fmaf(s[kb][e], p.c, -shift));
-        sum[kb][e] += mine && at <= place && at >= from ? w : 0.f;
+      for (int nb = 0; nb < NB; ++nb) s[kb][nb] = f32x16{};
+    constexpr int kAhead = 4;
+    auto qread = [&](int i) {
+      return *reinterpret_cast<const bf16x8 *>(lds + (qa ^ (32 * (i / NB))) + 32 * (i % NB) * RB);
+    };
+    bf16x8 ring[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) ring[i] = qread(i);
+#pragma unroll
+    for (int i = 0; i < KS * NB; ++i) {
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) s[kb][i % NB] = mfma32(k[kb][i / NB], ring[i % kAhead], s[kb][i % NB]);
+      if (i + kAhead < KS * NB) ring[i % kAhead] = qread(i + kAhead);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    const bool whole = r + kMassRows <= r1 && p0 + KP - 1 <= first_place && p0 >= seen_from(p, begin, last_place);
+    if (whole) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) sum[kb][e] += fexp2(fmaf(s[kb][nb][e], p.c, shift[nb]));
+    } else {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) {
+        const int row = r + 32 * nb + c, place = place0 + token_of(p, min(row, all - 1));
+        const int from = seen_from(p, begin, place), to = row < r1 ? place : -1;
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int at = p0 + 32 * kb + 8 * (e >> 2) + 4 * half + (e & 3);
+            const float w = fexp2(fmaf(s[kb][nb][e], p.c, shift[nb]));
+            sum[kb][e] += at <= to && at >= from ? w : 0.f;
+          }
       }
+    }
   }
   // over the 32 rows
   float *mass = g.mass + (int64_t(slot) * g.kv_heads + h) * g.capacity;
@@ -909,9 +962,9 @@ hipError_t launch_dt(const KvGeom &g, const ChunkDev &p, hipStream_t s) {
   }
   if (e == hipSuccess && p.a.mass_tokens > 0) {
     // the first block begins at or before the first place seen
-    const int blocks = p.a.max_len / MassTile<D>::kPlaces + 1;
+    const int blocks = p.a.max_len / (kMassPlaces * kWaves) + 1;
     hipLaunchKernelGGL((attn_prefill_mass_kernel<D, kF8>), flat_grid(int64_t(p.a.batch) * g.kv_heads * blocks),
-                       dim3(kThreads), 0, s, g, p, blocks);
+                       dim3(kThreads), 2 * kMassRows * 2 * D, s, g, p, blocks);
     e = hipGetLastError();
   }
   return e;
@@ -926,7 +979,7 @@ hipError_t launch_d(const KvGeom &g, const ChunkDev &p, bool f8, hipStream_t s) 
 
 bool chunk_fits(const gdn_kv_pool *p, int batch, int tokens, int q_heads, int max_len) {
   const int64_t group = q_heads / p->d.kv_heads, limit = int64_t(1) << 31;
-  const int64_t blocks = int64_t(max_len) / MassTile<256>::kPlaces + 1;
+  const int64_t blocks = int64_t(max_len) / (kMassPlaces * kWaves) + 1;
   // rows of a request and tiles are counted in 31 bits, workgroups in 40
   return int64_t(tokens) * group < limit - kRows && chunk_tiles(batch, tokens, int(group)) < limit / p->d.kv_heads &&
          int64_t(batch) * p->d.kv_heads < (int64_t(1) << 40) / blocks;
