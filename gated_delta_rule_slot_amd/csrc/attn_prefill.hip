@@ -365,7 +365,9 @@ void attn_prefill_kernel(ChunkArgsAll) {
       *at = hidden(t, j) ? u32x4{0, 0, 0, 0} : x;
     }
   };
-  // e4m3: through registers, 16 values a lane
+  // e4m3: through registers, 16 values a lane; with heads of 256 the keys before the values, as there
+  // are no registers for both
+  constexpr bool kTwoSteps = kF8 && D == 256;
   u32x4 kraw[kF8 ? NL : 1], vraw[kF8 ? NL : 1];
   auto fetch = [&](u32x4 *raw, const char *base) {
     if constexpr (kF8) {
@@ -481,6 +483,11 @@ void attn_prefill_kernel(ChunkArgsAll) {
         return __builtin_bit_cast(bf16x8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
       };
       const int flag = sbad[t & 1];
+      if constexpr (kTwoSteps) {
+        located(next, locate_all(next));
+        load_ids(next + 1);
+        fetch(kraw, g.k);
+      }
       bf16x8 ring[kAhead];
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) ring[i] = kread(i);
@@ -492,7 +499,7 @@ void attn_prefill_kernel(ChunkArgsAll) {
         __builtin_amdgcn_sched_barrier(0);
         s[i % KB] = mfma32(ring[i % kAhead], q[i / KB], s[i % KB]);
         if (i + kAhead < KS * KB) ring[i % kAhead] = kread(i + kAhead);
-        if (i % kEvery == 0) {
+        if (!kTwoSteps && i % kEvery == 0) {
           const int j = i / kEvery / 2;
           if (i / kEvery % 2 == 0) {
             bad |= locate(next, j);
@@ -506,10 +513,15 @@ void attn_prefill_kernel(ChunkArgsAll) {
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) ring[i] = vread(i);
       __builtin_amdgcn_sched_barrier(0);
-      located(next, bad);
-      fetch(kraw, g.k);
-      fetch(vraw, g.v);
-      load_ids(next + 1);
+      if constexpr (kTwoSteps) {
+        put(kraw, lds + ((t + 1) & 1) * 2 * T::kBytes);
+        fetch(vraw, g.v);
+      } else {
+        located(next, bad);
+        fetch(kraw, g.k);
+        fetch(vraw, g.v);
+        load_ids(next + 1);
+      }
       const bool flagged = uniform(flag) == t;
       if (p0 < wfrom_last || p0 + KT - 1 > wfirst || flagged) [[unlikely]] {  // seen in part
         const int from = seen_from(p, ch.begin, place);
@@ -572,7 +584,12 @@ void attn_prefill_kernel(ChunkArgsAll) {
           if (i + kAhead < 2 * KB * DB) ring[i % kAhead] = vread(i + kAhead);
         }
       }
-      convert(t + 1);
+      if constexpr (kTwoSteps) {
+        if (edge || kind != kAsIs) [[unlikely]] change_raw(next, kind);
+        put(vraw, lds + ((t + 1) & 1) * 2 * T::kBytes + T::kBytes);
+      } else {
+        convert(t + 1);
+      }
     }
     skip(w1, t1);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -656,7 +673,7 @@ void attn_prefill_kernel(ChunkArgsAll) {
       }
       // (flags: static shared memory would move the blocks off address 0)
       const bool any = __any(bad != 0.f);
-      if (lane == 0) sbad[2 + (wave & 1)] = 0;
+      if (threadIdx.x == 0) sbad[2] = 0;
       __syncthreads();
       if (any && lane == 0) sbad[2] = 1;
       __syncthreads();
@@ -770,7 +787,9 @@ void attn_prefill_mass_kernel(KvGeom g, ChunkDev p, int blocks) {
   const int place0 = len - n, first = n - late;
   const int lane = threadIdx.x & 63, c = lane & 31, half = lane >> 5;
   const int wave = uniform(threadIdx.x >> 6);
-  const int g0 = seen_from(p, begin, place0 + first) / PLACES * PLACES + int(rest % blocks) * PLACES;
+  const int lowest = seen_from(p, begin, place0 + first);
+  if (lowest >= len) return;
+  const int g0 = lowest / PLACES * PLACES + int(rest % blocks) * PLACES;
   if (g0 >= len) return;
   const int p0 = g0 + wave * KP;
   const int G = p.group, all = n * G;

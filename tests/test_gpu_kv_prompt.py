@@ -213,6 +213,87 @@ def test_chunk_later_tokens_that_are_not_finite(dim, group, window):
     assert torch.isnan(got[saw_key]).all() and torch.isnan(lse.cpu()[saw_key]).all()
 
 
+@pytest.mark.parametrize("dim,group,f8", [(64, 3, True), (128, 4, False), (256, 8, True), (256, 2, False)])
+def test_chunk_values_that_are_not_finite_in_divided_places(dim, group, f8):
+    """The same where the places are divided and joined, and in an e4m3 cache (which has NaN only)."""
+    n, L = 20, 3000
+    c = make_cache(dim + group, [L], None, 1, dim, 16, f8)
+    t = c.table[c.slots[0]]
+    bad = [(L - 7, 3)] if f8 else [(L - 7, 3), (L - 12, 9), (1000, 40)]
+    for i, (place, column) in enumerate(bad):
+        c.v[0, int(t[place // 16]), 0, place % 16, column] = float("nan") if i == 0 else float("inf")
+    pool, q, out, lse, sc = chunk_call(c, [n], group, late=n)
+    clean = make_cache(dim + group, [L], None, 1, dim, 16, f8)
+    _, _, want, wl, _ = chunk_call(clean, [n], group, q=q.cuda())
+    got, want = out.float().cpu(), want.float().cpu()
+    assert torch.equal(lse, wl) and torch.isfinite(pool.mass).all()
+    place = torch.arange(L - n, L)
+    hit = torch.zeros(n, dim, dtype=torch.bool)
+    for i, (at, column) in enumerate(bad):
+        sees = place >= at
+        hit[sees, column] = True
+        v = got[sees][:, :, column]
+        assert (torch.isnan(v) if i == 0 else torch.isposinf(v)).all()
+    free = ~hit[:, None, :].expand_as(got)
+    assert ((got - want).abs() <= 4 * 2.0 ** -8 * (want.abs() + 4))[free].all()
+
+
+@pytest.mark.parametrize("batch,dim,group", [(65, 64, 1), (300, 128, 3), (5000, 64, 2)])
+def test_chunk_many_requests(batch, dim, group):
+    """More requests than a wave has lanes, and than two steps of its search reach, some of them
+    empty or padding, lengths of a few."""
+    r = np.random.default_rng(batch)
+    new = [int(x) for x in r.integers(0, 4, size=batch)]
+    lens = [max(1, n + int(x)) for n, x in zip(new, r.integers(0, 6, size=batch))]
+    slots = [int(x) + 1 for x in r.permutation(batch)]
+    for b in range(0, batch, 11):
+        slots[b] = 0
+    c = make_cache(batch, lens, None, 1, dim, 4, slots=slots)
+    pool, q, out, lse, sc = chunk_call(c, new, group, late=2, extra=3)
+    check_chunk(c, new, q, sc, out, lse, 0, 2, pool.mass)
+    assert int(pool.err_word.item()) == 0
+
+
+def test_chunk_more_tiles_than_one_dimension_of_a_grid():
+    """A prompt of 70000 tokens and 64 query heads in a narrow window (35000 tiles): rows from all over
+    it against the definition."""
+    import gated_delta_rule_slot_amd as gdn
+
+    n, page, window = 70000, 64, 40
+    g = torch.Generator(device="cuda").manual_seed(5)
+    pages = -(-n // page) + 1
+    k, v = (torch.randn(1, pages, 1, page, 64, device="cuda", generator=g).to(torch.bfloat16) for _ in range(2))
+    table = torch.zeros(2, pages - 1, dtype=torch.int32)
+    table[1] = torch.randperm(pages - 1, generator=torch.Generator().manual_seed(1)).to(torch.int32) + 1
+    pool = gdn.kv_pool_create(k, v, table.cuda(), err_word=i32([0]))
+    q = torch.randn(n, 64, 64, device="cuda", generator=g).to(torch.bfloat16)
+    out = torch.full_like(q, -7.0)
+    ws = torch.empty(gdn.attn_prefill_workspace_bytes(pool, 1, n, 64, n), dtype=torch.uint8, device="cuda")
+    gdn.attn_prefill_paged(pool, 0, i32([0, n]), i32([1]), i32([n]), q, out, n, window=window, scale=0.125, workspace=ws)
+    assert int(pool.err_word.item()) == 0
+    kh, vh = (t[0].float().cpu().double().numpy() for t in (k, v))
+    for i in (0, 1, 39, 40, 1999, 4463, 4464, 35000, 65535, 65536, n - 1):
+        want, _, _, (spread, size) = kv_ops.attend(kh, vh, table.numpy(), 1, max(0, i - window + 1), i + 1,
+                                                   q[i].float().cpu().double().numpy(), 0.125)
+        slack = attn_slack(size, 64, 2 * window)
+        tol = 2.0 ** -8 * np.abs(want) + (slack[:, None] + 2.0 ** -8) * (1 + 2.0 ** -8) * spread
+        assert (np.abs(out[i].float().cpu().double().numpy() - want) <= tol).all(), i
+
+
+def test_chunk_begins_past_every_place():
+    """A first visible place at the end of the int32 range: rows that see nothing, no weights."""
+    c = make_cache(2, [300, 40], None, 2, 64, 16)
+    begins, c.begins = c.begins, [2 ** 31 - 1, 41]
+    pool, q, out, lse, sc = chunk_call(c, [200, 40], 2, late=200)
+    assert not out.float().any() and torch.isneginf(lse).all() and torch.equal(pool.mass.cpu(), c.mass)
+    assert int(pool.err_word.item()) == 0
+    pool, q, out, lse, sc = chunk_call(c, [200, 40], 2, window=2 ** 31 - 1, late=2 ** 31 - 1)
+    assert not out.float().any() and torch.equal(pool.mass.cpu(), c.mass)
+    c.begins = begins
+    pool, q, out, lse, sc = chunk_call(c, [200, 40], 2, window=2 ** 31 - 1, late=2 ** 31 - 1)
+    check_chunk(c, [200, 40], q, sc, out, lse, 0, 200, pool.mass)
+
+
 def test_chunk_scores_that_are_not_finite():
     """-inf scores leave a place out, rows of nothing else are empty, +inf makes a row NaN."""
     c = nan_free(make_cache(3, [40, 40, 40], None, 1, 64, 8))
@@ -616,7 +697,8 @@ def run_release(pool, table, free, n_free, slots, lens, keep, in_place=False):
 
 
 @pytest.mark.parametrize("B,page,hi", [(1, 16, 0), (1, 16, 5000), (9, 1, 70), (64, 16, 3000), (33, 64, 64),
-                                       (1100, 32, 90), (3, 1024, 9000)])
+                                       (1100, 32, 90), (3, 1024, 9000), (1100, 16, 200),
+                                       (2, 1, 3000)])
 def test_release(B, page, hi):
     r = np.random.default_rng(B + page)
     lens = [int(x) for x in r.integers(0, hi + 1, size=B)]
