@@ -61,6 +61,7 @@ struct ChunkDev {
   ChunkArgs a;
   int group, tiles;
   int parts, piece; // a tile's blocks are divided into pieces of this many; at most `parts`
+  int spread;       // whether a tile's pieces go to different XCDs
   float c;          // |scale * k_scale| in log2 units
   uint32_t flip, keep;  // for two bf16 queries: the scale's sign, and 0 if it is 0 (c is 1 then)
   uint32_t inverse;     // ceil(2^32 / group), for a group of 2 or more
@@ -243,7 +244,9 @@ void attn_prefill_kernel(ChunkArgsAll) {
   const ChunkDev p = args->p;
   // (tiles in both of the grid's last two dimensions where none is divided)
   const int h = blockIdx.x, part = p.parts > 1 ? int(blockIdx.z) : 0;
-  const int tile = p.tiles - 1 - int(blockIdx.y + (p.parts > 1 ? 0 : blockIdx.z * kMostTiles));
+  int order = int(blockIdx.y) + (p.parts > 1 ? (p.spread ? part : 0) : int(blockIdx.z) * kMostTiles);
+  if (p.spread && order >= p.tiles) order %= p.tiles;
+  const int tile = p.tiles - 1 - order;
   if (tile < 0) return;
   const int b = last_request(p, [&](int b, int cu) { return ((int64_t(cu) * p.group) >> kRowBits) + b <= tile; });
   const Chunk ch = chunk_of(g, p, tile, b, h == 0 && part == 0 && threadIdx.x == 0);
@@ -928,7 +931,7 @@ int64_t chunk_tiles(int batch, int tokens, int group) { return int64_t(tokens) *
 // How a call's tiles are divided.
 struct ChunkPlan {
   int64_t tiles;
-  int parts, piece;
+  int parts, piece, spread;
   size_t o, ml, lse;  // parts of the workspace, in order
 };
 ChunkPlan chunk_plan(const gdn_kv_pool *p, int batch, int tokens, int q_heads, int max_len, int mass_tokens) {
@@ -939,18 +942,27 @@ ChunkPlan chunk_plan(const gdn_kv_pool *p, int batch, int tokens, int q_heads, i
   const int most = max_len / KT + 1;  // blocks of a tile
   constexpr int64_t slots = 2 * kCUs;
   // As if all requests were alike (the host knows no more).  With as many tiles as workgroups that
-  // run at once none is divided.  Fewer are divided into as many pieces as fill the compute units: once
-  // where all tiles see about as many places (by the bound), a little or half more often where lengths
-  // differ or a tile sees half as many on the average, as the short ones leave room.  A piece has 4
-  // blocks or more.
-  const int64_t each = (int64_t(tokens) + batch - 1) / batch, tiles = batch * ((each * group + kRows - 1) / kRows);
-  const int64_t units = tiles * p->d.kv_heads;
-  if (units < slots) {
-    const bool rising = each > max_len / 2;
-    const int64_t want = rising ? (3 * slots / 2 + units - 1) / units : (batch > 1 ? 23 * slots / 20 : slots) / units;
-    r.parts = int(std::min<int64_t>(want, most / 4));
+  // run at once, none is divided: further pieces gain nothing (6144 tokens, 8 by 2 heads of 256: 345 us
+  // whole, 412 in two pieces).  Fewer are, so that the pieces fill the compute units: once for one
+  // request whose tiles all see about as many places, half more often where lengths differ or the
+  // first tiles see few places (1024 tokens: 52 us whole, 45 in six, 56 in nine), and more often yet where
+  // pieces stay long (25 requests of up to 30000: 476 us in two, 254 in ten, 263 in twenty).  A piece
+  // takes some 5 us more than its blocks and the join 5 to 10, so there are at least 4 blocks to a
+  // piece, 7 of several requests, and short lists stay whole (4 requests of up to 333: 26 us, 37 in two).
+  const int64_t each = (int64_t(tokens) + batch - 1) / batch, own = (each * group + kRows - 1) / kRows;
+  const int64_t units = batch * own * p->d.kv_heads;
+  if (units < slots && most >= 16) {
+    const int64_t half_more = (3 * slots / 2 + units - 1) / units;
+    int64_t want = slots / units, limit = most / 4;
+    if (2 * each > max_len) want = half_more;
+    else if (batch > 1) want = std::max(half_more, std::min(4 * slots / units, int64_t(most / 48))), limit = most / 7;
+    r.parts = int(std::min(want, limit));
   }
   r.parts = std::max(1, r.parts);
+  // Pieces of one tile would all run on the XCDs that its number gives (of lists that differ in
+  // length some XCDs would have the long ones: 110 against 77 us for 32 requests of up to 8192), which
+  // is as well where a request has many tiles that read the same keys (1.1 against 1.7 ms for 32 tiles).
+  r.spread = r.parts > 1 && own == 1;
   r.piece = (most + r.parts - 1) / r.parts;
   r.parts = (most + r.piece - 1) / r.piece;
   if (r.parts > 1) {
@@ -1019,6 +1031,7 @@ hipError_t launch_attn_prefill(const gdn_kv_pool *pool, int layer, const ChunkAr
   p.tiles = int(w.tiles);
   p.parts = w.parts;
   p.piece = w.piece;
+  p.spread = w.spread;
   p.c = fabsf(a.scale) * pool->d.k_scale * kLog2e;
   p.flip = std::signbit(a.scale) ? 0x80008000u : 0u;
   p.keep = p.c == 0.f ? 0u : ~0u;  // (a score of -inf must stay -inf where it is multiplied by c)
