@@ -232,7 +232,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2)))
 void attn_prefill_kernel(ChunkArgsAll) {
   using T = Tile<D, kF8>;
   constexpr int KT = T::KT, KB = KT / 32, KS = D / 16, DB = D / 32, NL = T::kLoads;
-  constexpr int kAhead = D == 256 ? 3 : 4;  // fragments asked for before they are used
+  constexpr int kAhead = 3;  // fragments asked for before they are used (4 and 6 are the same where registers allow)
   extern __shared__ __attribute__((aligned(16))) char lds[];
   const args_t args = (args_t)__builtin_amdgcn_kernarg_segment_ptr();
   // a block (by its number's parity) that has a page outside the pool
@@ -494,6 +494,8 @@ void attn_prefill_kernel(ChunkArgsAll) {
       bf16x8 ring[kAhead];
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) ring[i] = kread(i);
+      // a wave in its products goes before one in its softmax (2 to 3 % in all)
+      __builtin_amdgcn_s_setprio(1);
       // the next block's loads go out between the products, whose issue they do not hold up
       constexpr int kEvery = KS * KB / (2 * NL);  // products between two loads
       bool bad = false;
@@ -512,6 +514,7 @@ void attn_prefill_kernel(ChunkArgsAll) {
           }
         }
       }
+      __builtin_amdgcn_s_setprio(0);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) ring[i] = vread(i);
@@ -571,6 +574,7 @@ void attn_prefill_kernel(ChunkArgsAll) {
           sum[e & 3] += s[kb][e];
         }
       l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      __builtin_amdgcn_s_setprio(1);
 #pragma unroll
       for (int ks = 0; ks < 2 * KB; ++ks) {
         u32x4 w;
@@ -587,6 +591,7 @@ void attn_prefill_kernel(ChunkArgsAll) {
           if (i + kAhead < 2 * KB * DB) ring[i % kAhead] = vread(i + kAhead);
         }
       }
+      __builtin_amdgcn_s_setprio(0);
       if constexpr (kTwoSteps) {
         if (edge || kind != kAsIs) [[unlikely]] change_raw(next, kind);
         put(vraw, lds + ((t + 1) & 1) * 2 * T::kBytes + T::kBytes);
