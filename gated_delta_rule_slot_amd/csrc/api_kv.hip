@@ -448,7 +448,7 @@ GDN_API gdn_status rope_append(gdn_kv_pool_t pool, int32_t layer, int32_t n, con
               {"position", {position, 1, n * int64_t(4), n * int64_t(4)}}, {"freqs", {freqs, 1, rot_dim * 4, rot_dim * 4}},
               {"err_word", {pool->d.err_word, 1, 4, 4}}};
     for (const auto &x : in) {
-      if (x.rows.base == q && q_out == q && q_out_stride == q_stride) continue;
+      if (&x == in && q_out == q && q_out_stride == q_stride) continue;  // in place
       const bool meet = x.rows.n == 1 && x.rows.row == x.rows.stride ? overlap(to, x.rows.base, x.rows.row)
                                                                      : rows_meet(to, x.rows);
       if (meet) return fail(GDN_ERR_ARG, "q_out overlaps %s", x.name);

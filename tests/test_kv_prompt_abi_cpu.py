@@ -181,6 +181,9 @@ def test_release_refuses_overlaps(pool, written, size, other, bytes_):
     # the projection's rows [q | k | v], turned in place: k one vector too early
     dict(q=P, q_out=P, qs=512, qos=512, k=P + 512 - 16, ks=512, v=P + 768, vs=512),
     dict(q=P, q_out=P, qs=512, qos=512, k=P + 512, ks=512, v=P + 768 + 16, vs=512),
+    # keys or values in the place of the queries that are turned
+    dict(q_out=ROPE["q"], k=ROPE["q"]), dict(q_out=ROPE["q"], k=ROPE["q"], ks=256),
+    dict(q_out=ROPE["q"], v=ROPE["q"], vs=256),
     # other strides within the same range
     dict(q=P, q_out=P, qs=512, qos=512, k=P + 512, ks=256, v=P + 768, vs=512),
 ])
