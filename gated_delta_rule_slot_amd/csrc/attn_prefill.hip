@@ -2,9 +2,9 @@
 // (formulas: include/gdn_kv.h).
 //
 // The query heads of one key-value head read the same keys, so a request's rows of one
-// key-value head are (new token, head of the group), token by token, and a workgroup takes
-// kRows of them over tiles of KT places.  4 D flops for every (row, place): bound by the
-// matrix units, or, for few rows, by the reading of the cache.
+// key-value head are (new token, head of the group), token by token.  A tile has kRows of them, 32 of
+// each wave of a workgroup, which walks over blocks of KT places.  4 D flops for every (row, place):
+// bound by the matrix units, or, for few rows, by the reading of the cache.
 //
 //   S^T = K Q^T   A = keys (rows = places), B = queries (columns = rows of the call).  A lane
 //                 gets, for row c = lane % 32 and half h = lane / 32, the scores of places
@@ -15,7 +15,13 @@
 // The row is the lane's column in both products, so the softmax's m and l are lane-local and
 // only the maximum crosses the halves.  Queries stay in registers.  Keys and values go from
 // memory to shared memory without passing registers (bf16; e4m3 is converted on its way), one
-// tile ahead, with one barrier a tile.
+// block ahead, with one barrier a block; their loads are issued between the products, and a wave in
+// its products goes before one in its softmax.
+//
+// Two workgroups run on a compute unit (256 registers a lane, 64 KB), one in its products while the
+// other is in its softmax: heads of 256 need O, the queries and 32 scores a row at once, which is why
+// KT is 32 there.  A single spilled register in the walk waits for all loads behind it (456 instead
+// of 345 us for a 6144-token prompt), so what the walk does not need is worked out again behind it.
 //
 // The exponent's reference m follows the running maximum only where that has grown by more
 // than 2^8 (a wave's common decision), so O is rarely rescaled: weights are at most 2^8 then,
@@ -23,6 +29,13 @@
 // the product (their sum l is not): an error of at most 2^-8 of a weighted mean of |v|, about as
 // large as the output's own rounding.  Two bf16 parts would take half as many matrix
 // instructions again.
+//
+// Measured on MI355X (a matrix product of 8192^3 runs at 1338 TFLOP/s there): one prompt of 24576
+// tokens 1050-1070 TFLOP/s with heads of 256, 1025 of 128 and 900 of 64 (whose softmax takes as long as
+// its products), from an e4m3 cache 955, 1015 and 830; 512 tokens behind 131072 1.05-1.11 ms, 1000-1050
+// TFLOP/s; 6144 tokens 335-355 us, 870-930 (the last tiles run alone); 32 requests of 1 to 7 tokens
+// over 500 to 8192: 75 us, 3.7 TB/s.  The matrix units are busy for half of the time that the compute
+// units are.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -788,8 +801,9 @@ void attn_prefill_mass_kernel(KvGeom g, ChunkDev p, int blocks) {
   const table_t cu = (table_t)p.a.cu_seqlens;
   const int bos = cu[b], eos = cu[b + 1], slot = ((table_t)p.a.slot_table)[b], len = ((table_t)p.a.kv_len)[b];
   const int begin = p.a.kv_begin ? ((table_t)p.a.kv_begin)[b] : 0;
+  if (bos < 0 || eos <= bos || eos > p.a.tokens) return;
   const int n = eos - bos;
-  if (bos < 0 || n <= 0 || eos > p.a.tokens || slot <= 0 || slot >= g.slots || len < n || len > p.a.max_len || begin < 0)
+  if (slot <= 0 || slot >= g.slots || len < n || len > p.a.max_len || begin < 0)
     return;
   const int late = min(n, p.a.mass_tokens);   // queries that count
   const int place0 = len - n, first = n - late;

@@ -213,8 +213,8 @@ enum { GDN_ERRW_NO_PAGES = 32 };
  * free_pages  device int32 [free_capacity]: the first n_free[0] entries are free pages
  * n_free      device int32 [1];  n_free_out: device int32 [1], may be n_free
  * The running sums of max(new_len, 0), limited to max_tokens, go to cu_seqlens [batch + 1].
- * A request is served if its slot is live (slots must be distinct), no number is negative,
- * kv_len + new_len is at most max_pages * page_size, its tokens end within max_tokens, its
+ * A request is served if its slot is live (slots must be distinct), its kv_len and new_len are not
+ * negative, kv_len + new_len is at most max_pages * page_size, its tokens end within max_tokens, its
  * positions below 2^31 (else GDN_ERRW_BAD_SEQLENS), and the pages that it and all such requests
  * before it lack are at most n_free, or it lacks none (else GDN_ERRW_NO_PAGES).  What it lacks,
  * entries ceil(kv_len / page_size) ... of its row of the pool's page table (which is written,
@@ -331,9 +331,9 @@ gdn_status attn_prefill_workspace_bytes(gdn_kv_pool_t pool, int32_t batch, int32
  * word) must not overlap what it reads or each other.
  * A token that sees nothing (its request is skipped, or no place is visible, or every score is -inf)
  * gets out = 0 and lse = -inf and adds no weight.  Places that a token does not see never reach its
- * result, whatever their rows hold (a chunk with NaN or infinite values is walked twice).  Infinite
- * values and scores, and the range of the values' sum, are as in attn_decode_paged.  Weights are
- * rounded to bf16 for the product with the values.  The result does not depend on the order in
+ * result, whatever their rows hold (128 rows that meet NaN or infinite values are walked four times).
+ * Infinite values and scores, and the range of the values' sum, are as in attn_decode_paged.  Weights
+ * are rounded to bf16 for the product with the values.  The result does not depend on the order in
  * which the workgroups run. */
 gdn_status attn_prefill_paged(gdn_kv_pool_t pool, int32_t layer, int32_t batch, int32_t tokens,
                               int32_t q_heads, int32_t max_len, const int32_t *cu_seqlens,
