@@ -754,6 +754,100 @@ def test_maps_in_a_graph_count_on():
 
 
 # ---------------------------------------------------------------------- together --
+class Steps:
+    """A layer's decode steps with buffers of their own, all of it on the device: lengths, positions
+    and the free list go on from step to step.  With 600 pages a request the attention divides its places."""
+
+    def __init__(self, page=4, B=5, H=2, G=3, dim=64, most=60):
+        import gated_delta_rule_slot_amd as gdn
+
+        self.gdn, self.cap, self.scale = gdn, most * page, dim ** -0.5
+        g = torch.Generator().manual_seed(7)
+        pages = 1 + B * most // 2
+        k = torch.full((1, pages, H, page, dim), float("nan"), dtype=torch.bfloat16, device="cuda")
+        self.pool = gdn.kv_pool_create(k, k.clone(), torch.zeros(B + 1, most, dtype=torch.int32, device="cuda"),
+                                       err_word=i32([0]))
+        self.free, self.n_free = i32(list(range(pages - 1, 0, -1))), i32([pages - 1])
+        self.slots, self.lens, self.nxt = i32([3, 1, 5, 2, 4]), i32([0] * B), i32([0, 9, 100, 7, 1])
+        self.new = i32([1, 2, 0, 3, 1])
+        T = 9
+        self.x = torch.randn(T, (H * G + 2 * H) * dim, generator=g).to(torch.bfloat16).cuda()
+        self.q, self.k, self.v = (t.view(T, -1, dim) for t in self.x.split([H * G * dim, H * dim, H * dim], dim=1))
+        self.cu, self.so = i32([0] * (B + 1)), i32([0] * B)
+        self.ts, self.ti, self.tp = (i32([0] * T) for _ in range(3))
+        self.qr, self.out = (torch.zeros(T, H * G, dim, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        f, self.amp = gdn.rope_frequencies(32)
+        self.freqs = f.cuda()
+        n = gdn.attn_prefill_workspace_bytes(self.pool, B, T, H * G, self.cap)
+        self.ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+
+    def step(self, stream=None):
+        self.gdn.kv_batch_map(self.pool, self.slots, self.lens, self.free, self.n_free, self.cu, self.so, self.lens,
+                              self.ts, self.ti, new_len=self.new, next_pos=self.nxt, next_pos_out=self.nxt,
+                              token_pos=self.tp, stream=stream)
+        self.gdn.rope_append(self.pool, 0, self.ts, self.ti, self.tp, self.q, self.qr, self.k, self.v, self.freqs,
+                             amplitude=self.amp, stream=stream)
+        self.gdn.attn_prefill_paged(self.pool, 0, self.cu, self.so, self.lens, self.qr, self.out, self.cap,
+                                    scale=self.scale, workspace=self.ws, stream=stream)
+
+    def release(self, stream=None):
+        self.gdn.kv_release(self.pool, self.slots, self.lens, self.free, self.n_free, stream=stream)
+
+    def state(self):
+        torch.cuda.synchronize()
+        return [t.clone() for t in (self.lens, self.nxt, self.n_free, self.free, self.pool.page_table, self.ts, self.ti,
+                                    self.tp, self.cu, self.so, self.qr, self.out, self.pool.err_word)]
+
+
+def same(a, b):
+    for i, (x, y) in enumerate(zip(a, b)):
+        assert torch.equal(x, y), i
+
+
+@pytest.mark.parametrize("most", [60, 600])
+def test_whole_steps_replayed(most):
+    """Steps of map, append and attention, captured once, replayed with eager work between: every
+    replay's state and outputs are those of eager steps on another pool."""
+    a, b = Steps(most=most), Steps(most=most)
+    assert (a.ws.numel() > 0) == (most == 600)
+    graph = torch.cuda.CUDAGraph()
+    start = [t.clone() for t in (a.lens, a.nxt, a.n_free, a.pool.page_table)]
+    a.step()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        a.step()
+    for t, s in zip((a.lens, a.nxt, a.n_free, a.pool.page_table), start):
+        t.copy_(s)
+    for _ in range(12):
+        x = torch.randn_like(a.x)
+        a.x.copy_(x), b.x.copy_(x)
+        graph.replay()
+        b.step()
+        same(a.state(), b.state())
+    assert a.out.float().abs().sum() > 0 and a.lens.tolist() == [12, 24, 0, 36, 12]
+    a.release(), b.release()
+    same(a.state(), b.state())
+    assert not a.pool.page_table.any()
+
+
+@pytest.mark.parametrize("most", [60, 600])
+def test_steps_on_streams_at_once(most):
+    """Two pools' steps on streams of their own, neither the current one, running at the same time."""
+    want = Steps(most=most)
+    for _ in range(10):
+        want.step()
+    want.release()
+    got, streams = [Steps(most=most), Steps(most=most)], [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for s, st in zip(got, streams):
+            s.step(stream=st)
+    for s, st in zip(got, streams):
+        s.release(stream=st)
+    for s in got:
+        same(s.state(), want.state())
+
+
 @pytest.mark.parametrize("f8,dim,rot,adjacent", [(False, 128, 128, False), (True, 64, 32, True), (False, 256, 64, False)])
 def test_prompts_then_decode_follow_a_host_model(f8, dim, rot, adjacent):
     """Prompts in chunks, then decode steps, eviction and the release of pages, all tables made on
