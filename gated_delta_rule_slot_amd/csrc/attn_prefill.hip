@@ -2,8 +2,8 @@
 // (formulas: include/gdn_kv.h).
 //
 // The query heads of one key-value head read the same keys, so a request's rows of one
-// key-value head are (new token, head of the group), token by token.  A tile has kRows of them, 32 of
-// each wave of a workgroup, which walks over blocks of KT places.  4 D flops for every (row, place):
+// key-value head are (new token, head of the group), token by token.  A tile has 128 of them, 32 of
+// each wave of a workgroup, or twice as many, and is walked over in blocks of KT places.  4 D flops for every (row, place):
 // bound by the matrix units, or, for few rows, by the reading of the cache.
 //
 //   S^T = K Q^T   A = keys (rows = places), B = queries (columns = rows of the call).  A lane
@@ -55,7 +55,7 @@ constexpr float kLn2 = 0.693147180559945309417f;
 constexpr float kNegInf = -__builtin_inff();
 constexpr float kGrowth = 8.f;  // log2 of how far the maximum may pass the reference
 
-constexpr int kRowBits = 7, kRows = 1 << kRowBits;  // rows of a tile, 32 of each wave
+constexpr int kRowBits = 7;  // a tile has 2^7 rows, 32 of each wave, or 2^8, 64 of each
 
 constexpr int kMostTiles = 32768;  // in one dimension of the grid
 
@@ -73,6 +73,7 @@ typedef const int32_t GDN_CONSTANT *table_t;
 struct ChunkDev {
   ChunkArgs a;
   int group, tiles;
+  int bits;         // a tile has 2^bits rows
   int parts, piece; // a tile's blocks are divided into pieces of this many; at most `parts`
   int spread;       // whether a tile's pieces go to different XCDs
   float c;          // |scale * k_scale| in log2 units
@@ -133,7 +134,7 @@ __device__ __forceinline__ uint32_t sorted_f8(uint32_t x, int kind) {
 __device__ __forceinline__ float beyond(float sum, int kind) { return sum + (kind == kUp ? -kNegInf : kNegInf); }
 
 // ---- which rows a tile has -------------------------------------------------
-// The tiles of request b begin at cu[b] * group / kRows + b: at least as many as it needs, and
+// The tiles of request b begin at cu[b] * group / 2^bits + b: at least as many as it needs, and
 // found from cu alone, so that no list of tiles has to be made first.
 struct Chunk {
   int bos, n, rows0;     // the request's first token and number of tokens, the tile's first row
@@ -162,7 +163,7 @@ __device__ __forceinline__ Chunk chunk_of(const KvGeom &g, const ChunkDev &p, in
   Chunk r;
   r.bos = cu[b];
   const int eos = cu[b + 1];
-  const int64_t at = (tile - ((int64_t(r.bos) * p.group) >> kRowBits) - b) * kRows;
+  const int64_t at = (tile - ((int64_t(r.bos) * p.group) >> p.bits) - b) << p.bits;
   const bool ok = r.bos >= 0 && eos >= r.bos && eos <= p.a.tokens;
   r.n = ok ? eos - r.bos : 0;
   r.any = ok && at >= 0 && at < int64_t(r.n) * p.group;
@@ -197,7 +198,7 @@ template <int KT>
 __device__ __forceinline__ Span span_of(const ChunkDev &p, const Chunk &ch) {
   if (!ch.live) return Span{0, 0};
   const int all = ch.n * p.group, place0 = ch.len - ch.n;
-  const int first = place0 + token_of(p, ch.rows0), last = place0 + token_of(p, min(ch.rows0 + kRows - 1, all - 1));
+  const int first = place0 + token_of(p, ch.rows0), last = place0 + token_of(p, min(ch.rows0 + (1 << p.bits) - 1, all - 1));
   const int lo = seen_from(p, ch.begin, first) / KT;
   return Span{lo, max(0, last / KT + 1 - lo)};
 }
@@ -240,7 +241,8 @@ __device__ __forceinline__ args_t fresh(args_t a) {
 // A workgroup has one piece of one tile's blocks, for one key-value head.  The first pieces come
 // first, and of them those of a request's last tiles, which see the most places: workgroups that
 // run at the same time read the same keys, and the last ones to start are short.
-template <int D, bool kF8, bool kWide>
+// R: 32 R rows of each wave.
+template <int D, bool kF8, bool kWide, int R>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(2)))
 void attn_prefill_kernel(ChunkArgsAll) {
   using T = Tile<D, kF8>;
@@ -261,7 +263,7 @@ void attn_prefill_kernel(ChunkArgsAll) {
   if (p.spread && order >= p.tiles) order %= p.tiles;
   const int tile = p.tiles - 1 - order;
   if (tile < 0) return;
-  const int b = last_request(p, [&](int b, int cu) { return ((int64_t(cu) * p.group) >> kRowBits) + b <= tile; });
+  const int b = last_request(p, [&](int b, int cu) { return ((int64_t(cu) * p.group) >> p.bits) + b <= tile; });
   const Chunk ch = chunk_of(g, p, tile, b, h == 0 && part == 0 && threadIdx.x == 0);
   if (!ch.any) return;
   const Span span = span_of<KT>(p, ch);
@@ -270,24 +272,28 @@ void attn_prefill_kernel(ChunkArgsAll) {
   const int t0 = span.lo + part * p.piece, t1 = min(span.lo + span.n, t0 + p.piece);
 
   const int all = ch.n * p.group;
-  const int row0 = ch.rows0 + 32 * wave;
+  const int row0 = ch.rows0 + 32 * R * wave;
   const bool wlive = ch.live && row0 < all;
   const int place0 = ch.len - ch.n;  // of the first new token
-  const int row = min(row0 + c, all - 1);  // (rows behind the last repeat it and are not stored)
-  const int token = token_of(p, row), place = place0 + token;
-  const int wfirst = place0 + token_of(p, min(row0, all - 1)), wlast = place0 + token_of(p, min(row0 + 31, all - 1));
+  int place[R];
+  const int wfirst = place0 + token_of(p, min(row0, all - 1));
+  const int wlast = place0 + token_of(p, min(row0 + 32 * R - 1, all - 1));
   const int wfrom = seen_from(p, ch.begin, wfirst), wfrom_last = seen_from(p, ch.begin, wlast);
 
-  bf16x8 q[KS];
-  if (wlive && t0 < t1) {
-    const int head = h * p.group + (row - token * p.group);
+  bf16x8 q[R][KS];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int row = min(row0 + 32 * r + c, all - 1);  // (rows behind the last repeat it and are not stored)
+    const int token = token_of(p, row), head = h * p.group + (row - token * p.group);
+    place[r] = place0 + token;
+    if (!wlive || t0 >= t1) continue;
     const uint16_t *src = p.a.q + (ch.bos + token) * p.a.q_stride + int64_t(head) * D + 8 * half;
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
       u32x4 w = *reinterpret_cast<const u32x4 *>(src + 16 * s);
 #pragma unroll
       for (int i = 0; i < 4; ++i) w[i] = (w[i] ^ p.flip) & p.keep;
-      q[s] = __builtin_bit_cast(bf16x8, w);
+      q[r][s] = __builtin_bit_cast(bf16x8, w);
     }
   }
 
@@ -428,13 +434,16 @@ void attn_prefill_kernel(ChunkArgsAll) {
   const int kaddr = c * T::RB + ((half ^ twist<D>(c)) << 4);
   const int vaddr = vrow * T::RB + ((vpair ^ twist<D>(vrow)) << 4) + 8 * (lane & 1) + T::kBytes;
 
-  f32x16 o[DB];
-  float m, l;
+  f32x16 o[R][DB];
+  float m[R], l[R];
   auto walk = [&](int kind) {
 #pragma unroll
-    for (int b = 0; b < DB; ++b) o[b] = f32x16{};
-    m = kNegInf;
-    l = 0.f;
+    for (int r = 0; r < R; ++r) {
+#pragma unroll
+      for (int b = 0; b < DB; ++b) o[r][b] = f32x16{};
+      m[r] = kNegInf;
+      l[r] = 0.f;
+    }
     __syncthreads();  // (the last walk's blocks have been read)
     if (threadIdx.x < 2) sbad[threadIdx.x] = -1;
     __syncthreads();
@@ -482,9 +491,11 @@ void attn_prefill_kernel(ChunkArgsAll) {
       arrive(t);
       const int p0 = t * KT;
       const int next = min(t + 1, t1 - 1);  // (the last block is asked for again: no branch among the products)
-      f32x16 s[KB];
+      f32x16 s[R][KB];
 #pragma unroll
-      for (int kb = 0; kb < KB; ++kb) s[kb] = f32x16{};
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) s[r][kb] = f32x16{};
       int ka = kaddr + (t & 1) * 2 * T::kBytes, va = vaddr + (t & 1) * 2 * T::kBytes;
       asm volatile("" : "+v"(ka), "+v"(va));  // (addresses are worked out here, not kept over the walk)
       auto kread = [&](int i) {
@@ -515,7 +526,8 @@ void attn_prefill_kernel(ChunkArgsAll) {
 #pragma unroll
       for (int i = 0; i < KS * KB; ++i) {
         __builtin_amdgcn_sched_barrier(0);
-        s[i % KB] = mfma32(ring[i % kAhead], q[i / KB], s[i % KB]);
+#pragma unroll
+        for (int r = 0; r < R; ++r) s[r][i % KB] = mfma32(ring[i % kAhead], q[r][i / KB], s[r][i % KB]);
         if (i + kAhead < KS * KB) ring[i % kAhead] = kread(i + kAhead);
         if (!kTwoSteps && i % kEvery == 0) {
           const int j = i / kEvery / 2;
@@ -543,14 +555,17 @@ void attn_prefill_kernel(ChunkArgsAll) {
       }
       const bool flagged = uniform(flag) == t;
       if (p0 < wfrom_last || p0 + KT - 1 > wfirst || flagged) [[unlikely]] {  // seen in part
-        const int from = seen_from(p, ch.begin, place);
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
+        for (int r = 0; r < R; ++r) {
+          const int from = seen_from(p, ch.begin, place[r]);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int at = p0 + 32 * kb + 8 * (e >> 2) + 4 * half + (e & 3);
-            if (at > place || at < from) s[kb][e] = kNegInf;
-          }
+          for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int at = p0 + 32 * kb + 8 * (e >> 2) + 4 * half + (e & 3);
+              if (at > place[r] || at < from) s[r][kb][e] = kNegInf;
+            }
+        }
         if (flagged) {
 #pragma unroll
           for (int kb = 0; kb < KB; ++kb)
@@ -558,49 +573,60 @@ void attn_prefill_kernel(ChunkArgsAll) {
             for (int e = 0; e < 16; ++e) {
               const int at = p0 + 32 * kb + 8 * (e >> 2) + 4 * half + (e & 3);
               const int id = g.page_table[int64_t(ch.slot) * g.max_pages + (min(at, ch.len - 1) >> g.page_shift)];
-              if (id <= 0 || id >= g.pages) s[kb][e] = kNegInf;
+              if (id <= 0 || id >= g.pages) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) s[r][kb][e] = kNegInf;
+              }
             }
         }
       }
-      float top = s[0][0];
 #pragma unroll
-      for (int kb = 0; kb < KB; ++kb)
+      for (int r = 0; r < R; ++r) {
+        float top = s[r][0][0];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) top = fmaxf(top, s[kb][e]);
-      top = halves_max(top) * p.c;
-      if (__any(top > m + kGrowth)) {
-        const float to = fmaxf(m, top), f = fexp2(m - ref(to));
-        l *= f;
+        for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-        for (int b = 0; b < DB; ++b)
+          for (int e = 0; e < 16; ++e) top = fmaxf(top, s[r][kb][e]);
+        top = halves_max(top) * p.c;
+        if (__any(top > m[r] + kGrowth)) {
+          const float to = fmaxf(m[r], top), f = fexp2(m[r] - ref(to));
+          l[r] *= f;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[b][e] *= f;
-        m = to;
-      }
-      const float mr = ref(m);
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          for (int b = 0; b < DB; ++b)
 #pragma unroll
-      for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          s[kb][e] = fexp2(fmaf(s[kb][e], p.c, -mr));
-          sum[e & 3] += s[kb][e];
+            for (int e = 0; e < 16; ++e) o[r][b][e] *= f;
+          m[r] = to;
         }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        const float mr = ref(m[r]);
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            s[r][kb][e] = fexp2(fmaf(s[r][kb][e], p.c, -mr));
+            sum[e & 3] += s[r][kb][e];
+          }
+        l[r] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      }
       __builtin_amdgcn_s_setprio(1);
 #pragma unroll
       for (int ks = 0; ks < 2 * KB; ++ks) {
-        u32x4 w;
+        bf16x8 pf[R];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          w[i] = cvt_pk_bf16(s[ks >> 1][8 * (ks & 1) + 2 * i], s[ks >> 1][8 * (ks & 1) + 2 * i + 1]);
-        const bf16x8 pf = __builtin_bit_cast(bf16x8, w);
+        for (int r = 0; r < R; ++r) {
+          u32x4 w;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            w[i] = cvt_pk_bf16(s[r][ks >> 1][8 * (ks & 1) + 2 * i], s[r][ks >> 1][8 * (ks & 1) + 2 * i + 1]);
+          pf[r] = __builtin_bit_cast(bf16x8, w);
+        }
 #pragma unroll
         for (int b = 0; b < DB; ++b) {
           const int i = ks * DB + b;
           if (b == 0 && D == 256) asm volatile("" : "+v"(va));
           __builtin_amdgcn_sched_barrier(0);
-          o[b] = mfma32(ring[i % kAhead], pf, o[b]);
+#pragma unroll
+          for (int r = 0; r < R; ++r) o[r][b] = mfma32(ring[i % kAhead], pf[r], o[r][b]);
           if (i + kAhead < 2 * KB * DB) ring[i % kAhead] = vread(i + kAhead);
         }
       }
@@ -617,19 +643,19 @@ void attn_prefill_kernel(ChunkArgsAll) {
   };
 
   // ---- results ----
-  auto store = [&](int kind) {
-    int row = row0 + c;
+  auto store = [&](int kind, int r) {
+    int row = row0 + 32 * r + c;
     asm volatile("" : "+v"(row));
     const args_t again = fresh(args);
     const auto &p = again->p;
-    const float ln = halves_sum(l);
+    const float ln = halves_sum(l[r]);
     if (row >= ch.n * p.group) return;
     const int token = row / p.group;
     const int64_t orow = int64_t(ch.bos + token) * p.a.q_heads + h * p.group + (row - token * p.group);
     if (!whole) {
       const int64_t at = int64_t(part) * p.a.tokens * p.a.q_heads + orow;
       if (half == 0 && kind <= kFinite) {
-        p.ml[2 * at] = ln == 0.f ? kNegInf : m;
+        p.ml[2 * at] = ln == 0.f ? kNegInf : m[r];
         p.ml[2 * at + 1] = ln;
       }
       if (ln == 0.f) return;
@@ -638,7 +664,7 @@ void attn_prefill_kernel(ChunkArgsAll) {
       for (int b = 0; b < DB; ++b)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          f32x4 v = {o[b][4 * i], o[b][4 * i + 1], o[b][4 * i + 2], o[b][4 * i + 3]};
+          f32x4 v = {o[r][b][4 * i], o[r][b][4 * i + 1], o[r][b][4 * i + 2], o[r][b][4 * i + 3]};
           if (kind > kFinite) {
             const f32x4 old = ld4(to + 32 * b + 8 * i);
 #pragma unroll
@@ -649,7 +675,7 @@ void attn_prefill_kernel(ChunkArgsAll) {
       return;
     }
     if (p.lse && half == 0 && kind <= kFinite)
-      p.lse[orow] = ln == 0.f ? kNegInf : (m + __builtin_amdgcn_logf(ln)) * kLn2;
+      p.lse[orow] = ln == 0.f ? kNegInf : (m[r] + __builtin_amdgcn_logf(ln)) * kLn2;
     const float f = ln == 0.f ? 0.f : again->g.v_scale / ln;
     uint16_t *to = p.a.out + orow * D + 8 * half;
 #pragma unroll
@@ -660,11 +686,11 @@ void attn_prefill_kernel(ChunkArgsAll) {
         u32x4 w;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const uint32_t x = cvt_pk_bf16(o[b][8 * i + 2 * e] * f, o[b][8 * i + 2 * e + 1] * f);
-          const uint32_t y = cvt_pk_bf16(o[b][8 * i + 4 + 2 * e] * f, o[b][8 * i + 5 + 2 * e] * f);
-          const auto r = __builtin_amdgcn_permlane32_swap(x, y, false, false);
-          w[e] = r[0];
-          w[2 + e] = r[1];
+          const uint32_t x = cvt_pk_bf16(o[r][b][8 * i + 2 * e] * f, o[r][b][8 * i + 2 * e + 1] * f);
+          const uint32_t y = cvt_pk_bf16(o[r][b][8 * i + 4 + 2 * e] * f, o[r][b][8 * i + 5 + 2 * e] * f);
+          const auto both = __builtin_amdgcn_permlane32_swap(x, y, false, false);
+          w[e] = both[0];
+          w[2 + e] = both[1];
         }
         u32x4 *at = reinterpret_cast<u32x4 *>(to + 32 * b + 16 * i);
         if (kind > kFinite) {
@@ -688,9 +714,11 @@ void attn_prefill_kernel(ChunkArgsAll) {
       float bad = 0.f;
       if (wlive) {
 #pragma unroll
-        for (int b = 0; b < DB; ++b)
+        for (int r = 0; r < R; ++r)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) bad = fmaf(o[b][e], 0.f, bad);
+          for (int b = 0; b < DB; ++b)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) bad = fmaf(o[r][b][e], 0.f, bad);
       }
       // (flags: static shared memory would move the blocks off address 0)
       const bool any = __any(bad != 0.f);
@@ -703,7 +731,8 @@ void attn_prefill_kernel(ChunkArgsAll) {
         continue;
       }
     }
-    store(kind);
+#pragma unroll
+    for (int r = 0; r < R; ++r) store(kind, r);
     if (kind == kAsIs || kind == kDown) break;
     ++kind;
   }
@@ -729,7 +758,7 @@ __global__ __launch_bounds__(kThreads) void attn_prefill_join_kernel(KvGeom g, C
 #pragma unroll 1
   for (int head = first; head < min(first + heads, p.a.q_heads); ++head) {
     const int row = (token - bos) * p.group + head % p.group;
-    const int tile = int((int64_t(bos) * p.group) >> kRowBits) + b + (row >> kRowBits);
+    const int tile = int((int64_t(bos) * p.group) >> p.bits) + b + (row >> p.bits);
     const Chunk ch = chunk_of(g, p, tile, b, false);
     if (!ch.any) return;
     const int pieces = (span_of<Tile<D, false>::KT>(p, ch).n + p.piece - 1) / p.piece;
@@ -945,22 +974,23 @@ void attn_prefill_mass_kernel(KvGeom g, ChunkDev p, int blocks) {
 
 size_t pad256(size_t n) { return (n + 255) & ~size_t(255); }
 
-int64_t chunk_tiles(int batch, int tokens, int group) { return int64_t(tokens) * group / kRows + batch; }
+int64_t chunk_tiles(int batch, int tokens, int group, int bits = kRowBits) {
+  return ((int64_t(tokens) * group) >> bits) + batch;
+}
 
 // How a call's tiles are divided.
 struct ChunkPlan {
   int64_t tiles;
-  int parts, piece, spread;
+  int bits, parts, piece, spread;
   size_t o, ml, lse;  // parts of the workspace, in order
 };
 ChunkPlan chunk_plan(const gdn_kv_pool *p, int batch, int tokens, int q_heads, int max_len, int mass_tokens) {
   ChunkPlan r{};
   if (batch == 0 || tokens == 0) return r;
   const int KT = p->d.head_dim == 256 ? 32 : 64, group = q_heads / p->d.kv_heads;
-  r.tiles = chunk_tiles(batch, tokens, group);
   const int most = max_len / KT + 1;  // blocks of a tile
   constexpr int64_t slots = 2 * kCUs;
-  // As if all requests were alike (the host knows no more).  With as many tiles as workgroups that
+  // What follows is as if all requests were alike (the host knows no more).  With as many tiles as workgroups that
   // run at once, none is divided: further pieces gain nothing (6144 tokens, 8 by 2 heads of 256: 345 us
   // whole, 412 in two pieces).  Fewer are, so that the pieces fill the compute units: once for one
   // request whose tiles all see about as many places, half more often where lengths differ or the
@@ -968,8 +998,15 @@ ChunkPlan chunk_plan(const gdn_kv_pool *p, int batch, int tokens, int q_heads, i
   // pieces stay long (25 requests of up to 30000: 476 us in two, 254 in ten, 263 in twenty).  A piece
   // takes some 5 us more than its blocks and the join 5 to 10, so there are at least 4 blocks to a
   // piece, 7 of several requests, and short lists stay whole (4 requests of up to 333: 26 us, 37 in two).
-  const int64_t each = (int64_t(tokens) + batch - 1) / batch, own = (each * group + kRows - 1) / kRows;
+  const int64_t each = (int64_t(tokens) + batch - 1) / batch, own = ((each * group - 1) >> kRowBits) + 1;
   const int64_t units = batch * own * p->d.kv_heads;
+  // Tiles of twice the rows, where a wave has the registers for them, read shared memory half as often and
+  // convert e4m3 half as often (24576 tokens, 64 heads of 64: 4.98 instead of 5.4 ms, from e4m3 4.92 instead of 5.9;
+  // 4 e4m3 requests of 2048, 4096 tiles of 128 rows: 194 instead of 219 us), but half as many end less evenly
+  // (4 bf16 requests of 4096, 1536 tiles: 172 us instead of 154; 8 of them: 287 and 284).
+  const int64_t enough = p->d.kv_dtype == GDN_BF16 ? 4096 : 2048;
+  r.bits = kRowBits + (p->d.head_dim == 64 && units >= enough ? 1 : 0);
+  r.tiles = chunk_tiles(batch, tokens, group, r.bits);
   if (units < slots && most >= 16) {
     const int64_t half_more = (3 * slots / 2 + units - 1) / units;
     int64_t want = slots / units, limit = most / 4;
@@ -996,8 +1033,9 @@ ChunkPlan chunk_plan(const gdn_kv_pool *p, int batch, int tokens, int q_heads, i
 template <int D, bool kF8>
 hipError_t launch_dt(const KvGeom &g, const ChunkDev &p, hipStream_t s) {
   const bool wide = (1 << g.page_shift) >= 16;
-  const int64_t units = int64_t(p.tiles) * g.kv_heads;
-  const auto kernel = wide ? attn_prefill_kernel<D, kF8, true> : attn_prefill_kernel<D, kF8, false>;
+  auto kernel = wide ? attn_prefill_kernel<D, kF8, true, 1> : attn_prefill_kernel<D, kF8, false, 1>;
+  if constexpr (D == 64)
+    if (p.bits > kRowBits) kernel = wide ? attn_prefill_kernel<D, kF8, true, 2> : attn_prefill_kernel<D, kF8, false, 2>;
   constexpr int shared = Tile<D, kF8>::kShared;
   const dim3 grid(unsigned(g.kv_heads), unsigned(std::min(p.tiles, kMostTiles)),
                   unsigned(p.parts > 1 ? p.parts : (p.tiles + kMostTiles - 1) / kMostTiles));
@@ -1031,7 +1069,7 @@ bool chunk_fits(const gdn_kv_pool *p, int batch, int tokens, int q_heads, int ma
   const int64_t group = q_heads / p->d.kv_heads, limit = int64_t(1) << 31;
   const int64_t blocks = int64_t(max_len) / (kMassPlaces * kWaves) + 1;
   // rows of a request and tiles are counted in 31 bits, workgroups in 40
-  return int64_t(tokens) * group < limit - kRows && chunk_tiles(batch, tokens, int(group)) < limit / p->d.kv_heads &&
+  return int64_t(tokens) * group < limit - 256 && chunk_tiles(batch, tokens, int(group)) < limit / p->d.kv_heads &&
          int64_t(batch) * p->d.kv_heads < (int64_t(1) << 40) / blocks;
 }
 
@@ -1048,6 +1086,7 @@ hipError_t launch_attn_prefill(const gdn_kv_pool *pool, int layer, const ChunkAr
   const ChunkPlan w = chunk_plan(pool, a.batch, a.tokens, a.q_heads, a.max_len, a.mass_tokens);
   p.inverse = uint32_t(((uint64_t(1) << 32) + p.group - 1) / p.group);
   p.tiles = int(w.tiles);
+  p.bits = w.bits;
   p.parts = w.parts;
   p.piece = w.piece;
   p.spread = w.spread;

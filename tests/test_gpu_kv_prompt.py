@@ -238,6 +238,34 @@ def test_chunk_values_that_are_not_finite_in_divided_places(dim, group, f8):
     assert ((got - want).abs() <= 4 * 2.0 ** -8 * (want.abs() + 4))[free].all()
 
 
+@pytest.mark.parametrize("f8,page,window,late", [(False, 16, 0, 70), (True, 32, 0, 5), (False, 4, 90, 0),
+                                                 (True, 2, 90, 400), (False, 64, 1, 3)])
+def test_chunk_tiles_of_twice_the_rows(f8, page, window, late):
+    """So many heads of 64 that a tile has 256 rows: requests of one to a few hundred tokens, tiles and
+    waves filled in part, values that are not finite in one request."""
+    H, G, B, late_place = 64, 3 if f8 else 2, 33 if f8 else 65, 45
+    r = np.random.default_rng(page)
+    new = [300, 87, 0, 129] + [int(x) for x in r.integers(0, 6, size=B - 4)]
+    new[-1] = 1
+    cached = [20, 0, 9, 70] + [int(x) for x in r.integers(0, 40, size=B - 4)]
+    lens = [max(1, n + m) for n, m in zip(new, cached)]
+    begins = [int(r.integers(0, n)) if i % 5 == 3 else 0 for i, n in enumerate(lens)]
+    c = make_cache(page, lens, begins, H, 64, page, f8)
+    pool, q, clean, lse, sc = chunk_call(c, new, G, window, late, extra=2)
+    check_chunk(c, new, q, sc, clean, lse, window, late, pool.mass)
+    at = lens[0] - late_place
+    c.v[0, int(c.table[c.slots[0], at // page]), 7, at % page, 11] = float("nan") if f8 else float("inf")
+    pool, _, out, lse2, _ = chunk_call(c, new, G, window, late, q=q.cuda(), extra=2)
+    assert torch.equal(lse, lse2) and torch.isfinite(pool.mass).all()
+    first = 300 - late_place
+    hit = torch.zeros_like(out, dtype=torch.bool)
+    hit[first:min(300, first + window) if window else 300, 7 * G:8 * G, 11] = True
+    assert (torch.isnan(out[hit]) if f8 else torch.isposinf(out[hit])).all()
+    x, y = out[~hit].float(), clean[~hit].float()
+    assert ((x - y).abs() <= 4 * 2.0 ** -8 * (y.abs() + 4)).all()
+    assert int(pool.err_word.item()) == 0
+
+
 @pytest.mark.parametrize("batch,dim,group", [(65, 64, 1), (300, 128, 3), (5000, 64, 2)])
 def test_chunk_many_requests(batch, dim, group):
     """More requests than a wave has lanes, and than two steps of its search reach, some of them
