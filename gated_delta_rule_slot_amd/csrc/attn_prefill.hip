@@ -433,6 +433,10 @@ void attn_prefill_kernel(ChunkArgsAll) {
   const int vrow = 4 * half + ((lane >> 2) & 3), vpair = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
   const int kaddr = c * T::RB + ((half ^ twist<D>(c)) << 4);
   const int vaddr = vrow * T::RB + ((vpair ^ twist<D>(vrow)) << 4) + 8 * (lane & 1) + T::kBytes;
+  // a row of 512 bytes has twice the pieces that the twist permutes: steps and blocks of columns that
+  // differ by half of a row follow each other, and have their address in common
+  auto step_of = [](int i) { return D == 256 ? (i >> 1) + (i & 1) * (KS / 2) : i; };
+  auto block_of = [](int i) { return D == 256 ? (i >> 1) + (i & 1) * (DB / 2) : i; };
 
   f32x16 o[R][DB];
   float m[R], l[R];
@@ -496,17 +500,24 @@ void attn_prefill_kernel(ChunkArgsAll) {
       for (int r = 0; r < R; ++r)
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) s[r][kb] = f32x16{};
-      int ka = kaddr + (t & 1) * 2 * T::kBytes, va = vaddr + (t & 1) * 2 * T::kBytes;
+      // (the blocks' base in shared memory is a multiple of a row's bytes, so the twist's bits can be changed
+      // behind its addition)
+      typedef __attribute__((address_space(3))) char *lp;
+      uint32_t ka = uint32_t(uintptr_t((lp)lds)) + kaddr + (t & 1) * 2 * T::kBytes, va = ka - kaddr + vaddr;
       asm volatile("" : "+v"(ka), "+v"(va));  // (addresses are worked out here, not kept over the walk)
       auto kread = [&](int i) {
-        return *reinterpret_cast<const bf16x8 *>(lds + (ka ^ (32 * (i / KB))) + 32 * (i % KB) * T::RB);
+        const uint32_t at = 32 * step_of(i / KB), twisted = D == 256 ? at % 256 : at;
+        return *(__attribute__((address_space(3))) const bf16x8 *)(uintptr_t)((ka ^ twisted) + (at - twisted) +
+                                                                             32 * (i % KB) * T::RB);
       };
       auto vread = [&](int i) {
         s16x4t v[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          v[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4t *)(
-              lds + (va ^ (64 * (i % DB) + 32 * e)) + (16 * (i / DB) + 8 * e) * T::RB));
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t at = 64 * block_of(i % DB) + 32 * e, twisted = D == 256 ? at % 256 : at;
+          v[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4t *)(uintptr_t)(
+              (va ^ twisted) + (at - twisted) + (16 * (i / DB) + 8 * e) * T::RB));
+        }
         return __builtin_bit_cast(bf16x8, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
       };
       const int flag = sbad[t & 1];
@@ -527,7 +538,7 @@ void attn_prefill_kernel(ChunkArgsAll) {
       for (int i = 0; i < KS * KB; ++i) {
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int r = 0; r < R; ++r) s[r][i % KB] = mfma32(ring[i % kAhead], q[r][i / KB], s[r][i % KB]);
+        for (int r = 0; r < R; ++r) s[r][i % KB] = mfma32(ring[i % kAhead], q[r][step_of(i / KB)], s[r][i % KB]);
         if (i + kAhead < KS * KB) ring[i % kAhead] = kread(i + kAhead);
         if (!kTwoSteps && i % kEvery == 0) {
           const int j = i / kEvery / 2;
@@ -626,7 +637,7 @@ void attn_prefill_kernel(ChunkArgsAll) {
           if (b == 0 && D == 256) asm volatile("" : "+v"(va));
           __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-          for (int r = 0; r < R; ++r) o[r][b] = mfma32(ring[i % kAhead], pf[r], o[r][b]);
+          for (int r = 0; r < R; ++r) o[r][block_of(b)] = mfma32(ring[i % kAhead], pf[r], o[r][block_of(b)]);
           if (i + kAhead < 2 * KB * DB) ring[i % kAhead] = vread(i + kAhead);
         }
       }
