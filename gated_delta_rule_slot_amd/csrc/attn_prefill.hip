@@ -3,8 +3,8 @@
 //
 // The query heads of one key-value head read the same keys, so a request's rows of one
 // key-value head are (new token, head of the group), token by token.  A tile has 128 of them, 32 of
-// each wave of a workgroup, or twice as many, and is walked over in blocks of KT places.  4 D flops for every (row, place):
-// bound by the matrix units, or, for few rows, by the reading of the cache.
+// each wave of a workgroup, or twice as many, and walks over blocks of KT places.  4 D flops for every
+// (row, place): bound by the matrix units, or, for few rows, by the reading of the cache.
 //
 //   S^T = K Q^T   A = keys (rows = places), B = queries (columns = rows of the call).  A lane
 //                 gets, for row c = lane % 32 and half h = lane / 32, the scores of places
@@ -18,27 +18,30 @@
 // block ahead, with one barrier a block; their loads are issued between the products, and a wave in
 // its products goes before one in its softmax.
 //
-// Two workgroups run on a compute unit (256 registers a lane, 64 KB), one in its products while the
+// Two workgroups run on a compute unit (256 registers a lane, 64 KB; three with heads of 64), one in its products while the
 // other is in its softmax: heads of 256 need O, the queries and 32 scores a row at once, which is why
 // KT is 32 there.  A single spilled register in the walk waits for all loads behind it (456 instead
 // of 345 us for a 6144-token prompt), so what the walk does not need is worked out again behind it.
 //
-// The exponent's reference m follows the running maximum only where that has grown by more
-// than 2^8 (a wave's common decision), so O is rarely rescaled: weights are at most 2^8 then,
-// and fp32 sums and bf16 weights lose nothing by that.  The weights are rounded to bf16 once for
-// the product (their sum l is not): an error of at most 2^-8 of a weighted mean of |v|, about as
-// large as the output's own rounding.  Two bf16 parts would take half as many matrix
-// instructions again.
+// The exponent's reference m is the maximum of some blocks before and stays as long as a lane's
+// weights of a block sum to 2^8 at most (a wave's common decision): fp32 sums and bf16 weights lose
+// nothing by that, and in most blocks neither is the maximum looked for nor O rescaled.  Where the sum is
+// larger the block's scores are worked out again and m follows.  (Looking for the maximum in every
+// block: 4.63 instead of 4.42 ms for 24576 tokens with heads of 128, 1006 instead of 1000 us for 512 tokens
+// behind 131072 with heads of 256.  Scores that rise by 16 or more from block to block throughout
+// pay for the second product: 8192 tokens 703 instead of 509 us.)
+//
+// The weights are rounded to bf16 once for the product (their sum l is not): an error of at most 2^-8
+// of a weighted mean of |v|, about as large as the output's own rounding.  Two bf16 parts would take
+// half as many matrix instructions again.
 //
 // Measured on MI355X (a matrix product of 8192^3 runs at 1338 TFLOP/s there): one prompt of 24576
-// tokens 1050-1070 TFLOP/s with heads of 256, 1025 of 128 and 900 of 64 (whose softmax takes as long as
-// its products), from an e4m3 cache 955, 1015 and 830; 512 tokens behind 131072 1.05-1.11 ms, 1000-1050
-// TFLOP/s; 6144 tokens 335-355 us, 870-930 (the last tiles run alone); 32 requests of 1 to 7 tokens
-// over 500 to 8192: 75 us, 3.7 TB/s.  The matrix units are busy for half of the time that the compute
-// units are.
+// tokens 1120-1175 TFLOP/s with heads of 256, 1075-1120 of 128, 1030-1060 of 64, from an e4m3 cache
+// 1065-1100, 1045-1080 and 1005-1030; 512 tokens behind 131072 1.00-1.04 ms, 1060-1100 TFLOP/s; 6144 tokens
+// 320-340 us, 910-960 (the last tiles run alone); 32 requests of 1 to 7 tokens over 500 to 8192: 75 us,
+// 3.7 TB/s.
 #include <algorithm>
 #include <cmath>
-#include <type_traits>
 
 #include "kv.hpp"
 #include "lanes.hpp"
@@ -53,7 +56,7 @@ constexpr int kCUs = 256;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.693147180559945309417f;
 constexpr float kNegInf = -__builtin_inff();
-constexpr float kGrowth = 8.f;  // log2 of how far the maximum may pass the reference
+constexpr float kMost = 256.f;  // sum of a lane's weights of a block up to which the reference stays
 
 constexpr int kRowBits = 7;  // a tile has 2^7 rows, 32 of each wave, or 2^8, 64 of each
 
@@ -565,41 +568,60 @@ void attn_prefill_kernel(ChunkArgsAll) {
         load_ids(next + 1);
       }
       const bool flagged = uniform(flag) == t;
-      if (p0 < wfrom_last || p0 + KT - 1 > wfirst || flagged) [[unlikely]] {  // seen in part
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const int from = seen_from(p, ch.begin, place[r]);
-#pragma unroll
-          for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int at = p0 + 32 * kb + 8 * (e >> 2) + 4 * half + (e & 3);
-              if (at > place[r] || at < from) s[r][kb][e] = kNegInf;
-            }
+      const bool in_part = p0 < wfrom_last || p0 + KT - 1 > wfirst || flagged;
+      auto hide = [&](int r) {  // what the rows do not see
+        uint32_t no = 0;        // scores of places that are in no page
+        if (flagged) [[unlikely]] {
+#pragma unroll 1
+          for (int e = 0; e < 16 * KB; ++e) {
+            const int at = p0 + 32 * (e >> 4) + 8 * ((e >> 2) & 3) + 4 * half + (e & 3);
+            const int id = g.page_table[int64_t(ch.slot) * g.max_pages + (min(at, ch.len - 1) >> g.page_shift)];
+            no |= id <= 0 || id >= g.pages ? 1u << e : 0u;
+          }
         }
-        if (flagged) {
-#pragma unroll
-          for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int at = p0 + 32 * kb + 8 * (e >> 2) + 4 * half + (e & 3);
-              const int id = g.page_table[int64_t(ch.slot) * g.max_pages + (min(at, ch.len - 1) >> g.page_shift)];
-              if (id <= 0 || id >= g.pages) {
-#pragma unroll
-                for (int r = 0; r < R; ++r) s[r][kb][e] = kNegInf;
-              }
-            }
-        }
-      }
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        float top = s[r][0][0];
+        const int from = seen_from(p, ch.begin, place[r]);
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) top = fmaxf(top, s[r][kb][e]);
-        top = halves_max(top) * p.c;
-        if (__any(top > m[r] + kGrowth)) {
+          for (int e = 0; e < 16; ++e) {
+            const int at = p0 + 32 * kb + 8 * (e >> 2) + 4 * half + (e & 3);
+            if (at > place[r] || at < from || (no >> (16 * kb + e) & 1)) s[r][kb][e] = kNegInf;
+          }
+      };
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (in_part) [[unlikely]] hide(r);
+        auto weigh = [&] {  // scores to weights, and their sum
+          const float mr = ref(m[r]);
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              s[r][kb][e] = fexp2(fmaf(s[r][kb][e], p.c, -mr));
+              sum[e & 3] += s[r][kb][e];
+            }
+          return (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        };
+        float sum = 0.f;
+        bool follow = in_part || __any(m[r] == kNegInf);
+        if (!follow) {
+          sum = weigh();
+          if (__any(!(sum <= kMost))) [[unlikely]] {
+            follow = true;
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb) s[r][kb] = f32x16{};
+#pragma unroll
+            for (int i = 0; i < KS * KB; ++i) s[r][i % KB] = mfma32(kread(i), q[r][step_of(i / KB)], s[r][i % KB]);
+          }
+        }
+        if (follow) [[unlikely]] {
+          float top = s[r][0][0];
+#pragma unroll
+          for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) top = fmaxf(top, s[r][kb][e]);
+          top = halves_max(top) * p.c;
           const float to = fmaxf(m[r], top), f = fexp2(m[r] - ref(to));
           l[r] *= f;
 #pragma unroll
@@ -607,17 +629,9 @@ void attn_prefill_kernel(ChunkArgsAll) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) o[r][b][e] *= f;
           m[r] = to;
+          sum = weigh();
         }
-        const float mr = ref(m[r]);
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            s[r][kb][e] = fexp2(fmaf(s[r][kb][e], p.c, -mr));
-            sum[e & 3] += s[r][kb][e];
-          }
-        l[r] += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        l[r] += sum;
       }
       __builtin_amdgcn_s_setprio(1);
 #pragma unroll

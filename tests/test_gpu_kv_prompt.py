@@ -238,6 +238,32 @@ def test_chunk_values_that_are_not_finite_in_divided_places(dim, group, f8):
     assert ((got - want).abs() <= 4 * 2.0 ** -8 * (want.abs() + 4))[free].all()
 
 
+@pytest.mark.parametrize("rise", [0.1, 1.0, -1.0])
+@pytest.mark.parametrize("dim,kv_heads,group,f8", [(64, 1, 3, False), (64, 1100, 2, False), (128, 2, 2, False),
+                                                   (256, 1, 4, False), (64, 1, 2, True), (128, 1, 8, True),
+                                                   (256, 1, 1, True)])
+def test_chunk_scores_that_rise_with_the_place(dim, kv_heads, group, f8, rise):
+    """Every block of places has much larger scores than those before (or, falling, smaller ones), so that
+    the reference of the exponent has to follow, for some rows of a wave and not for others."""
+    new, L = ([70, 3, 2, 1] if kv_heads > 2 else [150, 40], 333)
+    lens = [L] + [77] * (len(new) - 1)
+    c = make_cache(dim, lens, None, kv_heads, dim, 16, f8)
+    g = torch.Generator().manual_seed(dim + group)
+    T = sum(new)
+    for b, n in enumerate(lens):
+        at = torch.arange(n)
+        page = c.table[c.slots[b]][at // 16].long()
+        ramp = (at * rise).view(n, 1, 1) / dim
+        k = ramp + 0.3 * torch.randn(n, kv_heads, dim, generator=g)
+        c.k[0].view(torch.uint8 if f8 else torch.int16)[page, :, at % 16] = \
+            stored(k, f8).view(torch.uint8 if f8 else torch.int16)
+    # rows of one sign rise where those of the other fall
+    sign = torch.where(torch.rand(T, kv_heads * group, 1, generator=g) < 0.7, 1.0, -1.0)
+    q = (sign + 0.3 * torch.randn(T, kv_heads * group, dim, generator=g)).to(torch.bfloat16).cuda()
+    pool, q, out, lse, sc = chunk_call(c, new, group, late=7, q=q, scale=1.0)
+    check_chunk(c, new, q, sc, out, lse, 0, 7, pool.mass)
+
+
 @pytest.mark.parametrize("f8,page,window,late", [(False, 16, 0, 70), (True, 32, 0, 5), (False, 4, 90, 0),
                                                  (True, 2, 90, 400), (False, 64, 1, 3)])
 def test_chunk_tiles_of_twice_the_rows(f8, page, window, late):
