@@ -1015,10 +1015,10 @@ ChunkPlan chunk_plan(const gdn_kv_pool *p, int batch, int tokens, int q_heads, i
   const int KT = p->d.head_dim == 256 ? 32 : 64, group = q_heads / p->d.kv_heads;
   const int most = max_len / KT + 1;  // blocks of a tile
   constexpr int64_t slots = 2 * kCUs;
-  // What follows is as if all requests were alike (the host knows no more).  With as many tiles as workgroups that
-  // run at once, none is divided: pieces gain nothing (6144 tokens, 8 by 2 heads of 256: 347 us
-  // whole, 404 in pieces of up to 0.6 of the longest, 375 of 0.8).  Fewer are, so that the pieces fill the compute units: once for one
-  // request whose tiles all see about as many places, half more often where lengths differ or the
+  // What follows is as if all requests were alike (the host knows no more).  With as many tiles as
+  // workgroups that run at once, none is divided: pieces gain nothing (6144 tokens, 8 by 2 heads of 256:
+  // 347 us whole, 404 in pieces of up to 0.6 of the longest, 375 of 0.8).  Fewer are, so that the pieces
+  // fill the compute units: once for one request whose tiles all see about as many places, half more often where lengths differ or the
   // first tiles see few places (1024 tokens: 52 us whole, 45 in six, 56 in nine), and more often yet where
   // pieces stay long (25 requests of up to 30000: 476 us in two, 254 in ten, 263 in twenty).  A piece
   // takes some 5 us more than its blocks and the join 5 to 10, so there are at least 4 blocks to a
@@ -1026,11 +1026,11 @@ ChunkPlan chunk_plan(const gdn_kv_pool *p, int batch, int tokens, int q_heads, i
   const int64_t each = (int64_t(tokens) + batch - 1) / batch, own = ((each * group - 1) >> kRowBits) + 1;
   const int64_t units = batch * own * p->d.kv_heads;
   // Tiles of twice the rows, where a wave has the registers for them, read shared memory half as often and
-  // convert e4m3 half as often (24576 tokens, 64 heads of 64: 4.98 instead of 5.4 ms, from e4m3 4.92 instead of 5.9;
-  // 4 e4m3 requests of 2048, 4096 tiles of 128 rows: 194 instead of 219 us), but half as many end less evenly
-  // (4 bf16 requests of 4096, 1536 tiles: 172 us instead of 154; 8 of them: 287 and 284).
-  const int64_t enough = p->d.kv_dtype == GDN_BF16 ? 4096 : 2048;
-  r.bits = kRowBits + (p->d.head_dim == 64 && units >= enough ? 1 : 0);
+  // convert e4m3 half as often, but fewer of them run at once and end less evenly.  24576 tokens, 64 heads
+  // of 64: 4.77 instead of 5.04 ms, from e4m3 4.95 instead of 5.20, 32 heads (6144 tiles of 128 rows) 2.41
+  // instead of 2.53; 8 requests of 4096 by 12 heads (3072 tiles): 284 us instead of 272; 64 short requests
+  // (8192 tiles, 16 of a head) 469 instead of 454.
+  r.bits = kRowBits + (p->d.head_dim == 64 && units >= 12 * slots && own >= 32 ? 1 : 0);
   r.tiles = chunk_tiles(batch, tokens, group, r.bits);
   if (units < slots && most >= 16) {
     const int64_t half_more = (3 * slots / 2 + units - 1) / units;

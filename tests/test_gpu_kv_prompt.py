@@ -239,17 +239,17 @@ def test_chunk_values_that_are_not_finite_in_divided_places(dim, group, f8):
 
 
 @pytest.mark.parametrize("rise", [0.1, 1.0, -1.0])
-@pytest.mark.parametrize("dim,kv_heads,group,f8", [(64, 1, 3, False), (64, 1100, 2, False), (128, 2, 2, False),
+@pytest.mark.parametrize("dim,kv_heads,group,f8", [(64, 1, 3, False), (64, 32, 2, False), (128, 2, 2, False),
                                                    (256, 1, 4, False), (64, 1, 2, True), (128, 1, 8, True),
                                                    (256, 1, 1, True)])
 def test_chunk_scores_that_rise_with_the_place(dim, kv_heads, group, f8, rise):
     """Every block of places has much larger scores than those before (or, falling, smaller ones), so that
     the reference of the exponent has to follow, for some rows of a wave and not for others."""
-    new, L = ([70, 3, 2, 1] if kv_heads > 2 else [150, 40], 333)
+    new, L, rest = ([200, 70, 2], 333, 12288) if kv_heads > 2 else ([150, 40], 333, 0)  # (tiles of 256 rows)
     lens = [L] + [77] * (len(new) - 1)
     c = make_cache(dim, lens, None, kv_heads, dim, 16, f8)
     g = torch.Generator().manual_seed(dim + group)
-    T = sum(new)
+    T = sum(new) + rest
     for b, n in enumerate(lens):
         at = torch.arange(n)
         page = c.table[c.slots[b]][at // 16].long()
@@ -260,28 +260,26 @@ def test_chunk_scores_that_rise_with_the_place(dim, kv_heads, group, f8, rise):
     # rows of one sign rise where those of the other fall
     sign = torch.where(torch.rand(T, kv_heads * group, 1, generator=g) < 0.7, 1.0, -1.0)
     q = (sign + 0.3 * torch.randn(T, kv_heads * group, dim, generator=g)).to(torch.bfloat16).cuda()
-    pool, q, out, lse, sc = chunk_call(c, new, group, late=7, q=q, scale=1.0)
+    pool, q, out, lse, sc = chunk_call(c, new, group, late=7, q=q, scale=1.0, extra=rest)
     check_chunk(c, new, q, sc, out, lse, 0, 7, pool.mass)
 
 
 @pytest.mark.parametrize("f8,page,window,late", [(False, 16, 0, 70), (True, 32, 0, 5), (False, 4, 90, 0),
                                                  (True, 2, 90, 400), (False, 64, 1, 3)])
 def test_chunk_tiles_of_twice_the_rows(f8, page, window, late):
-    """So many heads of 64 that a tile has 256 rows: requests of one to a few hundred tokens, tiles and
-    waves filled in part, values that are not finite in one request."""
-    H, G, B, late_place = 64, 3 if f8 else 2, 33 if f8 else 65, 45
+    """A call of so many rows of heads of 64 that a tile has 256 of them (most behind the last request):
+    requests of one to a few hundred tokens, tiles and waves filled in part, values that are not finite in one."""
+    H, G, B, late_place, rest = 32, 2, 6, 45, 12000
     r = np.random.default_rng(page)
-    new = [300, 87, 0, 129] + [int(x) for x in r.integers(0, 6, size=B - 4)]
-    new[-1] = 1
-    cached = [20, 0, 9, 70] + [int(x) for x in r.integers(0, 40, size=B - 4)]
+    new, cached = [300, 87, 0, 129, 5, 1], [20, 0, 9, 70, 31, 200]
     lens = [max(1, n + m) for n, m in zip(new, cached)]
     begins = [int(r.integers(0, n)) if i % 5 == 3 else 0 for i, n in enumerate(lens)]
     c = make_cache(page, lens, begins, H, 64, page, f8)
-    pool, q, clean, lse, sc = chunk_call(c, new, G, window, late, extra=2)
+    pool, q, clean, lse, sc = chunk_call(c, new, G, window, late, extra=rest)
     check_chunk(c, new, q, sc, clean, lse, window, late, pool.mass)
     at = lens[0] - late_place
     c.v[0, int(c.table[c.slots[0], at // page]), 7, at % page, 11] = float("nan") if f8 else float("inf")
-    pool, _, out, lse2, _ = chunk_call(c, new, G, window, late, q=q.cuda(), extra=2)
+    pool, _, out, lse2, _ = chunk_call(c, new, G, window, late, q=q.cuda(), extra=rest)
     assert torch.equal(lse, lse2) and torch.isfinite(pool.mass).all()
     first = 300 - late_place
     hit = torch.zeros_like(out, dtype=torch.bool)
