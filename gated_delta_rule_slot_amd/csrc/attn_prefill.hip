@@ -18,8 +18,8 @@
 // block ahead, with one barrier a block; their loads are issued between the products, and a wave in
 // its products goes before one in its softmax.
 //
-// Two workgroups run on a compute unit (256 registers a lane, 64 KB; three with heads of 64), one in its products while the
-// other is in its softmax: heads of 256 need O, the queries and 32 scores a row at once, which is why
+// Two workgroups run on a compute unit (256 registers a lane, 64 KB; three with heads of 64), one in its
+// products while the other is in its softmax: heads of 256 need O, the queries and 32 scores a row at once, which is why
 // KT is 32 there.  A spilled register that is read again in the walk waits for all loads that were
 // asked for after it, so what the walk does not need is worked out again behind it.
 //
@@ -1018,8 +1018,8 @@ ChunkPlan chunk_plan(const gdn_kv_pool *p, int batch, int tokens, int q_heads, i
   // What follows is as if all requests were alike (the host knows no more).  With as many tiles as
   // workgroups that run at once, none is divided: pieces gain nothing (6144 tokens, 8 by 2 heads of 256:
   // 347 us whole, 404 in pieces of up to 0.6 of the longest, 375 of 0.8).  Fewer are, so that the pieces
-  // fill the compute units: once for one request whose tiles all see about as many places, half more often where lengths differ or the
-  // first tiles see few places (1024 tokens: 52 us whole, 45 in six, 56 in nine), and more often yet where
+  // fill the compute units: once for one request whose tiles all see about as many places, half more
+  // often where lengths differ or the first tiles see few places (1024 tokens: 52 us whole, 45 in six, 56 in nine), and more often yet where
   // pieces stay long (25 requests of up to 30000: 476 us in two, 254 in ten, 263 in twenty).  A piece
   // takes some 5 us more than its blocks and the join 5 to 10, so there are at least 4 blocks to a
   // piece, 7 of several requests, and short lists stay whole (4 requests of up to 333: 26 us, 37 in two).
