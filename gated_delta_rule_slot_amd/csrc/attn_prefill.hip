@@ -31,6 +31,10 @@
 // behind 131072 with heads of 256.  Scores that rise by 16 or more from block to block throughout
 // pay for the second product: 8192 tokens 703 instead of 509 us.)
 //
+// m is a rounded product s c, and fma(s, c, -m) takes it from the unrounded one: all weights of a row have a
+// factor of 2^(half a unit of m), at most 2^(2^-8) up to |m| = 2^16, which cancels.  Beyond, the product is
+// rounded first: from |m| = 2^31 on the factor would be 2^128 and more, and the row's sum infinite or 0.
+//
 // The weights are rounded to bf16 once for the product (their sum l is not): an error of at most 2^-8
 // of a weighted mean of |v|, about as large as the output's own rounding.  Two bf16 parts would take
 // half as many matrix instructions again.
@@ -57,6 +61,7 @@ constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.693147180559945309417f;
 constexpr float kNegInf = -__builtin_inff();
 constexpr float kMost = 256.f;  // sum of a lane's weights of a block up to which the reference stays
+constexpr float kFar = 65536.f;  // size of the reference up to which one fma takes it from the product s c
 
 constexpr int kRowBits = 7;  // a tile has 2^7 rows, 32 of each wave, or 2^8, 64 of each
 
@@ -88,6 +93,12 @@ struct ChunkDev {
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ __forceinline__ float ref(float m) { return m == kNegInf ? 0.f : m; }
+// s c - m with the product rounded first, as it was for m: 0 for the score that m is of
+__device__ __forceinline__ float rounded_apart(float s, float c, float m) {
+  float x = s * c;
+  asm("" : "+v"(x));  // (no fma)
+  return x - m;
+}
 // the larger / the sum of a value and its counterpart in the other half
 __device__ __forceinline__ float halves_max(float v) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
@@ -604,7 +615,7 @@ void attn_prefill_kernel(ChunkArgsAll) {
           return (sum[0] + sum[1]) + (sum[2] + sum[3]);
         };
         float sum = 0.f;
-        bool follow = in_part || __any(m[r] == kNegInf);
+        bool follow = in_part || __any(!(fabsf(m[r]) <= kFar));  // (-inf: nothing seen so far)
         if (!follow) {
           sum = weigh();
           if (__any(!(sum <= kMost))) [[unlikely]] {
@@ -629,7 +640,16 @@ void attn_prefill_kernel(ChunkArgsAll) {
 #pragma unroll
             for (int e = 0; e < 16; ++e) o[r][b][e] *= f;
           m[r] = to;
+          if (fabsf(ref(to)) > kFar) [[unlikely]] {  // (divided by c, so that the code of the weights serves)
+            const float back = 1.f / p.c;
+#pragma unroll
+            for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+              for (int e = 0; e < 16; ++e) s[r][kb][e] = rounded_apart(s[r][kb][e], p.c, to) * back;
+            m[r] = 0.f;
+          }
           sum = weigh();
+          m[r] = to;
         }
         l[r] += sum;
       }
