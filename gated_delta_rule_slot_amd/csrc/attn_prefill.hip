@@ -89,6 +89,7 @@ struct ChunkDev {
   uint32_t inverse;     // ceil(2^32 / group), for a group of 2 or more
   float *o, *ml;    // parts > 1: [part][token][q_heads] rows of O, and m and l
   float *lse;       // [tokens][q_heads], or NULL
+  float *row_ml;    // [tokens][q_heads] rows' m and 1 / l for the weights' kernel (see row_factors), or NULL
 };
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -98,6 +99,11 @@ __device__ __forceinline__ float rounded_apart(float s, float c, float m) {
   float x = s * c;
   asm("" : "+v"(x));  // (no fma)
   return x - m;
+}
+// What a row's weights 2^(s c - m) / l need; of a row that sees nothing, 2^-inf * 0
+__device__ __forceinline__ void row_factors(float *to, float m, float l) {
+  to[0] = l == 0.f ? -kNegInf : m;
+  to[1] = l == 0.f ? 0.f : 1.f / l;
 }
 // the larger / the sum of a value and its counterpart in the other half
 __device__ __forceinline__ float halves_max(float v) {
@@ -224,6 +230,13 @@ __device__ __forceinline__ Span span_of(const ChunkDev &p, const Chunk &ch) {
 template <int D>
 __device__ __forceinline__ int twist(int r) {
   return D == 64 ? (((r >> 1) & 1) << 2 | ((r >> 2) & 3)) : ((r & 3) << 2 | ((r >> 2) & 3));
+}
+
+// The order of a score's steps of 16 columns: a row of 512 bytes has twice the pieces that the twist
+// permutes, so steps that differ by half of a row follow each other, and have their address in common.
+template <int D>
+constexpr int step_at(int i) {
+  return D == 256 ? (i >> 1) + (i & 1) * (D / 32) : i;
 }
 
 template <int D, bool kF8>
@@ -447,9 +460,8 @@ void attn_prefill_kernel(ChunkArgsAll) {
   const int vrow = 4 * half + ((lane >> 2) & 3), vpair = ((lane >> 4) & 1) * 2 + ((lane & 3) >> 1);
   const int kaddr = c * T::RB + ((half ^ twist<D>(c)) << 4);
   const int vaddr = vrow * T::RB + ((vpair ^ twist<D>(vrow)) << 4) + 8 * (lane & 1) + T::kBytes;
-  // a row of 512 bytes has twice the pieces that the twist permutes: steps and blocks of columns that
-  // differ by half of a row follow each other, and have their address in common
-  auto step_of = [](int i) { return D == 256 ? (i >> 1) + (i & 1) * (KS / 2) : i; };
+  // (the blocks of columns likewise)
+  auto step_of = [](int i) { return step_at<D>(i); };
   auto block_of = [](int i) { return D == 256 ? (i >> 1) + (i & 1) * (DB / 2) : i; };
 
   f32x16 o[R][DB];
@@ -721,6 +733,7 @@ void attn_prefill_kernel(ChunkArgsAll) {
     }
     if (p.lse && half == 0 && kind <= kFinite)
       p.lse[orow] = ln == 0.f ? kNegInf : (m[r] + __builtin_amdgcn_logf(ln)) * kLn2;
+    if (p.row_ml && half == 0 && kind <= kFinite) row_factors(p.row_ml + 2 * orow, m[r], ln);
     const float f = ln == 0.f ? 0.f : again->g.v_scale / ln;
     uint16_t *to = p.a.out + orow * D + 8 * half;
 #pragma unroll
@@ -839,6 +852,7 @@ __global__ __launch_bounds__(kThreads) void attn_prefill_join_kernel(KvGeom g, C
       }
     }
     if (p.lse && lane == 0) p.lse[orow] = l == 0.f ? kNegInf : (top + __builtin_amdgcn_logf(l)) * kLn2;
+    if (p.row_ml && lane == 0) row_factors(p.row_ml + 2 * orow, top, l);
     const float f = l == 0.f ? 0.f : g.v_scale / l;
     uint16_t *to = p.a.out + orow * D + lane * N;
     if constexpr (N == 1) {
@@ -854,7 +868,9 @@ __global__ __launch_bounds__(kThreads) void attn_prefill_join_kernel(KvGeom g, C
 // One workgroup per request, key-value head and 4 * kMassPlaces places; a wave keeps the keys of its
 // places in registers and walks the rows of the last queries, kMassRows at a time, which the waves
 // share in shared memory (in the layout of a block of keys), asked for one step ahead.  So every
-// entry of mass has one owner and one order of summation.  A weight is exp(s - lse).
+// entry of mass has one owner and one order of summation.  A weight is 2^(s c - m) / l with the row's m and
+// l, its score and exponent worked out as for l, bit for bit (against the logarithm lse a large score would lose
+// |lse| 2^-23, and one whose columns are summed in another order as much).
 //
 // (512 queries over 131584 places, 16 heads of 256: 0.73 ms; reading the rows by each wave for
 // itself 2.25 ms, bound by its scattered reads.  64 places a wave instead of 32: 83 against 65 us for
@@ -923,7 +939,7 @@ void attn_prefill_mass_kernel(KvGeom g, ChunkDev p, int blocks) {
   const int r0 = max(first, g0 - place0) * G;
   int r1 = all;
   if (p.a.window) r1 = int(min(int64_t(all), max(int64_t(0), int64_t(g0) + PLACES - 1 + p.a.window - place0) * G));
-  float lse[NB];
+  f32x2_t ml[NB];
   auto ask = [&](int r, int buffer) {
 #pragma unroll
     for (int j = 0; j < LOADS; ++j) {
@@ -938,7 +954,7 @@ void attn_prefill_mass_kernel(KvGeom g, ChunkDev p, int blocks) {
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       const int row = min(r + 32 * nb + c, all - 1), token = token_of(p, row);
-      lse[nb] = p.lse[int64_t(bos + token) * p.a.q_heads + h * G + (row - token * G)];
+      ml[nb] = *reinterpret_cast<const f32x2_t *>(p.row_ml + 2 * (int64_t(bos + token) * p.a.q_heads + h * G + (row - token * G)));
     }
   };
   f32x16 sum[KB];
@@ -951,9 +967,14 @@ void attn_prefill_mass_kernel(KvGeom g, ChunkDev p, int blocks) {
   for (int r = r0; r < r1; r += kMassRows, buffer ^= 1) {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    float shift[NB];
+    float m[NB], part[NB];
+    bool far = false;
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) shift[nb] = lse[nb] == kNegInf ? kNegInf : -lse[nb] * kLog2e;
+    for (int nb = 0; nb < NB; ++nb) {
+      m[nb] = ml[nb][0];
+      part[nb] = ml[nb][1];
+      far |= !(fabsf(m[nb]) <= kFar);
+    }
     if (r + kMassRows < r1) ask(r + kMassRows, buffer ^ 1);
     const int first_place = place0 + token_of(p, r), last_place = place0 + token_of(p, min(r + kMassRows, r1) - 1);
     if (p0 > last_place || p0 + KP <= seen_from(p, begin, first_place)) continue;  // the wave's places are not seen
@@ -966,7 +987,7 @@ void attn_prefill_mass_kernel(KvGeom g, ChunkDev p, int blocks) {
       for (int nb = 0; nb < NB; ++nb) s[kb][nb] = f32x16{};
     constexpr int kAhead = 4;
     auto qread = [&](int i) {
-      return *reinterpret_cast<const bf16x8 *>(lds + (qa ^ (32 * (i / NB))) + 32 * (i % NB) * RB);
+      return *reinterpret_cast<const bf16x8 *>(lds + (qa ^ (32 * step_at<D>(i / NB))) + 32 * (i % NB) * RB);
     };
     bf16x8 ring[kAhead];
 #pragma unroll
@@ -975,10 +996,22 @@ void attn_prefill_mass_kernel(KvGeom g, ChunkDev p, int blocks) {
     for (int i = 0; i < KS * NB; ++i) {
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int kb = 0; kb < KB; ++kb) s[kb][i % NB] = mfma32(k[kb][i / NB], ring[i % kAhead], s[kb][i % NB]);
+      for (int kb = 0; kb < KB; ++kb) s[kb][i % NB] = mfma32(k[kb][step_at<D>(i / NB)], ring[i % kAhead], s[kb][i % NB]);
       if (i + kAhead < KS * NB) ring[i % kAhead] = qread(i + kAhead);
     }
     __builtin_amdgcn_sched_barrier(0);
+    if (__any(far)) [[unlikely]] {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+        if (m[nb] != -kNegInf && !(fabsf(m[nb]) <= kFar)) {
+          const float back = 1.f / p.c;
+#pragma unroll
+          for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[kb][nb][e] = rounded_apart(s[kb][nb][e], p.c, m[nb]) * back;
+          m[nb] = 0.f;
+        }
+    }
     const bool whole = r + kMassRows <= r1 && p0 + KP - 1 <= first_place && p0 >= seen_from(p, begin, last_place);
     if (whole) {
 #pragma unroll
@@ -986,7 +1019,7 @@ void attn_prefill_mass_kernel(KvGeom g, ChunkDev p, int blocks) {
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) sum[kb][e] += fexp2(fmaf(s[kb][nb][e], p.c, shift[nb]));
+          for (int e = 0; e < 16; ++e) sum[kb][e] = fmaf(fexp2(fmaf(s[kb][nb][e], p.c, -m[nb])), part[nb], sum[kb][e]);
     } else {
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb) {
@@ -997,8 +1030,8 @@ void attn_prefill_mass_kernel(KvGeom g, ChunkDev p, int blocks) {
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const int at = p0 + 32 * kb + 8 * (e >> 2) + 4 * half + (e & 3);
-            const float w = fexp2(fmaf(s[kb][nb][e], p.c, shift[nb]));
-            sum[kb][e] += at <= to && at >= from ? w : 0.f;
+            const float more = fmaf(fexp2(fmaf(s[kb][nb][e], p.c, -m[nb])), part[nb], sum[kb][e]);
+            sum[kb][e] = at <= to && at >= from ? more : sum[kb][e];
           }
       }
     }
@@ -1027,7 +1060,7 @@ int64_t chunk_tiles(int batch, int tokens, int group, int bits = kRowBits) {
 struct ChunkPlan {
   int64_t tiles;
   int bits, parts, piece, spread;
-  size_t o, ml, lse;  // parts of the workspace, in order
+  size_t o, ml, row_ml;  // parts of the workspace, in order
 };
 ChunkPlan chunk_plan(const gdn_kv_pool *p, int batch, int tokens, int q_heads, int max_len, int mass_tokens) {
   ChunkPlan r{};
@@ -1071,7 +1104,7 @@ ChunkPlan chunk_plan(const gdn_kv_pool *p, int batch, int tokens, int q_heads, i
     r.o = pad256(rows * p->d.head_dim * 4);
     r.ml = pad256(rows * 8);
   }
-  if (mass_tokens > 0) r.lse = pad256(size_t(tokens) * q_heads * 4);
+  if (mass_tokens > 0) r.row_ml = pad256(size_t(tokens) * q_heads * 8);
   return r;
 }
 
@@ -1120,7 +1153,7 @@ bool chunk_fits(const gdn_kv_pool *p, int batch, int tokens, int q_heads, int ma
 
 size_t chunk_workspace(const gdn_kv_pool *p, int batch, int tokens, int q_heads, int max_len, int mass_tokens) {
   const ChunkPlan w = chunk_plan(p, batch, tokens, q_heads, max_len, mass_tokens);
-  return w.o + w.ml + w.lse;
+  return w.o + w.ml + w.row_ml;
 }
 
 hipError_t launch_attn_prefill(const gdn_kv_pool *pool, int layer, const ChunkArgs &a, hipStream_t s) {
@@ -1142,7 +1175,8 @@ hipError_t launch_attn_prefill(const gdn_kv_pool *pool, int layer, const ChunkAr
   char *at = static_cast<char *>(a.workspace);
   p.o = reinterpret_cast<float *>(at);
   p.ml = reinterpret_cast<float *>(at += w.o);
-  p.lse = a.lse ? a.lse : a.mass_tokens > 0 ? reinterpret_cast<float *>(at + w.ml) : nullptr;
+  p.lse = a.lse;
+  p.row_ml = a.mass_tokens > 0 ? reinterpret_cast<float *>(at + w.ml) : nullptr;
   const bool f8 = pool->d.kv_dtype == GDN_F8_E4M3;
   switch (pool->d.head_dim) {
     case 64: return launch_d<64>(g, p, f8, s);

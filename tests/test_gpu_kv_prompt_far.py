@@ -58,7 +58,7 @@ def check_sharp(c, new, q, scale, out, lse, window=0, late=0, mass=None, mass0=N
 
 
 SCALES = [1e3, 1e6, 1e9, 1e12, -1e30]
-LATE = [0]  # queries whose weights are added to mass
+LATE = [0, 20]  # queries whose weights are added to mass
 
 
 @pytest.mark.parametrize("late", LATE)
@@ -150,11 +150,16 @@ def test_far_and_near_rows_of_a_wave(dim, f8, far):
         at += n
 
 
-@pytest.mark.parametrize("scale", [1e4, 1e8, 3e20])
+@pytest.mark.parametrize("scale", [0.3, 1e4, 1e8, 3e20])
 def test_far_scores_of_ordinary_heads(scale):
-    """Scores of any fraction: finite results, the logarithm of their sum within its roundings."""
-    for dim, f8 in ((64, False), (128, True), (256, False)):
+    """Scores of any fraction: finite results, the logarithm of their sum within its roundings, and
+    weights that sum to one for every row."""
+    for dim, f8 in ((64, False), (128, True), (256, False), (256, True)):
         c = make_cache(dim, [300, 90], None, 2, dim, 16, f8)
-        pool, q, out, lse, sc = chunk_call(c, [100, 3], 3, scale=float(np.float32(scale)))
+        c.mass.zero_()
+        pool, q, out, lse, sc = chunk_call(c, [100, 3], 3, late=9, scale=float(np.float32(scale)))
         check_chunk(c, [100, 3], q, sc, out, lse)
         assert torch.isfinite(out.float()).all()
+        total = pool.mass.sum(dim=-1).cpu()[0]
+        for b, rows in ((0, 9), (1, 3)):
+            assert ((total[c.slots[b]] - 3 * rows).abs() <= 3 * rows * 2.0 ** -12).all(), (dim, total[c.slots[b]])
