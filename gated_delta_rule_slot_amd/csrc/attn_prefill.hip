@@ -210,17 +210,17 @@ __device__ __forceinline__ int seen_from(const ChunkDev &p, int begin, int place
   return p.a.window ? max(begin, place - p.a.window + 1) : begin;
 }
 
-// The blocks of KT places that a tile's rows see: lo and how many.
+// The blocks of KT places that a tile's rows see: lo and how many, and the first of these places.
 struct Span {
-  int lo, n;
+  int lo, n, from;
 };
 template <int KT>
 __device__ __forceinline__ Span span_of(const ChunkDev &p, const Chunk &ch) {
-  if (!ch.live) return Span{0, 0};
+  if (!ch.live) return Span{0, 0, 0};
   const int all = ch.n * p.group, place0 = ch.len - ch.n;
   const int first = place0 + token_of(p, ch.rows0), last = place0 + token_of(p, min(ch.rows0 + (1 << p.bits) - 1, all - 1));
-  const int lo = seen_from(p, ch.begin, first) / KT;
-  return Span{lo, max(0, last / KT + 1 - lo)};
+  const int from = seen_from(p, ch.begin, first), lo = from / KT;
+  return Span{lo, from <= last ? last / KT + 1 - lo : 0, from};
 }
 
 // ---- shared memory ---------------------------------------------------------
@@ -332,17 +332,21 @@ void attn_prefill_kernel(ChunkArgsAll) {
   auto lane_row = [&]() { return int(threadIdx.x & 63) / T::kLanes; };
   const int lpiece = lane % T::kLanes;
   const int loff = (kWide ? lane_row() * T::SB : 0) + ((kF8 ? lpiece : lpiece ^ twist<D>(wave * T::kLoadRows + lane_row())) << 4);
+  // Pages in front of the first place that the tile's rows see need not be there: for rows of its first block
+  // that lie before, those of that place are read (from: that place).
+  constexpr int kAnywhere = INT32_MIN;
   int ids[kWide ? NL : 1];
-  auto load_ids = [&](int t) {
+  auto load_ids = [&](int t, int from = kAnywhere) {
     if constexpr (kWide) {
 #pragma unroll
-      for (int j = 0; j < NL; ++j) ids[j] = table[uint32_t(min(t * KT + load_row(j), ch.len - 1)) >> g.page_shift];
+      for (int j = 0; j < NL; ++j)
+        ids[j] = table[uint32_t(min(max(t * KT + load_row(j), from), ch.len - 1)) >> g.page_shift];
     }
   };
   bool edge;  // whether the block to come has rows that are no places of the request
   uint32_t src[NL];  // its rows in the layer's keys and values
-  auto locate = [&](int t, int j) {
-    const int at = t * KT + load_row(j) + (kWide ? 0 : lane_row());
+  auto locate = [&](int t, int j, int from = kAnywhere) {
+    const int at = max(t * KT + load_row(j) + (kWide ? 0 : lane_row()), kWide ? from & -T::kLoadRows : from);
     int id;
     if constexpr (kWide) id = ids[j];
     else id = g.page_table[int64_t(ch.slot) * g.max_pages + (min(at, ch.len - 1) >> g.page_shift)];
@@ -351,10 +355,10 @@ void attn_prefill_kernel(ChunkArgsAll) {
     src[j] = uint32_t(((id * g.kv_heads + h) << g.page_shift) + (at & page_mask));
     return wrong;
   };
-  auto locate_all = [&](int t) {
+  auto locate_all = [&](int t, int from = kAnywhere) {
     bool bad = false;
 #pragma unroll
-    for (int j = 0; j < NL; ++j) bad |= locate(t, j);
+    for (int j = 0; j < NL; ++j) bad |= locate(t, j, from);
     return bad;
   };
   // the block's rows have all been located; bad: one of the lane's is in no page
@@ -486,8 +490,8 @@ void attn_prefill_kernel(ChunkArgsAll) {
         put(vraw, to + T::kBytes);
       }
     };
-    load_ids(t0);
-    located(t0, locate_all(t0));
+    load_ids(t0, span.from);
+    located(t0, locate_all(t0, span.from));
     ask_all(t0);
     fetch(kraw, g.k);
     fetch(vraw, g.v);
@@ -520,7 +524,9 @@ void attn_prefill_kernel(ChunkArgsAll) {
     for (int t = w0; t < w1; ++t) {
       arrive(t);
       const int p0 = t * KT;
-      const int next = min(t + 1, t1 - 1);  // (the last block is asked for again: no branch among the products)
+      // (the last block is asked for again, as one that nobody reads: no branch among the products.  Pages are
+      // those of the places behind it, or, small ones, its own, which have been looked at)
+      const int next = min(t + 1, t1 - 1);
       f32x16 s[R][KB];
 #pragma unroll
       for (int r = 0; r < R; ++r)
@@ -548,7 +554,7 @@ void attn_prefill_kernel(ChunkArgsAll) {
       };
       const int flag = sbad[t & 1];
       if constexpr (kTwoSteps) {
-        located(next, locate_all(next));
+        located(t + 1, locate_all(next) && (kWide || next > t));
         load_ids(next + 1);
         fetch(kraw, g.k);
       }
@@ -585,7 +591,7 @@ void attn_prefill_kernel(ChunkArgsAll) {
         put(kraw, lds + ((t + 1) & 1) * 2 * T::kBytes);
         fetch(vraw, g.v);
       } else {
-        located(next, bad);
+        located(t + 1, bad && (kWide || next > t));
         fetch(kraw, g.k);
         fetch(vraw, g.v);
         load_ids(next + 1);
