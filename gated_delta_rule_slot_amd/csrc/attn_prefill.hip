@@ -123,8 +123,10 @@ __device__ __forceinline__ f32x16 mfma32(const bf16x8 &a, const bf16x8 &b, const
 // place's NaN or infinite values.  Where a workgroup's result is not finite, its tile is walked
 // again with every such value as 0, which gives the finite part of the sums, then with 1 in the
 // place of inf and NaN and 0 elsewhere, then with 1 in the place of -inf and NaN: a sum above 0
-// says that the row sees one with a weight above 0.
-enum { kAsIs, kFinite, kUp, kDown };
+// says that the row sees one with a weight above 0.  Where the finite sums are not finite either, they may have
+// outgrown fp32, as weights are up to 2^4 and more where the reference stayed behind: the second walk is done again with
+// the reference following every block, so that no weight is above 1.
+enum { kAsIs, kFinite, kClose, kUp, kDown };
 __device__ __forceinline__ u32x4 sorted(u32x4 x, int kind) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -133,7 +135,7 @@ __device__ __forceinline__ u32x4 sorted(u32x4 x, int kind) {
     for (int e = 0; e < 2; ++e) {
       const uint32_t v = (x[i] >> (16 * e)) & 0xffffu, a = v & 0x7fffu;
       const bool mark = a > 0x7f80u || v == (kind == kUp ? 0x7f80u : 0xff80u);
-      r |= (kind == kFinite ? (a < 0x7f80u ? v : 0u) : mark ? 0x3f80u : 0u) << (16 * e);
+      r |= (kind <= kClose ? (a < 0x7f80u ? v : 0u) : mark ? 0x3f80u : 0u) << (16 * e);
     }
     x[i] = r;
   }
@@ -146,7 +148,7 @@ __device__ __forceinline__ uint32_t sorted_f8(uint32_t x, int kind) {
   for (int e = 0; e < 4; ++e) {
     const uint32_t v = (x >> (8 * e)) & 0xffu;
     const bool nan = (v & 0x7fu) == 0x7fu;
-    r |= (kind == kFinite ? (nan ? 0u : v) : nan ? 0x38u : 0u) << (8 * e);
+    r |= (kind <= kClose ? (nan ? 0u : v) : nan ? 0x38u : 0u) << (8 * e);
   }
   return r;
 }
@@ -633,7 +635,7 @@ void attn_prefill_kernel(ChunkArgsAll) {
           return (sum[0] + sum[1]) + (sum[2] + sum[3]);
         };
         float sum = 0.f;
-        bool follow = in_part || __any(!(fabsf(m[r]) <= kFar));  // (-inf: nothing seen so far)
+        bool follow = in_part || kind == kClose || __any(!(fabsf(m[r]) <= kFar));  // (-inf: nothing seen so far)
         if (!follow) {
           sum = weigh();
           if (__any(!(sum <= kMost))) [[unlikely]] {
@@ -717,7 +719,7 @@ void attn_prefill_kernel(ChunkArgsAll) {
     const int64_t orow = int64_t(ch.bos + token) * p.a.q_heads + h * p.group + (row - token * p.group);
     if (!whole) {
       const int64_t at = int64_t(part) * p.a.tokens * p.a.q_heads + orow;
-      if (half == 0 && kind <= kFinite) {
+      if (half == 0 && kind <= kClose) {
         p.ml[2 * at] = ln == 0.f ? kNegInf : m[r];
         p.ml[2 * at + 1] = ln;
       }
@@ -728,7 +730,7 @@ void attn_prefill_kernel(ChunkArgsAll) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           f32x4 v = {o[r][b][4 * i], o[r][b][4 * i + 1], o[r][b][4 * i + 2], o[r][b][4 * i + 3]};
-          if (kind > kFinite) {
+          if (kind > kClose) {
             const f32x4 old = ld4(to + 32 * b + 8 * i);
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = v[e] > 0.f ? beyond(old[e], kind) : old[e];
@@ -737,9 +739,9 @@ void attn_prefill_kernel(ChunkArgsAll) {
         }
       return;
     }
-    if (p.lse && half == 0 && kind <= kFinite)
+    if (p.lse && half == 0 && kind <= kClose)
       p.lse[orow] = ln == 0.f ? kNegInf : (m[r] + __builtin_amdgcn_logf(ln)) * kLn2;
-    if (p.row_ml && half == 0 && kind <= kFinite) row_factors(p.row_ml + 2 * orow, m[r], ln);
+    if (p.row_ml && half == 0 && kind <= kClose) row_factors(p.row_ml + 2 * orow, m[r], ln);
     const float f = ln == 0.f ? 0.f : again->g.v_scale / ln;
     uint16_t *to = p.a.out + orow * D + 8 * half;
 #pragma unroll
@@ -757,7 +759,7 @@ void attn_prefill_kernel(ChunkArgsAll) {
           w[2 + e] = both[1];
         }
         u32x4 *at = reinterpret_cast<u32x4 *>(to + 32 * b + 16 * i);
-        if (kind > kFinite) {
+        if (kind > kClose) {
           const u32x4 old = *at;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -773,7 +775,7 @@ void attn_prefill_kernel(ChunkArgsAll) {
 #pragma unroll 1
   for (int kind = kAsIs;;) {
     walk(kind);
-    if (kind == kAsIs) {
+    if (kind <= kFinite) {
       // a NaN may come from a value that the row does not see (0 * NaN)
       float bad = 0.f;
       if (wlive) {
@@ -791,14 +793,14 @@ void attn_prefill_kernel(ChunkArgsAll) {
       if (any && lane == 0) sbad[2] = 1;
       __syncthreads();
       if (uniform(sbad[2])) {
-        kind = kFinite;
+        ++kind;
         continue;
       }
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) store(kind, r);
     if (kind == kAsIs || kind == kDown) break;
-    ++kind;
+    kind = kind == kUp ? kDown : kUp;
   }
 }
 

@@ -1,0 +1,39 @@
+"""GPU: attention of chunks over values at the ends of their range, joined from many pieces, and of
+requests without new tokens."""
+import pytest
+import torch
+
+from tests.kv_helpers import make_cache, stored
+from tests.test_gpu_kv_prompt import check_chunk, chunk_call
+
+pytestmark = pytest.mark.gpu
+
+
+def set_rows(x, c, b, at, rows):
+    """rows [n, H, D] at the places `at` of request b."""
+    page = c.table[c.slots[b]][at // c.page].long()
+    bits = torch.uint8 if c.f8 else torch.int16
+    x[0].view(bits)[page, :, at % c.page] = stored(rows, c.f8).view(bits)
+
+
+@pytest.mark.parametrize("max_len", [None, 9000])
+@pytest.mark.parametrize("dim,n,new", [(64, 950, 3), (128, 700, 30), (256, 470, 5)])
+def test_sums_of_the_largest_values(dim, n, new, max_len):
+    """Visible places times the largest value just below the end of fp32, and scores that rise by
+    almost as much as the exponent's reference may stay behind: the mean is finite, and there."""
+    c = make_cache(dim, [n], None, 1, dim, 16, capacity=max_len)
+    block = 32 if dim == 256 else 64
+    at = torch.arange(n)
+    k = torch.zeros(n, 1, dim)
+    # a lane has half of a block's places: 16 e^2.75 or 32 e^2 are just below 256
+    k[:, 0, 0] = torch.where(at % (5 * block) < block, 0.0, 2.75 if dim == 256 else 2.0)
+    v = torch.full((n, 1, dim), 3.3e38 / n)
+    v[:, 0, 1::2] *= -1
+    v[:, 0, 2] = torch.randn(n, generator=c.g)
+    set_rows(c.k, c, 0, at, k)
+    set_rows(c.v, c, 0, at, v)
+    q = torch.zeros(new, 2, dim, dtype=torch.bfloat16)
+    q[:, :, 0] = 1.0
+    pool, _, out, lse, sc = chunk_call(c, [new], 2, late=2, q=q.cuda(), scale=1.0, max_len=max_len)
+    assert torch.isfinite(out.float()).all()
+    check_chunk(c, [new], q, sc, out, lse, 0, 2, pool.mass)
