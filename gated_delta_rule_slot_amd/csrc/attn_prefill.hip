@@ -841,7 +841,9 @@ __global__ __launch_bounds__(kThreads) void attn_prefill_join_kernel(KvGeom g, C
       for (int d = 32; d; d >>= 1) mm = fmaxf(mm, __shfl_xor(mm, d));
       const float f = pl == 0.f ? 0.f : fexp2(m - mm), old = top == kNegInf ? 0.f : fexp2(top - mm);
       l = fmaf(l, old, wave_sum(pl * f));
-      o *= old;
+      // (what has underflowed is left out, as in the walk: never 0 * inf)
+#pragma unroll
+      for (int c = 0; c < N; ++c) o[c] = old == 0.f ? 0.f : o[c] * old;
       top = mm;
       const float *src = p.o + (orow + base * stride) * D + lane * N;
       for (int k = 0; k < n; k += kPieces) {
@@ -855,7 +857,7 @@ __global__ __launch_bounds__(kThreads) void attn_prefill_join_kernel(KvGeom g, C
           const float fk = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), at));
           const float lk = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(pl), at));
 #pragma unroll
-          for (int c = 0; c < N; ++c) o[c] = lk == 0.f || k + u > 63 ? o[c] : fmaf(v[u][c], fk, o[c]);
+          for (int c = 0; c < N; ++c) o[c] = lk == 0.f || fk == 0.f || k + u > 63 ? o[c] : fmaf(v[u][c], fk, o[c]);
         }
       }
     }

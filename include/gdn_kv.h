@@ -333,8 +333,9 @@ gdn_status attn_prefill_workspace_bytes(gdn_kv_pool_t pool, int32_t batch, int32
  * gets out = 0 and lse = -inf and adds no weight.  Places that a token does not see never reach its
  * result, whatever their rows hold (a tile of 128 or 256 rows that meets NaN or infinite values is walked
  * four times, five if its sums leave fp32 on the way).  Infinite values and scores, and the range of the
- * values' sum, are as in attn_decode_paged, up to 3.3e38.  Weights are rounded to bf16 for the product with the
- * values.  The result does not depend on the order in which the workgroups run. */
+ * values' sum, are as in attn_decode_paged, up to 3.3e38, but a value that is not finite and whose weight is below
+ * 2^-100 of the largest acts as an infinite or NaN value does or is left out.  Weights are rounded to bf16 for the
+ * product with the values.  The result does not depend on the order in which the workgroups run. */
 gdn_status attn_prefill_paged(gdn_kv_pool_t pool, int32_t layer, int32_t batch, int32_t tokens,
                               int32_t q_heads, int32_t max_len, const int32_t *cu_seqlens,
                               const int32_t *slot_table, const int32_t *kv_len, const int32_t *kv_begin,

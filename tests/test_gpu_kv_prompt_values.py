@@ -37,3 +37,31 @@ def test_sums_of_the_largest_values(dim, n, new, max_len):
     pool, _, out, lse, sc = chunk_call(c, [new], 2, late=2, q=q.cuda(), scale=1.0, max_len=max_len)
     assert torch.isfinite(out.float()).all()
     check_chunk(c, [new], q, sc, out, lse, 0, 2, pool.mass)
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("n", [900, 5000, 27000])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("first", [True, False])
+def test_values_that_are_not_finite_and_have_no_weight(dim, n, first, value):
+    """A value that is not finite and whose weight is below 2^-100 of the largest makes its column so too or is
+    as if it were not there; never NaN from an infinite one.  Divided or not, and whichever piece comes first."""
+    new = 3
+    c, clean = (make_cache(dim, [n], None, 1, dim, 64) for _ in range(2))
+    at = torch.arange(n)
+    low = at < n // 2 if first else (at >= n // 2) & (at < n - new)
+    k = torch.zeros(n, 1, dim)
+    k[:, 0, 0] = torch.where(low, -200.0, 0.0)
+    for x in (c, clean):
+        set_rows(x.k, x, 0, at, k)
+    bad = at[low][17:18]
+    set_rows(c.v, c, 0, bad, torch.full((1, 1, dim), value))
+    q = torch.randn(new, 2, dim, generator=c.g).to(torch.bfloat16)
+    q[:, :, 0] = 1.0
+    pool, _, out, lse, sc = chunk_call(c, [new], 2, late=2, q=q.cuda(), scale=1.0)
+    _, _, want, wl, _ = chunk_call(clean, [new], 2, q=q.cuda(), scale=1.0)
+    check_chunk(clean, [new], q, sc, want, wl)
+    assert torch.equal(lse, wl) and torch.isfinite(pool.mass).all()
+    o, w = out.float(), want.float()
+    shown = torch.isnan(o) if value != value else o == value
+    assert (shown | ((o - w).abs() <= 4 * 2.0 ** -8 * (w.abs() + 4))).all()
