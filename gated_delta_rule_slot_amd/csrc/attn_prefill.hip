@@ -196,9 +196,10 @@ __device__ __forceinline__ Chunk chunk_of(const KvGeom &g, const ChunkDev &p, in
   const bool lens = r.len >= r.n && r.len <= p.a.max_len && r.begin >= 0;
   r.live = r.any && r.slot > 0 && r.slot < g.slots && lens;
   if (tell) {
+    const bool told = r.any || r.n == 0;  // (a request without rows has a tile too)
     if (!ok) set_err(g.err, GDN_ERRW_BAD_SEQLENS);
-    else if (r.any && r.slot >= g.slots) set_err(g.err, GDN_ERRW_BAD_SLOT);
-    else if (r.any && r.slot > 0 && !lens) set_err(g.err, GDN_ERRW_BAD_SEQLENS);
+    else if (told && r.slot >= g.slots) set_err(g.err, GDN_ERRW_BAD_SLOT);
+    else if (told && r.slot > 0 && !lens) set_err(g.err, GDN_ERRW_BAD_SEQLENS);
   }
   return r;
 }

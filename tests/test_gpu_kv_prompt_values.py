@@ -65,3 +65,24 @@ def test_values_that_are_not_finite_and_have_no_weight(dim, n, first, value):
     o, w = out.float(), want.float()
     shown = torch.isnan(o) if value != value else o == value
     assert (shown | ((o - w).abs() <= 4 * 2.0 ** -8 * (w.abs() + 4))).all()
+
+
+@pytest.mark.parametrize("where", [0, 2, 4])
+def test_requests_without_new_tokens_are_checked_too(where):
+    """Bad slots, lengths and begins of a request that has no rows set their bit; the others' rows are there."""
+    import gated_delta_rule_slot_amd as gdn
+
+    new = [9, 20, 30, 5, 6]
+    new[where] = 0
+    lens, slots = [50, 60, 70, 80, 90], [1, 4, 3, 2, 5]
+    for change, bit in ((dict(), 0), (dict(slots=0), 0), (dict(slots=-3), 0), (dict(slots=6), gdn.ERRW_BAD_SLOT),
+                        (dict(lens=-1), gdn.ERRW_BAD_SEQLENS), (dict(lens=97), gdn.ERRW_BAD_SEQLENS),
+                        (dict(begins=-1), gdn.ERRW_BAD_SEQLENS), (dict(lens=0), 0),
+                        (dict(slots=0, lens=-1), 0)):
+        c = make_cache(3, lens, None, 2, 128, 16, slots=slots, capacity=96)
+        for name, x in change.items():
+            getattr(c, name)[where] = x
+        pool, q, out, lse, sc = chunk_call(c, new, 4, late=3, max_len=96)
+        assert int(pool.err_word.item()) == bit, change
+        c.slots[where] = 0
+        check_chunk(c, new, q, sc, out, lse, 0, 3, pool.mass)
