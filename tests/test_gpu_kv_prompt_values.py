@@ -67,6 +67,32 @@ def test_values_that_are_not_finite_and_have_no_weight(dim, n, first, value):
     assert (shown | ((o - w).abs() <= 4 * 2.0 ** -8 * (w.abs() + 4))).all()
 
 
+@pytest.mark.parametrize("f8", [False, True])
+@pytest.mark.parametrize("dim,new,group", [(64, 1, 1), (64, 4, 2), (128, 2, 3), (256, 3, 1)])
+def test_join_of_hundreds_of_pieces(dim, new, group, f8):
+    """One request over so many places that the pieces of a tile take several rounds of a wave's lanes:
+    maxima that rise over the pieces, that fall, and first pieces that see nothing."""
+    import gated_delta_rule_slot_amd as gdn
+
+    n = 27000
+    for kind in ("rises", "falls", "late"):
+        c = make_cache(dim, [n], None, 1, dim, 64, f8)
+        at = torch.arange(n)
+        ramp = 12.0 * at / n if kind == "rises" else 12.0 * (1 - at / n)
+        if kind != "late":
+            k = 0.3 * torch.randn(n, 1, dim, generator=c.g)
+            k[:, 0, 0] = ramp
+            set_rows(c.k, c, 0, at, k)
+        else:
+            c.table[c.slots[0], :21000 // 64] = 0
+        q = torch.randn(new, group, dim, generator=c.g).to(torch.bfloat16)
+        q[:, :, 0] = 2.0
+        pool, _, out, lse, sc = chunk_call(c, [new], group, late=2, q=q.cuda(), scale=0.8 if kind != "late" else 0.1)
+        assert gdn.attn_prefill_workspace_bytes(pool, 1, new, group, n) >= 65 * new * group * (dim + 2) * 4
+        check_chunk(c, [new], q, sc, out, lse, 0, 2, pool.mass)
+        assert int(pool.err_word.item()) == (gdn.ERRW_BAD_PAGE if kind == "late" else 0)
+
+
 @pytest.mark.parametrize("where", [0, 2, 4])
 def test_requests_without_new_tokens_are_checked_too(where):
     """Bad slots, lengths and begins of a request that has no rows set their bit; the others' rows are there."""
@@ -86,3 +112,15 @@ def test_requests_without_new_tokens_are_checked_too(where):
         assert int(pool.err_word.item()) == bit, change
         c.slots[where] = 0
         check_chunk(c, new, q, sc, out, lse, 0, 3, pool.mass)
+
+
+def test_attention_leaves_the_table_and_the_cache_alone():
+    """Bad pages, slots and lengths among the requests: table, keys and values as they were."""
+    c = make_cache(21, [50, 60, 70, 80], None, 2, 128, 16, slots=[1, 0, 3, 2])
+    c.table[3, 2], c.table[2, 1] = 0, c.k.shape[1]
+    c.lens[0] = 200
+    table = c.table.clone()
+    pool, q, out, lse, sc = chunk_call(c, [10, 11, 12, 13], 4, late=5, max_len=80)
+    assert torch.equal(pool.page_table.cpu(), table) and int(pool.err_word.item()) != 0
+    assert torch.equal(pool.k.cpu().view(torch.int16), c.k.view(torch.int16))
+    assert torch.equal(pool.v.cpu().view(torch.int16), c.v.view(torch.int16))
