@@ -37,13 +37,13 @@
 //
 // The weights are rounded to bf16 once for the product (their sum l is not): an error of at most 2^-8
 // of a weighted mean of |v|, about as large as the output's own rounding.  Two bf16 parts would take
-// half as many matrix instructions again.
+// half as many matrix instructions again, which prompts would pay for in full.  Calls of a few rows a request are
+// bound by reading and would not: they share the one form (attn_decode_paged, for single tokens, has two parts).
 //
-// Measured on MI355X (a matrix product of 8192^3 runs at 1338 TFLOP/s there): one prompt of 24576
-// tokens 1120-1175 TFLOP/s with heads of 256, 1075-1120 of 128, 1030-1060 of 64, from an e4m3 cache
-// 1065-1100, 1045-1080 and 1005-1030; 512 tokens behind 131072 1.00-1.04 ms, 1060-1100 TFLOP/s; 6144 tokens
-// 320-340 us, 910-960 (the last tiles run alone); 32 requests of 1 to 7 tokens over 500 to 8192: 75 us,
-// 3.7 TB/s.
+// Measured on MI355X (a matrix product of 8192^3 runs at 1325 TFLOP/s there): one prompt of 24576
+// tokens 1105 TFLOP/s with heads of 256, 1059 of 128, 1007 of 64, from an e4m3 cache 1051, 1025 and 993; 512
+// tokens behind 131072 1.04 ms, 1060 TFLOP/s; 6144 tokens 327 us, 947 (the last tiles run alone); 32 requests of
+// 1 to 7 tokens over 500 to 8192: 76 us, 3.7 TB/s.  On other cards up to 7 % faster (305 us, 0.99 ms).
 #include <algorithm>
 #include <cmath>
 
@@ -123,9 +123,9 @@ __device__ __forceinline__ f32x16 mfma32(const bf16x8 &a, const bf16x8 &b, const
 // place's NaN or infinite values.  Where a workgroup's result is not finite, its tile is walked
 // again with every such value as 0, which gives the finite part of the sums, then with 1 in the
 // place of inf and NaN and 0 elsewhere, then with 1 in the place of -inf and NaN: a sum above 0
-// says that the row sees one with a weight above 0.  Where the finite sums are not finite either, they may have
-// outgrown fp32, as weights are up to 2^4 and more where the reference stayed behind: the second walk is done again with
-// the reference following every block, so that no weight is above 1.
+// says that the row sees one with a weight above 0.  Where the second walk's sums are not finite either, they may
+// have outgrown fp32, as weights reach 2^4 and more where the reference stayed behind: it is done again with the
+// reference following every block, so that no weight is above 1.
 enum { kAsIs, kFinite, kClose, kUp, kDown };
 __device__ __forceinline__ u32x4 sorted(u32x4 x, int kind) {
 #pragma unroll
@@ -883,9 +883,9 @@ __global__ __launch_bounds__(kThreads) void attn_prefill_join_kernel(KvGeom g, C
 // l, its score and exponent worked out as for l, bit for bit (against the logarithm lse a large score would lose
 // |lse| 2^-23, and one whose columns are summed in another order as much).
 //
-// (512 queries over 131584 places, 16 heads of 256: 0.73 ms; reading the rows by each wave for
-// itself 2.25 ms, bound by its scattered reads.  64 places a wave instead of 32: 83 against 65 us for
-// two 4099-token prompts, as there are too few waves.)
+// (512 queries over 131584 places, 16 heads of 256: 0.70 ms; two 4099-token prompts 57 us.  Reading the rows
+// by each wave for itself: 2.25 ms for the former, bound by its scattered reads; 64 places a wave instead of 32:
+// 83 against 65 us for the latter when that was tried, as there are too few waves.)
 constexpr int kMassRows = 64, kMassPlaces = 32;
 
 template <int D, bool kF8>
@@ -965,7 +965,8 @@ void attn_prefill_mass_kernel(KvGeom g, ChunkDev p, int blocks) {
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       const int row = min(r + 32 * nb + c, all - 1), token = token_of(p, row);
-      ml[nb] = *reinterpret_cast<const f32x2_t *>(p.row_ml + 2 * (int64_t(bos + token) * p.a.q_heads + h * G + (row - token * G)));
+      const int64_t orow = int64_t(bos + token) * p.a.q_heads + h * G + (row - token * G);
+      ml[nb] = *reinterpret_cast<const f32x2_t *>(p.row_ml + 2 * orow);
     }
   };
   f32x16 sum[KB];
@@ -1007,7 +1008,8 @@ void attn_prefill_mass_kernel(KvGeom g, ChunkDev p, int blocks) {
     for (int i = 0; i < KS * NB; ++i) {
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int kb = 0; kb < KB; ++kb) s[kb][i % NB] = mfma32(k[kb][step_at<D>(i / NB)], ring[i % kAhead], s[kb][i % NB]);
+      for (int kb = 0; kb < KB; ++kb)
+        s[kb][i % NB] = mfma32(k[kb][step_at<D>(i / NB)], ring[i % kAhead], s[kb][i % NB]);
       if (i + kAhead < KS * NB) ring[i % kAhead] = qread(i + kAhead);
     }
     __builtin_amdgcn_sched_barrier(0);

@@ -44,8 +44,8 @@ __device__ __forceinline__ uint64_t block_scan(uint32_t v, uint32_t *wave, uint6
 // each of which makes the sums for itself, and a second launch of one workgroup writes the
 // counts behind them.
 //
-// Measured: 128 requests of one token 4.8 us on the device, latency (lengths, then the list, two sums
-// over the waves); 64 requests of up to 1500 tokens, 48 000 in all, 4.9 + 2.5 us.
+// Measured: 128 requests of one token 4.7 us on the device, latency (lengths, then the list, two sums
+// over the waves); 64 requests of up to 1500 tokens, 48 000 in all, 5.1 + 2.6 us.
 constexpr int kTokensPer = 4;
 
 template <int THREADS>

@@ -11,8 +11,8 @@
 // fp32: its error is 2^-24 of a turn at most however far the position (fp32 would be wrong by
 // whole radians at position 10^7).  Everything else is fp32, and each output is rounded once.
 //
-// Measured: 6144 tokens of 32 + 2 * 8 heads of 128 into e4m3, 139 MB, 31-34 us (29 at a copy's rate);
-// 128 tokens of 16 + 2 * 2 heads of 256 4.7 us, latency.
+// Measured: 6144 tokens of 32 + 2 * 8 heads of 128 into e4m3, 139 MB, 34-36 us (29 at a copy's rate);
+// 128 tokens of 16 + 2 * 2 heads of 256 4.5 us, latency.
 #include <algorithm>
 #include <cmath>
 
@@ -130,8 +130,8 @@ hipError_t launch_d(const gdn_kv_pool *p, int layer, const RopeArgs &a, hipStrea
   constexpr int ROWS = 64 / (D / 16);
   const int turns = (a.q_heads + 2 * g.kv_heads + ROWS - 1) / ROWS;  // of one wave over a token's rows
   // Few tokens: a wave for every turn, up to the waves that run at once.  128 tokens of 16 + 2 * 2 heads of
-  // 256 3.8 us (one wave a token: 6.0), 512 5.4 (5.9), 2048 10.2 (10.2; all turns: 12.3); of 32 + 2 * 8 heads
-  // of 128 into e4m3, 2048 tokens 11.4 (12.5; 16.3).
+  // 256 4.4 us (one wave a token: 6.6), 512 6.1 (6.7), 2048 10.8 (11.0; all turns: 13.0); of 32 + 2 * 8 heads
+  // of 128 into e4m3, 2048 tokens 12.1 (12.9; 17.0).
   const int split = int(std::max<int64_t>(1, std::min<int64_t>(turns, 4096 / a.n)));
   const int64_t units = int64_t(a.n) * split;
   const bool f8 = p->d.kv_dtype == GDN_F8_E4M3, adjacent = a.layout == GDN_ROPE_INTERLEAVED;

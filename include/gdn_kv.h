@@ -211,11 +211,12 @@ enum { GDN_ERRW_NO_PAGES = 32 };
  * new_len     device int32 [batch] or NULL (= 1 each)
  * next_pos    device int32 [batch] or NULL (= kv_len): position of the first new token
  * free_pages  device int32 [free_capacity]: the first n_free[0] entries are free pages
- * n_free      device int32 [1];  n_free_out: device int32 [1], may be n_free
+ * n_free      device int32 [1] (outside [0, free_capacity]: GDN_ERRW_BAD_SEQLENS, and the nearer end is
+ *             taken);  n_free_out: device int32 [1], may be n_free
  * The running sums of max(new_len, 0), limited to max_tokens, go to cu_seqlens [batch + 1].
  * A request is served if its slot is live (slots must be distinct), its kv_len and new_len are not
  * negative, kv_len + new_len is at most max_pages * page_size, its tokens end within max_tokens, its
- * positions below 2^31 (else GDN_ERRW_BAD_SEQLENS), and the pages that it and all such requests
+ * positions and the next one are below 2^31 (else GDN_ERRW_BAD_SEQLENS), and the pages that it and all such requests
  * before it lack are at most n_free, or it lacks none (else GDN_ERRW_NO_PAGES).  What it lacks,
  * entries ceil(kv_len / page_size) ... of its row of the pool's page table (which is written,
  * const as the descriptor's pointer is), comes from the end of the free list, in the order of
@@ -243,8 +244,9 @@ gdn_status kv_batch_map(gdn_kv_pool_t pool, int32_t batch, int32_t max_tokens, c
  * Slots must be distinct and no page be in two rows.  An entry that is no page sets
  * GDN_ERRW_BAD_PAGE and is left out; so does a page that the list (free_capacity) has no room
  * for, which stays in the table.  A negative number or kv_len past max_pages * page_size sets
- * GDN_ERRW_BAD_SEQLENS and skips the request.  n_free_out may be n_free; nothing else that the
- * call writes (free_pages, page table, n_free_out) may overlap what it reads. */
+ * GDN_ERRW_BAD_SEQLENS and skips the request; n_free is as in kv_batch_map.  n_free_out may be
+ * n_free; nothing else that the call writes (free_pages, page table, n_free_out) may overlap what it
+ * reads. */
 gdn_status kv_release(gdn_kv_pool_t pool, int32_t batch, const int32_t *slot_table, const int32_t *kv_len,
                       const int32_t *keep, int32_t free_capacity, int32_t *free_pages,
                       const int32_t *n_free, int32_t *n_free_out, void *stream);
@@ -306,9 +308,11 @@ gdn_status attn_prefill_workspace_bytes(gdn_kv_pool_t pool, int32_t batch, int32
  * and values are stored before).  Request b's new tokens are cu_seqlens[b] .. cu_seqlens[b + 1] - 1
  * of q; with n of them, token i stands at place t = kv_len[b] - n + i and sees the places
  *   max(kv_begin[b], t - window + 1) .. t      (from kv_begin[b] on if window is 0)
- * Formulas, head groups and slots as in attn_decode_paged; one token per request is the same as there.
+ * Formulas, head groups and slots as in attn_decode_paged, and so are the results of one token per request, up to
+ * the rounding of the weights (below).
  * tokens      rows of q and out; cu_seqlens[batch] may be less, and the rows behind it are left as
- *             they are
+ *             they are.  With 0 nothing is done and no request looked at (otherwise those without new
+ *             tokens set their error bits too)
  * q_heads     as in attn_decode_paged
  * max_len     host int: no request has more tokens with the new ones (one that has, or fewer than new
  *             ones, or a negative begin, sets GDN_ERRW_BAD_SEQLENS and is skipped).  It decides how
@@ -319,7 +323,8 @@ gdn_status attn_prefill_workspace_bytes(gdn_kv_pool_t pool, int32_t batch, int32
  * q           device bf16, token i at q + i * q_stride (elements, a multiple of 8, at least q_heads *
  *             head_dim; 16-byte aligned), [q_heads][head_dim] there
  * window      >= 0; 0: none.  It and kv_begin count places: see attn_decode_paged for slots that were
- *             cut
+ *             cut.  The table's entries in front of the first place that a request's new tokens see are
+ *             not looked at
  * mass_tokens >= 0: the last that many new tokens of each request add their weights to the pool's
  *             mass (which it must have; live slots must be distinct then), so that an eviction right
  *             after a prompt has something to go by; 0: none do.  Only visible places' entries change

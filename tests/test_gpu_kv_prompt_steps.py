@@ -124,7 +124,8 @@ class Server:
         return given
 
 
-@pytest.mark.parametrize("f8,dim,rot,adjacent", [(False, 128, 128, False), (True, 64, 32, True), (False, 256, 64, False)])
+@pytest.mark.parametrize("f8,dim,rot,adjacent", [(False, 128, 128, False), (True, 64, 32, True),
+                                                 (False, 256, 64, False)])
 def test_steps_after_a_cut_and_after_a_release(f8, dim, rot, adjacent):
     s = Server(f8, dim, rot, adjacent)
     s.step([40, 17, 1], "prompts")
